@@ -558,6 +558,99 @@ SNACK_API snack_status snack_conv1x1(const snack_plan* plan, const void* vals, s
                                      void* stream);
 
 /*
+ * Low-rank adapters of many requests beside one shared projection.  Adapter
+ * l < L adds s_l B_l^T A_l to the layer's weight for the tokens that carry
+ * its index.  Both factors are stored by rank: A is L x R x K, B is
+ * L x R x M (B_l^T is the M x r factor), elements of the activations' type,
+ * so that every product walks rows of contiguous features.
+ *   scale  L floats on the device, NULL: all 1
+ *   rank   L int32 on the device, NULL: all R.  The rank r of an adapter is
+ *          its entry clamped to [0, R]; rows at and past r are never used
+ *          (they may hold anything).
+ * ids: int32 [T] on the device, the adapter of each token; negative: none
+ * (its row gets base alone).  An id >= L reads nothing: its output row is
+ * NaN and it takes no part in the gradients.
+ * Activations are batch-major with a row stride in elements (ldx >= K and so
+ * on); any alignment.  L <= 8192, R <= 256.
+ *
+ * snack_lora_fwd: with a = ids[i],
+ *     t[i, j] = sum_k A[a, j, k] X[i, k]                 (fp32; 0 for j >= r)
+ *     Y[i, m] = base[i, m] + s_a sum_j t[i, j] B[a, j, m]
+ * one rounding to the output type.  base (nullable: zeros) is the shared
+ * projection's output and may be Y itself (same stride).  t (nullable,
+ * T x R floats, contiguous) receives t for snack_lora_bwd.  X and Y must not
+ * overlap.
+ *
+ * snack_lora_bwd: with u[i, j] = sum_m B[a, j, m] dY[i, m],
+ *     dX[i, k] = base[i, k] + s_a sum_j u[i, j] A[a, j, k]
+ *     dA[l, j, k] = s_l sum_{i : ids[i] = l} u[i, j] X[i, k]
+ *     dB[l, j, m] = s_l sum_{i : ids[i] = l} t[i, j] dY[i, m]
+ * base (nullable) is the shared projection's input gradient and may be dX
+ * itself.  Any of dX, dA, dB may be NULL (not wanted).  t (nullable) is what
+ * the forward stored; without it t is computed again.  dA and dB (L x R x K,
+ * L x R x M) are overwritten, with zeros where an adapter has no token or
+ * for ranks it does not have.  dX must not overlap X or dY.
+ *
+ * snack_lora_workspace: bytes of ws for T tokens (backward 0 or 1).
+ * Both calls are asynchronous, allocate nothing, use no atomics and give the
+ * same bits for the same inputs.  Errors: SNACK_E_NULL, SNACK_E_DTYPE,
+ * SNACK_E_SHAPE (sizes, strides, overlap), SNACK_E_WORKSPACE.
+ */
+typedef struct snack_lora {
+  int32_t M, K, L, R;
+  const void* A;
+  const void* B;
+  const float* scale;
+  const int32_t* rank;
+} snack_lora;
+
+SNACK_API snack_status snack_lora_workspace(const snack_lora* lora, snack_dtype dtype, int32_t T,
+                                            int32_t backward, size_t* bytes);
+SNACK_API snack_status snack_lora_fwd(const snack_lora* lora, snack_dtype dtype,
+                                      const int32_t* ids, int32_t T, const void* X, int64_t ldx,
+                                      const void* base, int64_t ldb, void* Y, int64_t ldy,
+                                      float* t, void* ws, size_t ws_bytes, void* stream);
+SNACK_API snack_status snack_lora_bwd(const snack_lora* lora, snack_dtype dtype,
+                                      const int32_t* ids, const float* t, int32_t T,
+                                      const void* X, int64_t ldx, const void* dY, int64_t lddy,
+                                      const void* base, int64_t ldb, void* dX, int64_t lddx,
+                                      void* dA, void* dB, void* ws, size_t ws_bytes,
+                                      void* stream);
+
+/*
+ * The 2-norm over many gradients, and clipping by it.
+ *     norm = sqrt(sum over all tensors and elements of g^2)
+ *     out  = round(g * min(1, max_norm / (norm + eps)))
+ * `grads` is a host array of `count` entries, read before the call returns;
+ * each tensor is n contiguous elements of its own dtype (any alignment, n may
+ * be 0).  out NULL or equal to grad: in place; otherwise out must not overlap
+ * any grad of the list.  Sums, norm and factor are held in 64 bits, so no
+ * square overflows (a norm past the range of float is stored as infinity, and
+ * the factor is still right).
+ * NaN and infinities go by the formula: a NaN norm makes every output NaN, an
+ * infinite one gives factor 0 (NaN where the gradient is infinite).
+ * norm: device float (nullable in snack_grad_clip).  ws: device memory of
+ * snack_grad_workspace(count) bytes.  Asynchronous; same bits for the same
+ * inputs.  Errors: SNACK_E_NULL, SNACK_E_DTYPE, SNACK_E_SHAPE (n < 0,
+ * max_norm < 0, eps < 0), SNACK_E_COUNT (count < 0), SNACK_E_OVERFLOW
+ * (n > 2^40), SNACK_E_NAN (max_norm or eps NaN), SNACK_E_WORKSPACE.
+ */
+typedef struct snack_grad {
+  const void* grad;
+  void* out;
+  int64_t n;
+  int32_t dtype;
+  int32_t reserved;
+} snack_grad;
+
+SNACK_API snack_status snack_grad_workspace(int32_t count, size_t* bytes);
+SNACK_API snack_status snack_grad_norm(const snack_grad* grads, int32_t count, float* norm,
+                                       void* ws, size_t ws_bytes, void* stream);
+SNACK_API snack_status snack_grad_clip(const snack_grad* grads, int32_t count, float max_norm,
+                                       float eps, float* norm, void* ws, size_t ws_bytes,
+                                       void* stream);
+
+/*
  * GELU with the exact error function, h = z * Phi(z), and its backward
  * dz = dh * (Phi(z) + z * phi(z)), elementwise over n fp32 values (the
  * nonlinearity between the two sparse layers of a GPT-2-shaped MLP block).

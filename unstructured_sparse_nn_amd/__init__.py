@@ -17,5 +17,9 @@ from .binding import (ACT_GELU, ACT_NONE, ACT_RELU, BATCH_MAJOR, BF16, CONV_NCHW
                       snack_spmm_bwd_fused, snack_spmm_bwd_fused_adam, snack_spmm_bwd_input,
                       snack_spmm_fwd,
                       snack_spmm_fwd_act, snack_version, snack_calibrate,
+                      snack_lora, snack_lora_workspace, snack_lora_fwd, snack_lora_bwd,
+                      snack_grad_table, snack_grad_workspace, snack_grad_norm, snack_grad_clip,
                       status_str)
+from .adapters import LoraAdapters, lora_bwd, lora_fwd  # noqa: F401
+from .clip import clip_grad_norm_, clip_grads, grad_norm  # noqa: F401
 from .layer import SparseLinear, Topology  # noqa: F401

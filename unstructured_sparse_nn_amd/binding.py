@@ -63,6 +63,13 @@ class SnackAdam(ctypes.Structure):
                 ("eps", ctypes.c_float), ("step", ctypes.c_int32)]
 
 
+class SnackLora(ctypes.Structure):
+    """Mirror of ``struct snack_lora``."""
+    _fields_ = [("M", ctypes.c_int32), ("K", ctypes.c_int32), ("L", ctypes.c_int32),
+                ("R", ctypes.c_int32), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("rank", ctypes.c_void_p)]
+
+
 class SnackPlan(ctypes.Structure):
     """Mirror of ``struct snack_plan``."""
     _fields_ = [("M", ctypes.c_int32), ("K", ctypes.c_int32), ("nnz", ctypes.c_int64),
@@ -123,6 +130,13 @@ def _load():
         "snack_fixed_code": ([P, ctypes.POINTER(sz)], P),
         "snack_fixed_free": ([P], None),
         "snack_conv1x1": ([plan_p, P, i32, P, i32, i32, i32, P, P], i32),
+        "snack_lora_workspace": ([P, i32, i32, i32, ctypes.POINTER(sz)], i32),
+        "snack_lora_fwd": ([P, i32, P, i32, P, i64, P, i64, P, i64, P, P, sz, P], i32),
+        "snack_lora_bwd": ([P, i32, P, P, i32, P, i64, P, i64, P, i64, P, i64, P, P, P, sz, P],
+                           i32),
+        "snack_grad_workspace": ([i32, ctypes.POINTER(sz)], i32),
+        "snack_grad_norm": ([P, i32, P, P, sz, P], i32),
+        "snack_grad_clip": ([P, i32, ctypes.c_float, ctypes.c_float, P, P, sz, P], i32),
         "snack_gelu_fwd": ([P, P, i64, P], i32),
         "snack_gelu_bwd": ([P, P, P, i64, P], i32),
         "snack_dense_fwd": ([P, P, i32, i32, i32, P, i32, P, P], i32),
@@ -411,6 +425,72 @@ def snack_conv1x1(plan, vals, X, N: int, HW: int, layout: int, Y, stream=None, d
     dt = _dtype(vals, X, Y, dtype=dtype)
     _check(_lib.snack_conv1x1(ctypes.byref(plan), _ptr(vals), dt, _ptr(X), N, HW, layout,
                               _ptr(Y), _stream(stream)), "snack_conv1x1")
+
+
+def snack_lora(A, B, M: int, K: int, L: int, R: int, scale=None, rank=None) -> SnackLora:
+    """The adapters' struct: A (L x R x K), B (L x R x M), scale (L floats) and
+    rank (L int32) are device arrays, the last two optional."""
+    return SnackLora(M, K, L, R, _ptr(A), _ptr(B), _ptr(scale), _ptr(rank))
+
+
+def snack_lora_workspace(lora: SnackLora, dtype: int, T: int, backward: bool = False) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.snack_lora_workspace(ctypes.byref(lora), dtype, T, int(backward),
+                                     ctypes.byref(out)), "snack_lora_workspace")
+    return out.value
+
+
+def snack_lora_fwd(lora: SnackLora, ids, T: int, X, ldx: int, base, ldb: int, Y, ldy: int, t=None,
+                   ws=None, stream=None, ws_bytes=None, dtype=None):
+    """Y = base + s_a (X A_a^T) B_a, a = ids[token]."""
+    dt = _dtype(X, Y, dtype=dtype)
+    _check(_lib.snack_lora_fwd(ctypes.byref(lora), dt, _ptr(ids), T, _ptr(X), ldx, _ptr(base), ldb,
+                               _ptr(Y), ldy, _ptr(t), _ptr(ws), _nbytes(ws, ws_bytes),
+                               _stream(stream)), "snack_lora_fwd")
+
+
+def snack_lora_bwd(lora: SnackLora, ids, t, T: int, X, ldx: int, dY, lddy: int, base, ldb: int,
+                   dX, lddx: int, dA=None, dB=None, ws=None, stream=None, ws_bytes=None,
+                   dtype=None):
+    """dX = base + s_a (dY B_a^T) A_a, dA and dB (each may be None)."""
+    dt = _dtype(X, dY, dtype=dtype)
+    _check(_lib.snack_lora_bwd(ctypes.byref(lora), dt, _ptr(ids), _ptr(t), T, _ptr(X), ldx,
+                               _ptr(dY), lddy, _ptr(base), ldb, _ptr(dX), lddx, _ptr(dA), _ptr(dB),
+                               _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream)),
+           "snack_lora_bwd")
+
+
+def snack_grad_table(grads, outs=None):
+    """The host array of ``struct snack_grad`` for tensors (outs: where the
+    scaled ones go, default in place), as an ``array('q')``."""
+    import torch
+    from array import array
+    codes = {torch.float32: F32, torch.bfloat16: BF16}
+    rows = array("q")
+    try:
+        for g, o in zip(grads, grads if outs is None else outs):
+            rows.extend((g.data_ptr(), o.data_ptr(), g.numel(), codes[g.dtype]))
+    except KeyError as e:
+        raise TypeError(f"unsupported dtype {e.args[0]}") from None
+    return rows
+
+
+def snack_grad_workspace(count: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.snack_grad_workspace(count, ctypes.byref(out)), "snack_grad_workspace")
+    return out.value
+
+
+def snack_grad_norm(table, count: int, norm, ws, stream=None, ws_bytes=None):
+    _check(_lib.snack_grad_norm(table.buffer_info()[0], count, _ptr(norm), _ptr(ws),
+                                _nbytes(ws, ws_bytes), _stream(stream)), "snack_grad_norm")
+
+
+def snack_grad_clip(table, count: int, max_norm: float, eps: float, norm, ws, stream=None,
+                    ws_bytes=None):
+    _check(_lib.snack_grad_clip(table.buffer_info()[0], count, max_norm, eps, _ptr(norm),
+                                _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream)),
+           "snack_grad_clip")
 
 
 def snack_gelu_fwd(z, h, n=None, stream=None):

@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libsnack.so")
 # longest compiles first (they start first in the worker pool)
 SOURCES = ["wave_spmm_bf16.hip", "wave_spmm_f32.hip", "wave_fused.hip", "wave_sddmm_bf16.hip",
            "wave_sddmm_f32.hip", "spmm.hip", "prune_bitmap.hip", "api.hip", "prims.hip",
-           "prepare.hip", "prune.hip", "aux.hip", "fixed.hip", "wave.hip", "noalloc.hip", "calib.hip"]
+           "prepare.hip", "prune.hip", "lora.hip", "aux.hip", "fixed.hip", "wave.hip", "gradclip.hip",
+           "noalloc.hip", "calib.hip"]
 ARCH = "gfx950"  # the MI355X (CDNA4); no other target is built
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -80,8 +81,8 @@ def build(verbose: bool = False) -> str:
 
 # Sources whose host code is more than kernel launches: argument checks and
 # plan layout, the fixed-pattern code generator, the static workspace, the
-# calibration entry point.
-HOST_HEAVY = ["api.hip", "fixed.hip", "noalloc.hip", "calib.hip"]
+# calibration entry point, the checks and layouts of the adapters and of clipping.
+HOST_HEAVY = ["api.hip", "fixed.hip", "noalloc.hip", "calib.hip", "lora.hip", "gradclip.hip"]
 
 
 def build_host_sanitized(out_dir: str) -> str:
