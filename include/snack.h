@@ -571,7 +571,7 @@ SNACK_API snack_status snack_conv1x1(const snack_plan* plan, const void* vals, s
  * (its row gets base alone).  An id >= L reads nothing: its output row is
  * NaN and it takes no part in the gradients.
  * Activations are batch-major with a row stride in elements (ldx >= K and so
- * on); any alignment.  L <= 8192, R <= 256.
+ * on); any alignment.  L <= 8192, R <= 256, M and K <= 2^23.
  *
  * snack_lora_fwd: with a = ids[i],
  *     t[i, j] = sum_k A[a, j, k] X[i, k]                 (fp32; 0 for j >= r)
@@ -594,7 +594,8 @@ SNACK_API snack_status snack_conv1x1(const snack_plan* plan, const void* vals, s
  * snack_lora_workspace: bytes of ws for T tokens (backward 0 or 1).
  * Both calls are asynchronous, allocate nothing, use no atomics and give the
  * same bits for the same inputs.  Errors: SNACK_E_NULL, SNACK_E_DTYPE,
- * SNACK_E_SHAPE (sizes, strides, overlap), SNACK_E_WORKSPACE.
+ * SNACK_E_SHAPE (sizes, strides, overlap), SNACK_E_OVERFLOW (M or K > 2^23,
+ * T within 64 of 2^31), SNACK_E_WORKSPACE.
  */
 typedef struct snack_lora {
   int32_t M, K, L, R;
