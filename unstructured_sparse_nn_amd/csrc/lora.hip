@@ -11,9 +11,12 @@
 //
 // A few tokens take k_lora_few, a workgroup's worth of dot products each.
 // More tokens are brought into the order of their adapters (k_lora_route) and
-// cut into tiles of TILE tokens of one adapter, which feed the matrix cores.
+// cut into tiles of TILE tokens of one adapter, which feed the matrix cores:
+// reduce and expand of a tile in one kernel (k_lora_apply), the gradients in a
+// second one (k_lora_grad) that reads x and dy once more.
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "common.h"
 #include "internal.h"
@@ -24,7 +27,7 @@ namespace {
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 
-constexpr int32_t TILE = 64;  // tokens of a tile
+constexpr int32_t TILE = 32;  // tokens of a tile
 constexpr int32_t MAX_RANK = 256;
 constexpr int32_t MAX_ADAPTERS = 8192;
 constexpr int32_t MAX_FEATURES = 1 << 23;  // column blocks are a grid's y
@@ -46,7 +49,12 @@ __device__ __forceinline__ float scale_of(const lora_dev& d, int32_t l) {
 // Rows start at any element, so pieces are loaded and stored without an
 // alignment claim; the hardware takes a 16-byte access at any address.
 template <typename T> constexpr int EL = 16 / sizeof(T);
-template <typename T> struct __attribute__((aligned(16))) frag { T v[EL<T>]; };
+template <typename T> struct __attribute__((aligned(16))) frag { uint32_t w[4]; };
+
+__device__ __forceinline__ float at(const frag<bf16>& f, int e) {
+  return __uint_as_float(e & 1 ? f.w[e / 2] & 0xFFFF0000u : f.w[e / 2] << 16);
+}
+__device__ __forceinline__ float at(const frag<float>& f, int e) { return __uint_as_float(f.w[e]); }
 
 template <typename T>
 __device__ __forceinline__ frag<T> load_frag(const T* p) {
@@ -59,18 +67,44 @@ template <typename T>
 __device__ __forceinline__ frag<T> load_frag(const T* p, int32_t n) {
   if (n >= EL<T>) return load_frag(p);
   frag<T> f{};
-  for (int e = 0; e < EL<T> - 1; ++e)
-    if (e < n) f.v[e] = p[e];
+  if (n > 0) {
+    uint32_t v[EL<T> - 1];
+#pragma unroll
+    for (int e = 0; e < EL<T> - 1; ++e) {
+      v[e] = 0;
+      __builtin_memcpy(&v[e], p + min(e, n - 1), sizeof(T));
+    }
+#pragma unroll
+    for (int e = 0; e < EL<T> - 1; ++e)
+      if (e < n) f.w[e * sizeof(T) / 4] |= v[e] << (8 * (e * sizeof(T) % 4));
+  }
   return f;
+}
+// The same where `full` says, for the whole wave, that no piece ends early.
+template <typename T>
+__device__ __forceinline__ frag<T> load_frag(const T* p, int32_t n, bool full) {
+  return full ? load_frag(p) : load_frag(p, n);
 }
 template <typename T>
 __device__ __forceinline__ void store_frag(T* p, const frag<T>& f, int32_t n) {
   if (n >= EL<T>) {
     __builtin_memcpy(p, &f, 16);
   } else {
+#pragma unroll
     for (int e = 0; e < EL<T> - 1; ++e)
-      if (e < n) p[e] = f.v[e];
+      if (e < n) {
+        const uint32_t v = f.w[e * sizeof(T) / 4] >> (8 * (e * sizeof(T) % 4));
+        __builtin_memcpy(p + e, &v, sizeof(T));
+      }
   }
+}
+// f, or zeros.
+template <typename T>
+__device__ __forceinline__ frag<T> keep_if(bool keep, const frag<T>& f) {
+  frag<T> o;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) o.w[q] = keep ? f.w[q] : 0u;
+  return o;
 }
 
 __device__ __forceinline__ f4 mma(const frag<bf16>& a, const frag<bf16>& b, f4 c) {
@@ -81,38 +115,57 @@ __device__ __forceinline__ f4 mma(const frag<bf16>& a, const frag<bf16>& b, f4 c
 // the order of the contraction is free as long as both sides share it.
 __device__ __forceinline__ f4 mma(const frag<float>& a, const frag<float>& b, f4 c) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
+  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(at(a, e), at(b, e), c, 0, 0, 0);
   return c;
 }
 
-// v as two bf16 parts, hi + lo: off by at most 2^-16 of v.
-__device__ __forceinline__ void split_bf16(float v, bf16& hi, bf16& lo) {
-  hi = f32_to_bf16(v);
-  const float h = bf16_to_f32(hi);
-  lo = fabsf(h) < __builtin_inff() ? f32_to_bf16(v - h) : (bf16)0;  // infinities, NaN: hi alone
+// Two floats as bf16, rounded to nearest even, in one dword.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{a, b}), b2));
+}
+__device__ __forceinline__ frag<bf16> to_frag(const float (&v)[8]) {
+  return frag<bf16>{{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
+                     bf16_pair(v[6], v[7])}};
+}
+__device__ __forceinline__ frag<float> to_frag(const float (&v)[4]) {
+  return frag<float>{{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3])}};
+}
+
+// v as two bf16 parts, hi + lo: off by at most 2^-16 of v.  Infinities and NaN
+// are hi alone.
+__device__ __forceinline__ void split_frag(const float (&v)[8], frag<bf16>& hi, frag<bf16>& lo) {
+  hi = to_frag(v);
+  float rest[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float h = at(hi, e);
+    rest[e] = fabsf(h) < __builtin_inff() ? v[e] - h : 0.f;
+  }
+  lo = to_frag(rest);
 }
 
 // out[c] = column c of the 8 x 8 matrix whose row q is rows[q].
 __device__ __forceinline__ void transpose8(const frag<bf16> (&rows)[8], frag<bf16> (&out)[8]) {
-  uint32_t in[8][4], o[8][4];
-  __builtin_memcpy(in, rows, sizeof(in));
 #pragma unroll
   for (int d = 0; d < 4; ++d)
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      o[2 * d][p] = __builtin_amdgcn_perm(in[2 * p + 1][d], in[2 * p][d], 0x05040100u);
-      o[2 * d + 1][p] = __builtin_amdgcn_perm(in[2 * p + 1][d], in[2 * p][d], 0x07060302u);
+      const uint32_t a = rows[2 * p].w[d], b = rows[2 * p + 1].w[d];
+      out[2 * d].w[p] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+      out[2 * d + 1].w[p] = __builtin_amdgcn_perm(b, a, 0x07060302u);
     }
-  __builtin_memcpy(out, o, sizeof(o));
 }
 
 // --------------------------------------------------------------- a few tokens
-// One token per blockIdx.y; its eight waves split the ranks.
-// PARTS & 1: t[i, j] = sum_k F0[a, j, k] X[i, k], kept in LDS (and stored to t
-// if given).  PARTS & 2: Y[i, :] from t over 64 pieces of columns per
-// workgroup.  With both parts one launch does the whole token, every workgroup
-// of it computing t again.
-constexpr int FEW_WAVES = 8;
+// A workgroup has one token and every split-th block of 64 pieces of columns.
+// Its sixteen waves share the ranks, first for t (each workgroup of the token
+// computes all of t again: the factor comes from the caches), then for the
+// expansion, whose parts meet in LDS.  What the expansion reads first is
+// loaded before t, so one trip to memory covers both.
+constexpr int FEW_WAVES = 16;
 
 template <typename T>
 __device__ __forceinline__ float dot_frag(const frag<T>& a, const frag<T>& b, float acc) {
@@ -122,92 +175,124 @@ __device__ __forceinline__ float dot_frag(const frag<T>& a, const frag<T>& b, fl
   return dot_acc<T, EL<T>>(x, y, acc);
 }
 
-template <typename T, int PARTS>
+// out[q * FEW_WAVES] = sum_k F[q * FEW_WAVES, k] x[k] for RW rows, by one wave.
+template <typename T, int RW>
+__device__ __forceinline__ void few_dots(const T* x, const T* __restrict__ F, int32_t K, float* out) {
+  constexpr int E = EL<T>, U = RW == 1 ? 8 : 8 / RW;
+  const int l = lane_id();
+  const int64_t next = (int64_t)FEW_WAVES * K;
+  float acc[RW] = {};
+  int32_t k = l * E;
+  for (; k + (U - 1) * 64 * E + E <= K; k += U * 64 * E) {
+    frag<T> xv[U], fv[U][RW];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      xv[u] = load_frag(x + k + u * 64 * E);
+#pragma unroll
+      for (int q = 0; q < RW; ++q) fv[u][q] = load_frag(F + q * next + k + u * 64 * E);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int q = 0; q < RW; ++q) acc[q] = dot_frag(xv[u], fv[u][q], acc[q]);
+  }
+  for (; k + E <= K; k += 64 * E) {
+    const frag<T> xv = load_frag(x + k);
+#pragma unroll
+    for (int q = 0; q < RW; ++q) acc[q] = dot_frag(xv, load_frag(F + q * next + k), acc[q]);
+  }
+  if (k < K) {
+    const frag<T> xv = load_frag(x + k, K - k);
+#pragma unroll
+    for (int q = 0; q < RW; ++q) acc[q] = dot_frag(xv, load_frag(F + q * next + k, K - k), acc[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < RW; ++q) {
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) acc[q] += __shfl_xor(acc[q], m, 64);
+    if (l == 0) out[q * FEW_WAVES] = acc[q];
+  }
+}
+
+template <typename T>
 __global__ __launch_bounds__(FEW_WAVES * 64) void k_lora_few(
-    lora_dev d, const int32_t* __restrict__ ids, const T* __restrict__ A, int32_t K, const T* X,
-    int64_t ldx, const T* __restrict__ B, int32_t M, const T* base, int64_t ldb, T* Y, int64_t ldy,
-    float* t) {
-  constexpr int E = EL<T>;
+    lora_dev d, const int32_t* __restrict__ ids, int32_t Tn, int32_t split,
+    const T* __restrict__ A, int32_t K, const T* X, int64_t ldx, const T* __restrict__ B, int32_t M,
+    const T* base, int64_t ldb, T* Y, int64_t ldy, float* t) {
+  constexpr int E = EL<T>, C = 64 * E;
   __shared__ float ts[MAX_RANK];
-  __shared__ float red[FEW_WAVES][64 * E];
-  const int64_t i = blockIdx.y;
+  __shared__ float red[FEW_WAVES][C];
+  // From 8 tokens on a token's workgroups share a die, whose L2 then holds
+  // the token's factor once.
+  int32_t i = blockIdx.x / split, cb = blockIdx.x % split;
+  if (Tn >= NUM_XCD) {
+    const int32_t at = blockIdx.x / NUM_XCD;
+    i = at / split * NUM_XCD + blockIdx.x % NUM_XCD;
+    cb = at % split;
+  }
+  if (i >= Tn) return;
   const int32_t a = ids[i];
   const int w = threadIdx.x / 64, l = lane_id();
   const int32_t r = a >= 0 && a < d.L ? rank_of(d, a) : 0;
-  const int32_t col = blockIdx.x * 64 * E + l * E;
-  constexpr int RW = 4;  // ranks of a wave at a time
-  if (PARTS & 1) {
-    const int32_t j_of = PARTS == 1 ? blockIdx.x * FEW_WAVES * RW : 0;
-    const int32_t j_end = PARTS == 1 ? min(j_of + FEW_WAVES * RW, d.R) : r;
-    const T* x = X + i * ldx;
-    for (int32_t j0 = j_of + w; j0 < j_end; j0 += FEW_WAVES * RW) {
-      float acc[RW] = {};
-      const T* f[RW];
-#pragma unroll
-      for (int q = 0; q < RW; ++q)
-        f[q] = A + ((int64_t)max(a, 0) * d.R + min(j0 + q * FEW_WAVES, max(r - 1, 0))) * K;
-      if (j0 < r) {
-        int32_t k = l * E;
-#pragma unroll 4
-        for (; k + E <= K; k += 64 * E) {
-          const frag<T> xv = load_frag(x + k);
-#pragma unroll
-          for (int q = 0; q < RW; ++q) acc[q] = dot_frag(xv, load_frag(f[q] + k), acc[q]);
-        }
-        if (k < K) {
-          const frag<T> xv = load_frag(x + k, K - k);
-#pragma unroll
-          for (int q = 0; q < RW; ++q) acc[q] = dot_frag(xv, load_frag(f[q] + k, K - k), acc[q]);
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < RW; ++q) {
-        const int32_t j = j0 + q * FEW_WAVES;
-#pragma unroll
-        for (int m = 32; m > 0; m >>= 1) acc[q] += __shfl_xor(acc[q], m, 64);
-        if (l == 0 && j < (PARTS == 1 ? d.R : r)) {
-          const float v = j < r ? acc[q] : 0.f;
-          if (PARTS & 2) ts[j] = v;
-          else t[i * d.R + j] = v;
-        }
-      }
-    }
-    if (!(PARTS & 2)) return;
-  } else {
-    for (int32_t j = threadIdx.x; j < r; j += FEW_WAVES * 64) ts[j] = t[i * d.R + j];
-  }
-  __syncthreads();
-  if (PARTS == 3 && t && blockIdx.x == 0)
-    for (int32_t j = threadIdx.x; j < d.R; j += FEW_WAVES * 64) t[i * d.R + j] = j < r ? ts[j] : 0.f;
-  float y[E] = {};
-  if (col < M) {
-#pragma unroll 4
-    for (int32_t j = w; j < r; j += FEW_WAVES) {
-      const frag<T> bv = load_frag(B + ((int64_t)a * d.R + j) * M + col, M - col);
-#pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = fmaf(ts[j], elem<T>::to_f(bv.v[e]), y[e]);
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) red[w][l * E + e] = y[e];
-  __syncthreads();
   const float s = a >= d.L ? __builtin_nanf("") : r > 0 ? scale_of(d, a) : 1.f;
-  for (int32_t c = threadIdx.x; c < 64 * E; c += FEW_WAVES * 64) {
-    const int32_t m = blockIdx.x * 64 * E + c;
-    if (m >= M) break;
-    float v = 0.f;
+  const int64_t row0 = r > 0 ? (int64_t)a * d.R : 0;
+  const T* Bw = B + (row0 + w) * M;
+  const int c = threadIdx.x;
+  frag<T> b0{};
+  T base0 = 0;
+  if (w < r) b0 = load_frag(Bw + (int64_t)cb * C + l * E, M - cb * C - l * E);
+  if (base && c < C && cb * C + c < M) base0 = base[i * ldb + cb * C + c];
+  const T* x = X + i * ldx;
+  for (int32_t j = w; j < r;) {
+    const T* F = A + (row0 + j) * K;
+    if (j + 3 * FEW_WAVES < r) {
+      few_dots<T, 4>(x, F, K, ts + j);
+      j += 4 * FEW_WAVES;
+    } else if (j + FEW_WAVES < r) {
+      few_dots<T, 2>(x, F, K, ts + j);
+      j += 2 * FEW_WAVES;
+    } else {
+      few_dots<T, 1>(x, F, K, ts + j);
+      j += FEW_WAVES;
+    }
+  }
+  __syncthreads();
+  if (t && cb == 0 && c < d.R) t[(int64_t)i * d.R + c] = c < r ? ts[c] : 0.f;
+  for (bool first = true; cb * C < M; cb += split, first = false) {
+    const int32_t col = cb * C + l * E;
+    float y[E] = {};
+    if (!first) {
+      if (w < r) b0 = load_frag(Bw + col, M - col);
+      if (base && c < C && cb * C + c < M) base0 = base[i * ldb + cb * C + c];
+    }
+    if (w < r)
 #pragma unroll
-    for (int q = 0; q < FEW_WAVES; ++q) v += red[q][c];
-    v *= s;
-    if (base) v += elem<T>::to_f(base[i * ldb + m]);
-    Y[i * ldy + m] = elem<T>::from_f(v);
+      for (int e = 0; e < E; ++e) y[e] = ts[w] * at(b0, e);
+#pragma unroll 4
+    for (int32_t j = w + FEW_WAVES; j < r; j += FEW_WAVES) {
+      const frag<T> bv = load_frag(B + (row0 + j) * M + col, M - col);
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = fmaf(ts[j], at(bv, e), y[e]);
+    }
+    if (!first) __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) red[w][l * E + e] = y[e];
+    __syncthreads();
+    if (c < C && cb * C + c < M) {
+      float v = 0.f;
+#pragma unroll
+      for (int q = 0; q < FEW_WAVES; ++q) v += red[q][c];
+      v *= s;
+      if (base) v += elem<T>::to_f(base0);
+      Y[i * ldy + cb * C + c] = elem<T>::from_f(v);
+    }
   }
 }
 
 // ------------------------------------------------------- tokens in adapter order
 // A tile is a run of up to TILE tokens of one adapter in that order; group L
 // holds the tokens without an adapter.  A slot is a run of tiles of one
-// adapter whose gradient one workgroup sums; the slots of an adapter that has
+// adapter whose gradient is summed in one go; the slots of an adapter that has
 // several leave partial sums at `part`, part + 1, ...
 struct tile_t { int32_t l, begin, n, pad; };
 struct slot_t { int32_t l, tile, n, part; };  // part < 0: the adapter's only slot
@@ -224,8 +309,11 @@ struct route_t {
   const int32_t* count;    // tiles, slots
 };
 
+__device__ __forceinline__ int32_t tiles_of(const route_t& p) {
+  return p.order ? p.count[0] : (p.Tn + TILE - 1) / TILE;
+}
 __device__ __forceinline__ tile_t tile_at(const route_t& p, int32_t i) {
-  if (p.order) return i < p.count[0] ? p.tile[i] : tile_t{0, 0, 0, 0};
+  if (p.order) return p.tile[i];
   return tile_t{0, i * TILE, min(TILE, p.Tn - i * TILE), 0};
 }
 __device__ __forceinline__ slot_t slot_at(const route_t& p, int32_t i) {
@@ -237,16 +325,35 @@ __device__ __forceinline__ slot_t slot_at(const route_t& p, int32_t i) {
 __device__ __forceinline__ int32_t row_at(const route_t& p, int32_t i) {
   return p.order ? p.order[i] : i;
 }
-// Whether token `row` of a tile of adapter l has that adapter (tokens in their
-// own order may have none).
-__device__ __forceinline__ bool has_adapter(const route_t& p, int32_t L, int32_t l, int32_t row) {
-  return p.order ? l < L : p.ids[row] == 0;
+
+// Exclusive prefixes over a block of 1024 of four values per thread; total
+// receives the sums.  Contains barriers.
+struct four_t { int32_t v[4]; };
+__device__ __forceinline__ four_t scan_four(four_t x, four_t* lds, four_t& total) {
+  const int w = threadIdx.x / 64;
+  four_t inc, out;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) inc.v[q] = wave_incl_scan_i32(x.v[q]);
+  __syncthreads();
+  if (lane_id() == 63) lds[w] = inc;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) total.v[q] = 0, out.v[q] = inc.v[q] - x.v[q];
+#pragma unroll 2
+  for (int i = 0; i < 16; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int32_t t = lds[i].v[q];
+      if (i < w) out.v[q] += t;
+      total.v[q] += t;
+    }
+  return out;
 }
 
 // Stable counting sort of the tokens by adapter, then the tables of tiles and
 // slots, in one workgroup: wave w < nw walks its own run of tokens, once to
 // count and once to place; lanes that hold the same adapter find each other by
-// one ballot per bit.
+// one ballot per bit.  A walk loads RUN x 64 ids before it uses the first.
 __global__ __launch_bounds__(1024) void k_lora_route(const int32_t* __restrict__ ids, int32_t Tn,
                                                      int32_t L, int32_t nw, int32_t slot_tiles,
                                                      int32_t* __restrict__ order,
@@ -254,10 +361,12 @@ __global__ __launch_bounds__(1024) void k_lora_route(const int32_t* __restrict__
                                                      slot_t* __restrict__ slot,
                                                      join_t* __restrict__ join,
                                                      int32_t* __restrict__ count) {
-  extern __shared__ int32_t cnt[];  // [nw][L + 1]
-  __shared__ int32_t lds[16];
+  extern __shared__ int32_t cnt[];  // [nw][G], then first token and first tile of the groups
+  __shared__ four_t lds[16];
+  constexpr int RUN = 8;
   const int32_t G = L + 1;
   const int w = threadIdx.x / 64, l = lane_id();
+  int32_t *first = cnt + nw * G, *first_tile = first + G + 1;
   for (int32_t i = threadIdx.x; i < nw * G; i += 1024) cnt[i] = 0;
   __syncthreads();
   const int32_t run = ((Tn + nw - 1) / nw + 63) / 64 * 64;
@@ -266,27 +375,36 @@ __global__ __launch_bounds__(1024) void k_lora_route(const int32_t* __restrict__
   auto walk = [&](bool place) {
     if (w >= nw) return;
     int32_t* mine = cnt + w * G;
-    for (int64_t b = i0; b < i1; b += 64) {
-      const bool in = b + l < i1;
-      const int32_t id = in ? ids[b + l] : 0;
-      const int32_t g = id >= 0 && id < L ? id : L;
-      uint64_t peers = __ballot(in);
-      for (int k = 0; k < bits; ++k) {
-        const uint64_t m = __ballot((g >> k) & 1);
-        peers &= ((g >> k) & 1) ? m : ~m;
+    for (int64_t b0 = i0; b0 < i1; b0 += 64 * RUN) {
+      int32_t id[RUN];
+#pragma unroll
+      for (int q = 0; q < RUN; ++q) id[q] = ids[min(b0 + q * 64 + l, i1 - 1)];
+#pragma unroll
+      for (int q = 0; q < RUN; ++q) {
+        const int64_t b = b0 + q * 64;
+        if (b >= i1) break;
+        const bool in = b + l < i1;
+        const int32_t g = id[q] >= 0 && id[q] < L ? id[q] : L;
+        uint64_t peers = __ballot(in);
+        for (int k = 0; k < bits; ++k) {
+          const uint64_t m = __ballot((g >> k) & 1);
+          peers &= ((g >> k) & 1) ? m : ~m;
+        }
+        const int before = __popcll(peers & lanemask_lt());
+        int32_t at = 0;
+        if (in) at = mine[g] + before;
+        if (place && in) order[at] = (int32_t)(b + l);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (in && before == 0) mine[g] = at + __popcll(peers);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
       }
-      const int before = __popcll(peers & lanemask_lt());
-      int32_t at = 0;
-      if (in) at = mine[g] + before;
-      if (place && in) order[at] = (int32_t)(b + l);
-      __builtin_amdgcn_wave_barrier();
-      if (in && before == 0) mine[g] = at + __popcll(peers);
-      __builtin_amdgcn_wave_barrier();
     }
   };
   walk(false);
   __syncthreads();
-  int32_t tok = 0, til = 0, slo = 0, par = 0;  // totals of the groups so far
+  four_t sum{};  // tokens, tiles, slots and partial sums of the groups so far
   for (int32_t g0 = 0; g0 < G; g0 += 1024) {
     const int32_t g = g0 + threadIdx.x;
     int32_t n = 0;
@@ -294,369 +412,447 @@ __global__ __launch_bounds__(1024) void k_lora_route(const int32_t* __restrict__
       for (int32_t q = 0; q < nw; ++q) n += cnt[q * G + g];
     const int32_t nt = (n + TILE - 1) / TILE;
     const int32_t ns = g < L ? (nt + slot_tiles - 1) / slot_tiles : 0;
-    const int32_t np = ns > 1 ? ns : 0;
-    int32_t total;
-    int32_t b = block_excl_scan_i32<1024>(n, lds, &total) + tok;
-    tok += total;
-    const int32_t bt = block_excl_scan_i32<1024>(nt, lds, &total) + til;
-    til += total;
-    const int32_t bs = block_excl_scan_i32<1024>(ns, lds, &total) + slo;
-    slo += total;
-    const int32_t bp = block_excl_scan_i32<1024>(np, lds, &total) + par;
-    par += total;
+    four_t total;
+    four_t b = scan_four(four_t{{n, nt, ns, ns > 1 ? ns : 0}}, lds, total);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) b.v[q] += sum.v[q], sum.v[q] += total.v[q];
     if (g < G) {
-      for (int32_t k = 0; k < nt; ++k)
-        tile[bt + k] = tile_t{g, b + k * TILE, min(TILE, n - k * TILE), 0};
+      first[g] = b.v[0];
+      first_tile[g] = b.v[1];
       for (int32_t k = 0; k < ns; ++k)
-        slot[bs + k] = slot_t{g, bt + k * slot_tiles, min(slot_tiles, nt - k * slot_tiles),
-                              ns > 1 ? bp + k : -1};
-      if (g < L) join[g] = join_t{ns, bp};
+        slot[b.v[2] + k] = slot_t{g, b.v[1] + k * slot_tiles,
+                                  min(slot_tiles, nt - k * slot_tiles), ns > 1 ? b.v[3] + k : -1};
+      if (g < L) join[g] = join_t{ns, b.v[3]};
+      int32_t at = b.v[0];
       for (int32_t q = 0; q < nw; ++q) {
         const int32_t c = cnt[q * G + g];
-        cnt[q * G + g] = b;
-        b += c;
+        cnt[q * G + g] = at;
+        at += c;
       }
     }
   }
   if (threadIdx.x == 0) {
-    count[0] = til;
-    count[1] = slo;
+    count[0] = sum.v[1];
+    count[1] = sum.v[2];
+    first[G] = Tn;
   }
   __syncthreads();
   walk(true);
+  for (int32_t i = threadIdx.x; i < sum.v[1]; i += 1024) {
+    int32_t lo = 0, hi = G;  // the last group whose first tile is <= i
+    while (hi - lo > 1) {
+      const int32_t mid = (lo + hi) / 2;
+      if (first_tile[mid] <= i) lo = mid;
+      else hi = mid;
+    }
+    const int32_t at = first[lo] + (i - first_tile[lo]) * TILE;
+    tile[i] = tile_t{lo, at, min(TILE, first[lo + 1] - at), 0};
+  }
 }
 
-// ------------------------------------------------------------------- reduce
-// out[ks][i][j] = the part of sum_k F[a, j, k] X[i, k] that this workgroup's
-// range of k gives; the ks parts are summed where they are read.  A wave takes
-// its own range of k and all tokens and ranks of the tile: both operands of
-// the 16x16 products are rows that lie contiguous along the contraction, so
-// each lane loads its operand from memory as it is.
+// ------------------------------------------------------------- tiles of tokens
+// One workgroup takes a tile through both products.  t of the tile: every wave
+// sums its own range of k for all tokens and ranks, and the waves' sums meet
+// in LDS.  Then every wave expands t over its own columns.
+constexpr int WAVES = 8;
+enum { ROW_NONE = 0, ROW_HAS = 1, ROW_BAD = 2 };
+
 template <typename T>
-struct reduce_arg {
+struct reduce_arg {  // t[i, j] = sum_k F[a, j, k] X[i, k]
   const T* F;
   const T* X;
   int64_t ldx;
   int32_t K;
-  int32_t ks;   // parts
-  float* out;   // [ks][Tn][R]
+  const float* given;  // t itself, if it is there already
+  float* t;            // nullable: where t goes
+  void* pack;          // nullable: where t goes as the gradient's operand
+};
+template <typename T>
+struct expand_arg {  // Y[i, m] = base[i, m] + s sum_j t[i, j] F[a, j, m]
+  const T* F;
+  int32_t M;
+  const T* base;
+  int64_t ldb;
+  T* Y;
+  int64_t ldy;
 };
 
-constexpr int RED_WAVES = 8;
+struct tile_lds {
+  int32_t row[TILE];
+  int8_t kind[TILE];
+};
 
+// ts[token][rank < r] = t, 0 for tokens without the adapter; ld: ts's stride.
+// A wave brings 128 bytes of each row at a time: eight lanes a row, so that a
+// load touches 8 lines (16 rows of 64 bytes, as the products take them, would
+// cost a look-up in the cache for every lane).  LDS of its own turns them into
+// operands; row i's piece s lies at slot s ^ (i & 7), which spreads both the
+// writes and the reads over all banks.
 template <typename T, int RT, int NR>
-__device__ __forceinline__ void reduce_tile(const lora_dev& d, const route_t& p,
-                                            const reduce_arg<T>& q, const tile_t& tl, int32_t r,
-                                            int32_t rb, float (*red)[TILE * 16]) {
-  constexpr int KS = 4 * EL<T>;  // contraction of a step
+__device__ __forceinline__ void reduce_tile(const lora_dev& d, const reduce_arg<T>& q,
+                                            const tile_t& tl, int32_t r, const tile_lds& tk,
+                                            char* lds, float* ts, int32_t ld) {
+  constexpr int E = EL<T>, KS = 8 * E;       // contraction of a step
+  constexpr int NI = 2 * (RT + NR);          // loads of a step
+  constexpr int U = NI <= 6 ? 2 : 1;         // steps whose loads are under way together
   const int w = threadIdx.x / 64, l = lane_id(), c = l & 15, g = l >> 4;
-  const T* x[RT];
-  const T* f[NR];
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-    x[i] = q.X + (int64_t)row_at(p, tl.begin + min(i * 16 + c, tl.n - 1)) * q.ldx + g * EL<T>;
-#pragma unroll
-  for (int j = 0; j < NR; ++j)  // rows past the rank: results not used
-    f[j] = q.F + ((int64_t)tl.l * d.R + min(rb + j * 16 + c, r - 1)) * q.K + g * EL<T>;
-  f4 acc[RT][NR];
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < NR; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
-  const int64_t steps = (q.K + KS - 1) / KS, n = (int64_t)q.ks * RED_WAVES;
-  const int64_t at = (int64_t)blockIdx.y * RED_WAVES + w;
-  const int32_t s0 = (int32_t)(steps * at / n), s1 = (int32_t)(steps * (at + 1) / n);
+  const int row8 = l >> 3, slot = l & 7;
+  frag<T>* mine = reinterpret_cast<frag<T>*>(lds) + w * (NI * 64);
+  frag<T>* put = mine + row8 * 8 + (slot ^ row8);
+  const frag<T>* get = mine + c * 8;
+  const int32_t steps = (q.K + KS - 1) / KS;
+  const int32_t s0 = (int32_t)((int64_t)steps * w / WAVES),
+                s1 = (int32_t)((int64_t)steps * (w + 1) / WAVES);
   const int32_t full = min(s1, q.K / KS);
-#pragma unroll 4
-  for (int32_t s = s0; s < full; ++s) {
-    frag<T> xv[RT], fv[NR];
+  for (int32_t rb = 0; rb < r; rb += 16 * NR) {
+    const T* src[NI];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) xv[i] = load_frag(x[i] + (int64_t)s * KS);
+    for (int i = 0; i < 2 * RT; ++i)
+      src[i] = q.X + (int64_t)tk.row[i * 8 + row8] * q.ldx + slot * E;
 #pragma unroll
-    for (int j = 0; j < NR; ++j) fv[j] = load_frag(f[j] + (int64_t)s * KS);
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int j = 0; j < NR; ++j) acc[i][j] = mma(xv[i], fv[j], acc[i][j]);
-  }
-  if (full < s1) {  // the step that ends past K
-    const int32_t left = q.K - full * KS - g * EL<T>;
-    frag<T> xv[RT], fv[NR];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) xv[i] = load_frag(x[i] + (int64_t)full * KS, left);
-#pragma unroll
-    for (int j = 0; j < NR; ++j) fv[j] = load_frag(f[j] + (int64_t)full * KS, left);
+    for (int i = 0; i < 2 * NR; ++i)  // rows past the rank: results not used
+      src[2 * RT + i] = q.F + ((int64_t)tl.l * d.R + min(rb + i * 8 + row8, r - 1)) * q.K + slot * E;
+    f4 acc[RT][NR];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int j = 0; j < NR; ++j) acc[i][j] = mma(xv[i], fv[j], acc[i][j]);
-  }
-  float* out = q.out + (int64_t)blockIdx.y * p.Tn * d.R;
+      for (int j = 0; j < NR; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+    auto turn = [&](const frag<T> (&v)[NI]) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-  for (int j = 0; j < NR; ++j) {
-    if (rb + j * 16 >= d.R) break;
-    __syncthreads();
+      for (int i = 0; i < NI; ++i) put[i * 64] = v[i];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+      for (int h = 0; h < 2; ++h) {
+        frag<T> xv[RT], fv[NR];
+        const int at = (h * 4 + g) ^ (c & 7);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) red[w][(i * 16 + 4 * g + e) * 16 + c] = acc[i][j][e];
-    __syncthreads();
-    for (int32_t k = threadIdx.x; k < RT * 256; k += RED_WAVES * 64) {
-      const int32_t tok = k / 16, rank = rb + j * 16 + k % 16;
-      if (tok >= tl.n || rank >= d.R) continue;
-      float v = 0.f;
+        for (int i = 0; i < RT; ++i) xv[i] = get[i * 128 + at];
 #pragma unroll
-      for (int m = 0; m < RED_WAVES; ++m) v += red[m][k];
-      const int32_t row = row_at(p, tl.begin + tok);
-      out[(int64_t)row * d.R + rank] = rank < r && has_adapter(p, d.L, tl.l, row) ? v : 0.f;
+        for (int j = 0; j < NR; ++j) fv[j] = get[(RT + j) * 128 + at];
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int j = 0; j < NR; ++j) acc[i][j] = mma(xv[i], fv[j], acc[i][j]);
+      }
+    };
+    int32_t s = s0;
+    for (; s + U <= full; s += U) {
+      frag<T> v[U][NI];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) v[u][i] = load_frag(src[i] + (int64_t)(s + u) * KS);
+#pragma unroll
+      for (int u = 0; u < U; ++u) turn(v[u]);
     }
+    for (; s < s1; ++s) {  // what is left, and the step that ends past K
+      const int32_t left = q.K - s * KS - slot * E;
+      frag<T> v[NI];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) v[i] = load_frag(src[i] + (int64_t)s * KS, left, s < full);
+      turn(v);
+    }
+    float* red = reinterpret_cast<float*>(lds);  // over the operands of all waves
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+      if (rb + j * 16 >= r) break;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) red[w * RT * 256 + (i * 16 + 4 * g + e) * 16 + c] = acc[i][j][e];
+      __syncthreads();
+      if (threadIdx.x < RT * 256) {
+        const int32_t tok = threadIdx.x / 16, rank = threadIdx.x % 16;
+        float v = 0.f;
+#pragma unroll
+        for (int m = 0; m < WAVES; ++m) v += red[m * RT * 256 + threadIdx.x];
+        ts[tok * ld + rb + j * 16 + rank] = tk.kind[tok] == ROW_HAS ? v : 0.f;
+      }
+    }
+    if (rb + 16 * NR < r) __syncthreads();
   }
 }
 
-// grid: tiles x parts x (problems * rank blocks of 16 * NR)
-template <typename T, int NR>
-__global__ __launch_bounds__(RED_WAVES * 64) void k_lora_reduce(lora_dev d, route_t p,
-                                                                reduce_arg<T> q0,
-                                                                reduce_arg<T> q1,
-                                                                int32_t rank_blocks) {
-  __shared__ float red[RED_WAVES][TILE * 16];
-  const reduce_arg<T> q = (int32_t)blockIdx.z < rank_blocks ? q0 : q1;
-  const int32_t rb = (int32_t)blockIdx.z % rank_blocks * 16 * NR;
-  if ((int32_t)blockIdx.y >= q.ks) return;
-  const tile_t tl = tile_at(p, blockIdx.x);
-  if (tl.n <= 0) return;
-  const int32_t r = tl.l < d.L ? rank_of(d, tl.l) : 0;
-  if (rb >= r) {  // nothing of this adapter's here: zeros
-    float* out = q.out + (int64_t)blockIdx.y * p.Tn * d.R;
-    const int32_t n = min(16 * NR, d.R - rb);
-    for (int32_t k = threadIdx.x; k < tl.n * n; k += RED_WAVES * 64)
-      out[(int64_t)row_at(p, tl.begin + k / n) * d.R + rb + k % n] = 0.f;
-    return;
-  }
-  if (tl.n <= 16) reduce_tile<T, 1, NR>(d, p, q, tl, r, rb, red);
-  else reduce_tile<T, 4, NR>(d, p, q, tl, r, rb, red);
+// NR: rank tiles of the largest rank; an adapter takes as many as it has.
+template <typename T, int RT, int NR>
+__device__ __forceinline__ void reduce_ranks(const lora_dev& d, const reduce_arg<T>& q,
+                                             const tile_t& tl, int32_t r, const tile_lds& tk,
+                                             char* lds, float* ts, int32_t ld) {
+  if (NR == 1 || r <= 16) reduce_tile<T, RT, 1>(d, q, tl, r, tk, lds, ts, ld);
+  else if (NR == 2 || r <= 32) reduce_tile<T, RT, 2>(d, q, tl, r, tk, lds, ts, ld);
+  else reduce_tile<T, RT, 4>(d, q, tl, r, tk, lds, ts, ld);
 }
 
-// ------------------------------------------------------------------- expand
-// Y[i, m] = base[i, m] + s sum_j t[i, j] F[a, j, m] for a tile and 4 waves'
-// columns.  t is staged in LDS as the products' operand: for bf16 in two parts
-// (hi + lo, whose products sum to fp32's accuracy), for fp32 as it is.  The
-// factor's rows lie along m, so a lane's pieces of 8 rows are transposed in
-// registers into 8 operands of 8 ranks each; the results leave each lane with
-// EL columns side by side, one 16-byte piece of base in and one of Y out.
-constexpr int EXP_WAVES = 4;
-enum { ROW_NONE = 0, ROW_HAS = 1, ROW_BAD = 2 };
-
-template <typename T> struct expand_lds;
-template <> struct expand_lds<bf16> {
-  static size_t bytes(int32_t R) { return (size_t)cdiv(R, 32) * 4 * 2 * 64 * 16; }
-};
-template <> struct expand_lds<float> {
-  static size_t bytes(int32_t R) { return (size_t)TILE * (cdiv(R, 4) * 4 + 1) * 4; }
-};
-
-// t of token `row` at rank j, all parts summed.
-__device__ __forceinline__ float t_sum(const float* __restrict__ t, int64_t at, int64_t part,
-                                       int32_t ks) {
-  float v = t[at];
-  for (int32_t k = 1; k < ks; ++k) v += t[at + k * part];
-  return v;
-}
-
-template <typename T, int RT>
-__device__ __forceinline__ void expand_acc(const T* __restrict__ F, int32_t M, int32_t r,
-                                           int32_t R, int32_t col, const char* op,
-                                           f4 (&acc)[RT][EL<T>]) {
-  const int l = lane_id(), c = l & 15, g = l >> 4;
+// The scaled t of a tile as the operand of the products over tokens:
+//   bf16  pack[tile][rank tile][hi, lo][lane] pieces of 8 tokens
+//   fp32  pack[tile][token][ranks up to a multiple of 16]
+// zero for tokens and ranks that are not there.
+template <typename T>
+__device__ __forceinline__ void write_pack(void* pack, int32_t ti, int32_t NT, int32_t n, int32_t r,
+                                           float s, const float* ts, int32_t ld) {
   if constexpr (sizeof(T) == 2) {
-    const frag<bf16>* o = reinterpret_cast<const frag<bf16>*>(op);
-    for (int32_t rs = 0; rs * 32 < r; ++rs) {
-      frag<T> rows[8], cols[8];
+    frag<bf16>* o = reinterpret_cast<frag<bf16>*>(pack) + (int64_t)ti * NT * 2 * 64;
+    for (int32_t k = threadIdx.x; k < NT * 64; k += WAVES * 64) {
+      const int32_t l = k & 63, j = (k >> 6) * 16 + (l & 15);
+      float v[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const int32_t j = rs * 32 + 8 * g + q;
-        rows[q] = load_frag(F + (int64_t)j * M + col, j < r ? M - col : 0);
+        const int32_t tok = 8 * (l >> 4) + q;
+        v[q] = j < r && tok < n ? s * ts[tok * ld + j] : 0.f;
       }
-      transpose8(rows, cols);
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const frag<T> hi = o[((rs * 4 + i) * 2 + 0) * 64 + l], lo = o[((rs * 4 + i) * 2 + 1) * 64 + l];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[i][e] = mma(lo, cols[e], mma(hi, cols[e], acc[i][e]));
-      }
+      frag<bf16> hi, lo;
+      split_frag(v, hi, lo);
+      o[(k >> 6) * 2 * 64 + l] = hi;
+      o[(k >> 6) * 2 * 64 + 64 + l] = lo;
     }
   } else {
-    const float* ts = reinterpret_cast<const float*>(op);
-    const int32_t ld = (R + 3) / 4 * 4 + 1;
-#pragma unroll 4
-    for (int32_t q = 0; q < r; q += 4) {
-      const int32_t j = q + g;
-      const frag<T> row = load_frag(F + (int64_t)j * M + col, j < r ? M - col : 0);
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const float tv = ts[(i * 16 + c) * ld + j];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(tv, row.v[e], acc[i][e], 0, 0, 0);
-      }
+    float* o = reinterpret_cast<float*>(pack) + (int64_t)ti * TILE * NT * 16;
+    for (int32_t k = threadIdx.x; k < TILE * NT * 16; k += WAVES * 64) {
+      const int32_t tok = k / (NT * 16), j = k % (NT * 16);
+      o[k] = j < r && tok < n ? s * ts[tok * ld + j] : 0.f;
     }
   }
 }
 
-template <typename T, int RT>
-__device__ __forceinline__ void expand_tile(const lora_dev& d, const T* F, int32_t M, int32_t r,
-                                            const tile_t& tl, const char* op, const int32_t* rows,
-                                            const int8_t* kind, const T* base, int64_t ldb, T* Y,
-                                            int64_t ldy) {
-  constexpr int E = EL<T>;
-  const int l = lane_id(), c = l & 15, g = l >> 4;
-  const int32_t col = (blockIdx.y * EXP_WAVES + threadIdx.x / 64) * 16 * E + c * E;
-  f4 acc[RT][E];
+// Columns of a wave at a time: 16 pieces.  The factor's rows lie along m, so a
+// lane's pieces of 8 rows (bf16) are transposed in registers into 8 operands
+// of 8 ranks each; the results leave each lane with EL columns side by side,
+// one 16-byte piece of base in and one of Y out.  bf16 takes t in two parts
+// (hi + lo, whose products sum to fp32's accuracy): up to 16 ranks both parts
+// share one product (contraction 0-15 hi, 16-31 lo), above them each part has
+// its own, 32 ranks a step, staged in LDS (op).
+template <typename T, int RT, bool ONE>
+__device__ __forceinline__ void expand_tile(const expand_arg<T>& q, const T* __restrict__ F,
+                                            const tile_t& tl, int32_t r, float s,
+                                            const tile_lds& tk, const float* ts, int32_t ld,
+                                            const frag<bf16>* op, int32_t role, int32_t split) {
+  constexpr int E = EL<T>, CW = 16 * E;
+  const int w = threadIdx.x / 64, l = lane_id(), c = l & 15, g = l >> 4;
+  const int32_t blocks = (q.M + CW - 1) / CW;
+  frag<bf16> t1[RT];
+  if constexpr (sizeof(T) == 2 && ONE) {
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+    for (int i = 0; i < RT; ++i) {
+      float v[8];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[i][e] = f4{0.f, 0.f, 0.f, 0.f};
-  if (r > 0) expand_acc<T, RT>(F + (int64_t)tl.l * d.R * M, M, r, d.R, col, op, acc);
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int32_t tok = i * 16 + 4 * g + k;
-      if (tok >= tl.n || col >= M) continue;
-      const int64_t row = rows[tok];
-      const int8_t has = kind[tok];
-      frag<T> bv{}, out;
-      if (base) bv = load_frag(base + row * ldb + col, M - col);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        float v = has == ROW_HAS ? acc[i][e][k] : has == ROW_NONE ? 0.f : __builtin_nanf("");
-        if (base) v += elem<T>::to_f(bv.v[e]);
-        out.v[e] = elem<T>::from_f(v);
+      for (int e = 0; e < 8; ++e) {
+        const int32_t j = 8 * (g & 1) + e;
+        v[e] = j < r ? s * ts[(i * 16 + c) * ld + j] : 0.f;
       }
-      store_frag(Y + row * ldy + col, out, M - col);
+      frag<bf16> hi, lo;
+      split_frag(v, hi, lo);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) t1[i].w[q] = g < 2 ? hi.w[q] : lo.w[q];
     }
+  }
+  bool whole = tl.n == RT * 16;  // every row of the tile has the adapter
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) whole = whole && tk.kind[i * 16 + 4 * g + k] == ROW_HAS;
+  whole = __all(whole);
+  // r rows of the factor, JS a step; rows past the rank count as zeros
+  constexpr int JS = sizeof(T) == 4 ? 4 : ONE ? 16 : 32;
+  constexpr int RG = sizeof(T) == 2 && ONE ? 1 : RT;  // groups of 16 rows summed at a time
+  const bool even = r % JS == 0;
+  auto block = [&](int32_t b, auto whole_block) {
+    constexpr bool full = decltype(whole_block)::value;
+    const int32_t col = b * CW + c * E, left = q.M - col;
+    frag<T> bv[RT][4];
+    // The row's number, read anew for each block (and the factor's row below):
+    // addresses kept over the loop cost more registers than there are.
+    auto row_of_tile = [&](int32_t tok) {
+      int32_t row = tk.row[tok];
+      asm volatile("" : "+v"(row));
+      return (int64_t)row;
+    };
+    auto load_base = [&](int i) {
+      if (q.base)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          bv[i][k] = load_frag(q.base + row_of_tile(i * 16 + 4 * g + k) * q.ldb + col, left, full);
+    };
+    auto put = [&](int i, f4 (&acc)[E]) {
+      if (!whole) {  // rows without an adapter get base alone, wrong ids NaN
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int8_t has = tk.kind[i * 16 + 4 * g + k];
+          const float v = has == ROW_BAD ? __builtin_nanf("") : 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e][k] = has == ROW_HAS ? acc[e][k] : v;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int32_t tok = i * 16 + 4 * g + k;
+        if (tok >= tl.n || (!full && left <= 0)) continue;
+        float v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          v[e] = acc[e][k];
+          if (q.base) v[e] += at(bv[i][k], e);
+        }
+        store_frag(q.Y + row_of_tile(tok) * q.ldy + col, to_frag(v), full ? E : left);
+      }
+    };
+    f4 acc[RG][E];
+#pragma unroll
+    for (int i = 0; i < RG; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[i][e] = f4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (sizeof(T) == 2) {
+      int32_t j_of = 8 * (ONE ? g & 1 : g);
+      asm volatile("" : "+v"(j_of));
+      frag<T> rows[8], cols[8];
+      auto load_rows = [&](int32_t j0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          rows[k] = load_frag(F + (int64_t)min(j0 + j_of + k, r - 1) * q.M + col, left, full);
+      };
+      auto turn = [&](int32_t j0) {
+        if (!even)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) rows[k] = keep_if(j0 + j_of + k < r, rows[k]);
+        transpose8(rows, cols);
+      };
+      if (r > 0) load_rows(0);
+      load_base(0);
+      if constexpr (ONE) {
+        if (r > 0) turn(0);
+        if constexpr (RT > 1) load_base(1);  // the rows' registers are free now
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          if (r > 0)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[0][e] = mma(t1[i], cols[e], f4{0.f, 0.f, 0.f, 0.f});
+          put(i, acc[0]);
+        }
+      } else {
+        if constexpr (RT > 1) load_base(1);
+        for (int32_t j0 = 0; j0 < r; j0 += JS) {
+          turn(j0);
+          if (j0 + JS < r) load_rows(j0 + JS);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            const frag<bf16>* o = op + ((j0 / 32 * 2 + i) * 2) * 64 + l;
+            const frag<bf16> hi = o[0], lo = o[64];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[i][e] = mma(lo, cols[e], mma(hi, cols[e], acc[i][e]));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) put(i, acc[i]);
+      }
+    } else {
+      load_base(0);
+      if constexpr (RT > 1) load_base(1);
+#pragma unroll 4
+      for (int32_t j0 = 0; j0 < r; j0 += 4) {
+        const int32_t j = j0 + g;
+        const frag<T> row =
+            keep_if(j < r, load_frag(F + (int64_t)min(j, r - 1) * q.M + col, left, full));
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const float tv = j < r ? s * ts[(i * 16 + c) * ld + j] : 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(tv, at(row, e), acc[i][e], 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i) put(i, acc[i]);
+    }
+  };
+  for (int32_t b = role * WAVES + w; b < blocks; b += split * WAVES) {
+    if ((b + 1) * CW <= q.M) block(b, std::true_type());
+    else block(b, std::false_type());
+  }
 }
 
-// grid: tiles x columns of EXP_WAVES waves.  t: ks parts; t_out (nullable)
-// receives their sum.
-template <typename T>
-__global__ __launch_bounds__(EXP_WAVES * 64, 2) void k_lora_expand(
-    lora_dev d, route_t p, const T* __restrict__ F, int32_t M, const float* __restrict__ t,
-    int32_t ks, float* __restrict__ t_out, const T* base, int64_t ldb, T* Y, int64_t ldy) {
-  extern __shared__ char op[];
-  __shared__ int32_t rows[TILE];
-  __shared__ int8_t kind[TILE];
-  const tile_t tl = tile_at(p, blockIdx.x);
-  if (tl.n <= 0) return;
+// grid: 8 * (tiles of a die) * roles.  Roles 0 to split - 1 of a tile compute t
+// of problem a and a share of the columns each, role 0 writes what is wanted
+// of t; role `split`, if launched, does the same for problem b, which has no
+// expansion.  From 64 tiles on each die takes a run of tiles, so that an
+// adapter's factors fill few L2s.
+template <typename T, int NR>
+__global__ __launch_bounds__(WAVES * 64, NR == 1 ? 4 : 2) void k_lora_apply(
+    lora_dev d, route_t p, reduce_arg<T> a, reduce_arg<T> b, expand_arg<T> e, int32_t split,
+    int32_t roles, uint32_t* __restrict__ mask) {
+  extern __shared__ char lds[];
+  __shared__ tile_lds tk;
+  const int32_t tiles = tiles_of(p), NT = (d.R + 15) / 16, ld = NT * 16 + 1;
+  int32_t ti = blockIdx.x / roles, role = blockIdx.x % roles;
+  if (tiles >= 64) {
+    const int32_t each = (tiles + NUM_XCD - 1) / NUM_XCD, at = blockIdx.x / NUM_XCD / roles;
+    if (at >= each) return;
+    role = blockIdx.x / NUM_XCD % roles;
+    ti = blockIdx.x % NUM_XCD * each + at;
+  }
+  if (ti >= tiles) return;
+  const tile_t tl = tile_at(p, ti);
   const int32_t r = tl.l < d.L ? rank_of(d, tl.l) : 0;
+  const float s = r > 0 ? scale_of(d, tl.l) : 0.f;
   if (threadIdx.x < TILE) {
     const int32_t tok = threadIdx.x;
     const int32_t row = row_at(p, tl.begin + min(tok, tl.n - 1));
-    rows[tok] = row;
-    kind[tok] = tok >= tl.n ? ROW_NONE
-                : has_adapter(p, d.L, tl.l, row) ? ROW_HAS
-                : p.ids[row] >= d.L ? ROW_BAD : ROW_NONE;
+    const int32_t id = p.order && tl.l < d.L ? tl.l : p.ids[row];
+    const int8_t kind = tok >= tl.n ? ROW_NONE : id >= d.L ? ROW_BAD : id >= 0 ? ROW_HAS : ROW_NONE;
+    tk.row[tok] = row;
+    tk.kind[tok] = kind;
+    const uint64_t has = __ballot(kind == ROW_HAS);
+    if (mask && role == 0 && tok == 0) mask[ti] = (uint32_t)has;
   }
   __syncthreads();
-  const int64_t part = (int64_t)p.Tn * d.R;
-  const float s = r > 0 ? scale_of(d, tl.l) : 0.f;
-  if constexpr (sizeof(T) == 2) {
-    frag<bf16>* o = reinterpret_cast<frag<bf16>*>(op);
-    const int32_t steps = (r + 31) / 32;
-    for (int32_t k = threadIdx.x; k < steps * 4 * 64; k += EXP_WAVES * 64) {
-      const int32_t l = k & 63, i = (k >> 6) & 3, rs = k >> 8;
-      const int32_t tok = i * 16 + (l & 15), j0 = rs * 32 + 8 * (l >> 4);
-      frag<bf16> hi{}, lo{};
-      if (tok < tl.n && kind[tok] == ROW_HAS)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (j0 + e >= r) break;
-          split_bf16(s * t_sum(t, (int64_t)rows[tok] * d.R + j0 + e, part, ks), hi.v[e], lo.v[e]);
-        }
-      o[((rs * 4 + i) * 2 + 0) * 64 + l] = hi;
-      o[((rs * 4 + i) * 2 + 1) * 64 + l] = lo;
+  float* ts = reinterpret_cast<float*>(lds);
+  char* room = lds + (TILE * ld + 3) / 4 * 16;  // the waves' operands, their sums, the scaled t
+  const reduce_arg<T>& q = role < split ? a : b;
+  if (q.given) {
+    for (int32_t k = threadIdx.x; k < tl.n * d.R; k += WAVES * 64) {
+      const int32_t tok = k / d.R, j = k % d.R;
+      ts[tok * ld + j] = tk.kind[tok] == ROW_HAS ? q.given[(int64_t)tk.row[tok] * d.R + j] : 0.f;
     }
+  } else if (tl.n <= 16) {
+    reduce_ranks<T, 1, NR>(d, q, tl, r, tk, room, ts, ld);
   } else {
-    float* ts = reinterpret_cast<float*>(op);
-    const int32_t ld = (d.R + 3) / 4 * 4 + 1, n = (r + 3) / 4 * 4;
-    for (int32_t k = threadIdx.x; k < n * TILE; k += EXP_WAVES * 64) {
-      const int32_t tok = k / n, j = k % n;
-      ts[tok * ld + j] = j < r && tok < tl.n && kind[tok] == ROW_HAS
-                             ? s * t_sum(t, (int64_t)rows[tok] * d.R + j, part, ks) : 0.f;
-    }
+    reduce_ranks<T, 2, NR>(d, q, tl, r, tk, room, ts, ld);
   }
-  if (t_out && blockIdx.y == 0)
-    for (int32_t k = threadIdx.x; k < tl.n * d.R; k += EXP_WAVES * 64) {
-      const int64_t at = (int64_t)rows[k / d.R] * d.R + k % d.R;
-      t_out[at] = t_sum(t, at, part, ks);
-    }
   __syncthreads();
-  if (tl.n <= 16) expand_tile<T, 1>(d, F, M, r, tl, op, rows, kind, base, ldb, Y, ldy);
-  else expand_tile<T, 4>(d, F, M, r, tl, op, rows, kind, base, ldb, Y, ldy);
+  if (role == 0 || role == split) {
+    if (q.t)
+      for (int32_t k = threadIdx.x; k < tl.n * d.R; k += WAVES * 64) {
+        const int32_t tok = k / d.R, j = k % d.R;
+        q.t[(int64_t)tk.row[tok] * d.R + j] = j < r ? ts[tok * ld + j] : 0.f;
+      }
+    if (q.pack && tl.l < d.L) write_pack<T>(q.pack, ti, NT, tl.n, r, s, ts, ld);
+  }
+  if (role >= split || !e.Y) return;
+  frag<bf16>* op = reinterpret_cast<frag<bf16>*>(room);
+  if constexpr (sizeof(T) == 2 && NR > 1) {
+    const int32_t rts = tl.n <= 16 ? 1 : 2;
+    for (int32_t k = threadIdx.x; k < (r + 31) / 32 * 128; k += WAVES * 64) {
+      const int32_t l = k & 63, i = (k >> 6) & 1, j0 = k / 128 * 32 + 8 * (l >> 4);
+      const int32_t tok = i * 16 + (l & 15);
+      if (i >= rts) continue;
+      float v[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] = j0 + x < r ? s * ts[tok * ld + j0 + x] : 0.f;
+      frag<bf16> hi, lo;
+      split_frag(v, hi, lo);
+      op[(k >> 6) * 128 + l] = hi;
+      op[(k >> 6) * 128 + 64 + l] = lo;
+    }
+    __syncthreads();
+  }
+  const T* F = e.F + (r > 0 ? (int64_t)tl.l * d.R * e.M : 0);
+  if (tl.n <= 16) expand_tile<T, 1, NR == 1>(e, F, tl, r, s, tk, ts, ld, op, role, split);
+  else expand_tile<T, 2, NR == 1>(e, F, tl, r, s, tk, ts, ld, op, role, split);
 }
 
 // --------------------------------------------------------------------- grad
-// The scaled t (or u) of a tile as the operand of the products over tokens:
-//   bf16  pack[tile][half][rank tile][hi, lo][lane] pieces of 8 tokens
-//   fp32  pack[tile][token][ranks up to a multiple of 16]
-// zero for tokens and ranks that are not there.  full[tile][half]: whether all
-// 32 tokens of the half count.
-template <typename T>
-__global__ __launch_bounds__(256) void k_lora_pack(lora_dev d, route_t p,
-                                                   const float* __restrict__ t0, int32_t ks0,
-                                                   void* __restrict__ pack0,
-                                                   const float* __restrict__ t1, int32_t ks1,
-                                                   void* __restrict__ pack1,
-                                                   int32_t* __restrict__ full) {
-  __shared__ int32_t rows[TILE];  // -1: does not count
-  const tile_t tl = tile_at(p, blockIdx.x);
-  if (tl.n <= 0 || tl.l >= d.L) return;
-  const bool first = blockIdx.y == 0;
-  const float* t = first ? t0 : t1;
-  const int32_t ks = first ? ks0 : ks1;
-  if (!t) return;
-  const int32_t r = rank_of(d, tl.l), NT = (d.R + 15) / 16;
-  const float s = scale_of(d, tl.l);
-  if (threadIdx.x < TILE) {
-    const int32_t tok = threadIdx.x;
-    int32_t row = -1;
-    if (tok < tl.n) {
-      row = row_at(p, tl.begin + tok);
-      if (!has_adapter(p, d.L, tl.l, row)) row = -1;
-    }
-    rows[tok] = row;
-    const uint64_t ok = __ballot(row >= 0);
-    if ((tok & 31) == 0)
-      full[blockIdx.x * 2 + tok / 32] = (uint32_t)(ok >> tok) == 0xFFFFFFFFu;
-  }
-  __syncthreads();
-  const int64_t part = (int64_t)p.Tn * d.R;
-  if constexpr (sizeof(T) == 2) {
-    frag<bf16>* o = reinterpret_cast<frag<bf16>*>(first ? pack0 : pack1) +
-                    (int64_t)blockIdx.x * 2 * NT * 2 * 64;
-    for (int32_t k = threadIdx.x; k < 2 * NT * 64; k += 256) {
-      const int32_t l = k & 63, x = k >> 6, j = x % NT * 16 + (l & 15), h = x / NT;
-      frag<bf16> hi{}, lo{};
-      if (j < r)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int32_t row = rows[h * 32 + 8 * (l >> 4) + q];
-          if (row >= 0)
-            split_bf16(s * t_sum(t, (int64_t)row * d.R + j, part, ks), hi.v[q], lo.v[q]);
-        }
-      o[(x * 2 + 0) * 64 + l] = hi;
-      o[(x * 2 + 1) * 64 + l] = lo;
-    }
-  } else {
-    float* o = reinterpret_cast<float*>(first ? pack0 : pack1) +
-               (int64_t)blockIdx.x * TILE * NT * 16;
-    for (int32_t k = threadIdx.x; k < TILE * NT * 16; k += 256) {
-      const int32_t tok = k / (NT * 16), j = k % (NT * 16), row = rows[tok];
-      o[k] = row >= 0 && j < r ? s * t_sum(t, (int64_t)row * d.R + j, part, ks) : 0.f;
-    }
-  }
-}
-
 template <typename T>
 struct grad_arg {
   const T* X;
@@ -667,73 +863,137 @@ struct grad_arg {
   float* part;  // [partial slots][R][K]
 };
 
-constexpr int GRAD_WAVES = 4;
+// dF = sum over the slot's tokens.  A wave has 16 pieces of columns and every
+// tw-th tile of its slot; the tokens are the contraction, so (bf16) the lane's
+// pieces of 8 tokens are transposed in registers into operands, two columns at
+// a time.  The rows of the next tile are on their way while one is summed.
+// tw > 1: the waves of a workgroup share the columns and their sums meet in
+// LDS.  tw = 1: each wave has its own columns.  grid: column blocks (of X, then
+// of dY) x slots x rank blocks of 16 * NR.
+constexpr int grad_waves(int NR) { return NR == 1 ? 8 : 4; }
 
-// grid: column blocks (of X, then of dY) x slots x rank blocks of 16 * NR.
-// A wave takes every fourth half tile of the slot: 32 tokens, 16 pieces of
-// columns; the tokens are the contraction, so (bf16) the lane's pieces of 8
-// tokens are transposed in registers into operands.  The waves' sums meet in
-// LDS.
+template <typename T, int NR, bool FULL>
+__device__ __forceinline__ void grad_sum(const route_t& p, const grad_arg<T>& q, const slot_t& sl,
+                                         int32_t NT, int32_t nt, int32_t rt0, int32_t col, int32_t h,
+                                         int32_t tw, const uint32_t* __restrict__ mask,
+                                         f4 (&acc)[NR][EL<T>]) {
+  const int l = lane_id(), c = l & 15, g = l >> 4;
+  const int32_t left = q.K - col;
+  const T* X = q.X + col;
+  auto fetch = [&](int32_t ti, frag<T> (&rows)[8]) {
+    const tile_t tl = tile_at(p, ti);
+    const uint32_t has = mask[ti];
+    int32_t row[8];
+    if (p.order) {  // `order` goes on for a tile past its last token
+      __builtin_memcpy(row, p.order + tl.begin + 8 * g, 32);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) row[k] = tl.begin + 8 * g + k;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t at = 8 * g + k < tl.n ? row[k] : 0;
+      rows[k] = load_frag(X + at * q.ldx, left, FULL);
+      if (has != ~0u) rows[k] = keep_if((has >> (8 * g + k)) & 1, rows[k]);
+    }
+  };
+  auto use = [&](int32_t ti, const frag<T> (&rows)[8]) {
+    if constexpr (sizeof(T) == 2) {
+      const frag<bf16>* o =
+          reinterpret_cast<const frag<bf16>*>(q.pack) + ((int64_t)ti * NT + rt0) * 128 + l;
+      frag<bf16> hi[NR], lo[NR];
+#pragma unroll
+      for (int j = 0; j < NR; ++j)
+        if (rt0 + j < nt) hi[j] = o[j * 128], lo[j] = o[j * 128 + 64];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        frag<bf16> a, b;  // columns e and e + 1
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t x = rows[2 * k].w[e / 2], y = rows[2 * k + 1].w[e / 2];
+          a.w[k] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+          b.w[k] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+        }
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+          if (rt0 + j >= nt) break;
+          acc[j][e] = mma(lo[j], a, mma(hi[j], a, acc[j][e]));
+          acc[j][e + 1] = mma(lo[j], b, mma(hi[j], b, acc[j][e + 1]));
+        }
+      }
+    } else {
+      const float* o =
+          reinterpret_cast<const float*>(q.pack) + ((int64_t)ti * TILE + 8 * g) * NT * 16 + c;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+          if (rt0 + j >= nt) break;
+          const float u = o[(k * NT + rt0 + j) * 16];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[j][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(u, at(rows[k], e), acc[j][e], 0, 0, 0);
+        }
+    }
+  };
+  if (h >= sl.n || rt0 >= nt) return;
+  frag<T> now[8], next[8];
+  fetch(sl.tile + h, now);
+  for (; h < sl.n; h += tw) {
+    if (h + tw < sl.n) fetch(sl.tile + h + tw, next);
+    use(sl.tile + h, now);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) now[k] = next[k];
+  }
+}
+
 template <typename T, int NR>
-__global__ __launch_bounds__(GRAD_WAVES * 64, 2) void k_lora_grad(lora_dev d, route_t p,
-                                                                  grad_arg<T> q0, grad_arg<T> q1,
-                                                                  int32_t blocks0,
-                                                                  const int32_t* __restrict__ full) {
-  constexpr int E = EL<T>, CW = 16 * E;
-  __shared__ float red[GRAD_WAVES][16 * CW];
-  const bool first = (int32_t)blockIdx.x < blocks0;
-  const grad_arg<T> q = first ? q0 : q1;
+__global__ __launch_bounds__(grad_waves(NR) * 64, NR == 1 ? 4 : 2) void k_lora_grad(
+    lora_dev d, route_t p, grad_arg<T> q0, grad_arg<T> q1, int32_t blocks0, int32_t blocks,
+    int32_t tw, const uint32_t* __restrict__ mask) {
+  constexpr int E = EL<T>, CW = 16 * E, GW = grad_waves(NR);
+  extern __shared__ char lds[];
+  const int w = threadIdx.x / 64, l = lane_id(), c = l & 15, g = l >> 4;
+  const int32_t b = tw == 1 ? (int32_t)blockIdx.x * GW + w : (int32_t)blockIdx.x;
+  if (b >= blocks) return;
+  const bool first = b < blocks0;
+  const grad_arg<T>& q = first ? q0 : q1;
   const slot_t sl = slot_at(p, blockIdx.y);
   if (sl.n <= 0) return;
-  const int w = threadIdx.x / 64, l = lane_id(), c = l & 15, g = l >> 4;
-  const int32_t c0 = ((int32_t)blockIdx.x - (first ? 0 : blocks0)) * CW, col = c0 + c * E;
-  const int32_t NT = (d.R + 15) / 16, rt0 = blockIdx.z * NR;
+  const int32_t c0 = (b - (first ? 0 : blocks0)) * CW, col = c0 + c * E;
+  const int32_t NT = (d.R + 15) / 16, rt0 = blockIdx.z * NR, nt = (rank_of(d, sl.l) + 15) / 16;
   f4 acc[NR][E];
 #pragma unroll
   for (int j = 0; j < NR; ++j)
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[j][e] = f4{0.f, 0.f, 0.f, 0.f};
-  for (int32_t h = w; h < sl.n * 2; h += GRAD_WAVES) {
-    const int32_t ti = sl.tile + h / 2, half = h & 1;
-    const tile_t tl = tile_at(p, ti);
-    if (half * 32 >= tl.n) continue;
-    const bool whole = full[ti * 2 + half] != 0;
-    frag<T> rows[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int32_t tok = half * 32 + 8 * g + k;
-      const int32_t row = row_at(p, tl.begin + min(tok, tl.n - 1));
-      int32_t n = q.K - col;
-      if (!whole && (tok >= tl.n || !has_adapter(p, d.L, sl.l, row))) n = 0;
-      rows[k] = load_frag(q.X + (int64_t)row * q.ldx + col, n);
-    }
-    if constexpr (sizeof(T) == 2) {
-      frag<T> cols[8];
-      transpose8(rows, cols);
-      const frag<bf16>* o = reinterpret_cast<const frag<bf16>*>(q.pack) +
-                            ((int64_t)(ti * 2 + half) * NT) * 2 * 64 + l;
-#pragma unroll
-      for (int j = 0; j < NR; ++j) {
-        if (rt0 + j >= NT) break;
-        const frag<T> hi = o[((rt0 + j) * 2 + 0) * 64], lo = o[((rt0 + j) * 2 + 1) * 64];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[j][e] = mma(lo, cols[e], mma(hi, cols[e], acc[j][e]));
-      }
+  const int32_t h = tw == 1 ? 0 : w;
+  if (c0 + CW <= q.K) grad_sum<T, NR, true>(p, q, sl, NT, nt, rt0, col, h, tw, mask, acc);
+  else grad_sum<T, NR, false>(p, q, sl, NT, nt, rt0, col, h, tw, mask, acc);
+  auto put = [&](int32_t rank, int32_t m, const float (&v)[E]) {
+    if (rank >= d.R || m >= q.K) return;
+    if (sl.part < 0) {
+      store_frag(q.dF + ((int64_t)sl.l * d.R + rank) * q.K + m, to_frag(v), q.K - m);
     } else {
-      const float* o = reinterpret_cast<const float*>(q.pack) +
-                       ((int64_t)ti * TILE + half * 32 + 8 * g) * NT * 16 + c;
+      float* o = q.part + ((int64_t)sl.part * d.R + rank) * q.K + m;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-#pragma unroll
-        for (int j = 0; j < NR; ++j) {
-          if (rt0 + j >= NT) break;
-          const float u = o[(k * NT + rt0 + j) * 16];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[j][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(u, rows[k].v[e], acc[j][e], 0, 0, 0);
-        }
+      for (int e = 0; e < E; e += 4)
+        store_frag(o + e, to_frag({v[e], v[e + 1], v[e + 2], v[e + 3]}), q.K - m - e);
     }
+  };
+  if (tw == 1) {
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = acc[j][e][k];
+        put((rt0 + j) * 16 + 4 * g + k, col, v);
+      }
+    return;
   }
+  float* red = reinterpret_cast<float*>(lds);  // [GW][16][CW]
 #pragma unroll
   for (int j = 0; j < NR; ++j) {
     if (rt0 + j >= NT) break;
@@ -741,26 +1001,18 @@ __global__ __launch_bounds__(GRAD_WAVES * 64, 2) void k_lora_grad(lora_dev d, ro
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int e = 0; e < E; ++e) red[w][(4 * g + k) * CW + c * E + e] = acc[j][e][k];
+      for (int e = 0; e < E; ++e) red[(w * 16 + 4 * g + k) * CW + c * E + e] = acc[j][e][k];
     __syncthreads();
-    const int32_t rank = (rt0 + j) * 16 + (int32_t)threadIdx.x / 16;
-    const int32_t at = threadIdx.x / 16 * CW + threadIdx.x % 16 * E, m = c0 + threadIdx.x % 16 * E;
-    if (rank < d.R && m < q.K) {
+    if (threadIdx.x < 256) {
+      const int32_t at = threadIdx.x / 16 * CW + threadIdx.x % 16 * E;
       float v[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        v[e] = (red[0][at + e] + red[1][at + e]) + (red[2][at + e] + red[3][at + e]);
-      if (sl.part < 0) {
-        frag<T> out;
+      for (int e = 0; e < E; ++e) {
+        v[e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) out.v[e] = elem<T>::from_f(v[e]);
-        store_frag(q.dF + ((int64_t)sl.l * d.R + rank) * q.K + m, out, q.K - m);
-      } else {
-        float* o = q.part + ((int64_t)sl.part * d.R + rank) * q.K + m;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (m + e < q.K) o[e] = v[e];
+        for (int m = 0; m < GW; ++m) v[e] += red[m * 16 * CW + at + e];
       }
+      put((rt0 + j) * 16 + (int32_t)threadIdx.x / 16, c0 + threadIdx.x % 16 * E, v);
     }
   }
 }
@@ -777,16 +1029,20 @@ __global__ __launch_bounds__(256) void k_lora_join(lora_dev d, route_t p, int32_
   const int32_t m = (((int32_t)blockIdx.y - (first ? 0 : blocks0)) * 256 + threadIdx.x) * 4;
   const join_t jn = p.order ? p.join[l] : join_t{slots, 0};
   if (m >= q.K || jn.slots == 1) return;
-  const int32_t n = min(4, q.K - m);
+  const int32_t n = q.K - m;
   float v[4] = {};
   const float* o = q.part + ((int64_t)jn.part * d.R + j) * q.K + m;
-  for (int32_t s = 0; s < jn.slots; ++s, o += (int64_t)d.R * q.K)
+  const int64_t next = (int64_t)d.R * q.K;
+#pragma unroll 8
+  for (int32_t s = 0; s < jn.slots; ++s) {
+    const frag<float> f = load_frag(o + s * next, n);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < n) v[e] += o[e];
+    for (int e = 0; e < 4; ++e) v[e] += at(f, e);
+  }
+  T* out = q.dF + ((int64_t)l * d.R + j) * q.K + m;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    if (e < n) q.dF[((int64_t)l * d.R + j) * q.K + m + e] = elem<T>::from_f(v[e]);
+    if (e < n) out[e] = elem<T>::from_f(v[e]);
 }
 
 // --------------------------------------------------------------------- host
@@ -796,7 +1052,7 @@ snack_status check_lora(const snack_lora* p, snack_dtype dt, int32_t T) {
   if (p->M < 1 || p->K < 1 || p->L < 1 || p->L > MAX_ADAPTERS || p->R < 1 || p->R > MAX_RANK ||
       T < 0)
     return SNACK_E_SHAPE;
-  if (T > INT32_MAX - TILE || p->M > MAX_FEATURES || p->K > MAX_FEATURES) return SNACK_E_OVERFLOW;
+  if (T > INT32_MAX - 64 || p->M > MAX_FEATURES || p->K > MAX_FEATURES) return SNACK_E_OVERFLOW;
   return SNACK_OK;
 }
 
@@ -804,35 +1060,34 @@ snack_status check_lora(const snack_lora* p, snack_dtype dt, int32_t T) {
 constexpr int32_t FEW_TOKENS = 64;
 
 struct plan_t {
+  int32_t whole;  // tiles if all tokens had one adapter
   int32_t tiles, slots, slot_tiles, part_slots, blocksA, blocksB, NT;
-  int32_t ksK, ksM;  // parts of the reductions over K and over M
-  size_t order, tile, slot, join, count, t, u, pack_t, pack_u, full, partA, partB, total;
+  int32_t tw;     // waves that share a slot's tokens: 1 or all of a workgroup
+  size_t order, tile, slot, join, count, pack_t, pack_u, mask, partA, partB, total;
 };
-
-int32_t parts_of(int32_t tiles, int32_t K, int32_t step) {
-  const int64_t want = cdiv(256, std::max(tiles, 1)), most = std::max<int64_t>(1, K / (RED_WAVES * 2 * step));
-  return (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, most, 8}));
-}
 
 plan_t plan_of(const snack_lora* p, snack_dtype dt, int32_t T, bool backward) {
   plan_t w{};
   const int32_t e = dt == SNACK_BF16 ? 8 : 4;
-  const int32_t whole = (int32_t)cdiv(T, TILE);
-  w.tiles = p->L == 1 ? whole : (int32_t)std::min<int64_t>(T, (int64_t)T / TILE + p->L + 1);
-  w.ksK = parts_of(whole, p->K, 4 * e);
-  w.ksM = parts_of(whole, p->M, 4 * e);
+  w.whole = (int32_t)cdiv(T, TILE);
+  w.tiles = p->L == 1 ? w.whole : (int32_t)std::min<int64_t>(T, (int64_t)T / TILE + p->L + 1);
   w.NT = (int32_t)cdiv(p->R, 16);
   w.blocksA = (int32_t)cdiv(p->K, 16 * e);
   w.blocksB = (int32_t)cdiv(p->M, 16 * e);
-  // slots: enough workgroups to fill the GPU, each of at least 4 tiles
-  const int64_t runs = std::max<int64_t>(1, cdiv(512, w.blocksA + w.blocksB));
-  w.slot_tiles = (int32_t)std::max<int64_t>(4, cdiv(whole, runs));
-  w.slots = p->L == 1 ? (int32_t)cdiv(whole, w.slot_tiles)
-                      : (int32_t)std::min<int64_t>(w.tiles, whole / w.slot_tiles + p->L);
+  // One wave sums a slot where adapters and columns make waves enough;
+  // elsewhere the waves of a workgroup share it.
+  const int32_t gw = grad_waves(w.NT);
+  const int64_t blocks = w.blocksA + w.blocksB;
+  w.tw = blocks * std::min(p->L, w.whole) >= 2048 ? 1 : gw;
+  const int64_t runs = std::max<int64_t>(1, cdiv(4096 / gw, blocks));
+  w.slot_tiles = w.tw == 1 ? (int32_t)std::max<int64_t>(16, cdiv(w.whole, 32))
+                           : (int32_t)std::max<int64_t>(gw, cdiv(w.whole, runs));
+  w.slots = p->L == 1 ? (int32_t)cdiv(w.whole, w.slot_tiles)
+                      : (int32_t)std::min<int64_t>(w.tiles, w.whole / w.slot_tiles + p->L);
   // an adapter with several slots has more than slot_tiles tiles, so its
   // slots are at most three times its share of the tokens
   w.part_slots = p->L == 1 ? w.slots
-                           : (int32_t)std::min<int64_t>(w.slots, 3 * cdiv(whole, w.slot_tiles));
+                           : (int32_t)std::min<int64_t>(w.slots, 3 * cdiv(w.whole, w.slot_tiles));
   size_t o = 0;
   auto take = [&](size_t b) {
     const size_t at = o;
@@ -840,20 +1095,17 @@ plan_t plan_of(const snack_lora* p, snack_dtype dt, int32_t T, bool backward) {
     return at;
   };
   if (p->L > 1) {
-    w.order = take(4 * (size_t)T);
+    w.order = take(4 * ((size_t)T + TILE));
     w.tile = take(sizeof(tile_t) * (size_t)w.tiles);
     w.slot = take(sizeof(slot_t) * (size_t)w.slots);
     w.join = take(sizeof(join_t) * (size_t)p->L);
     w.count = take(8);
   }
-  const size_t tr = 4 * (size_t)T * p->R;
-  w.t = take(tr * w.ksK);
   if (backward) {
-    w.u = take(tr * w.ksM);
     const size_t pk = 4 * (size_t)w.tiles * TILE * w.NT * 16;
     w.pack_t = take(pk);
     w.pack_u = take(pk);
-    w.full = take(8 * (size_t)w.tiles);
+    w.mask = take(4 * (size_t)w.tiles);
     w.partA = take(4 * (size_t)w.part_slots * p->R * p->K);
     w.partB = take(4 * (size_t)w.part_slots * p->R * p->M);
   }
@@ -870,33 +1122,39 @@ route_t launch_route(const snack_lora* p, const plan_t& w, const int32_t* ids, i
   r.slot = (const slot_t*)(ws + w.slot);
   r.join = (const join_t*)(ws + w.join);
   r.count = (const int32_t*)(ws + w.count);
-  const int32_t nw = std::max(1, std::min(16, 15360 / (p->L + 1)));
-  hipLaunchKernelGGL(k_lora_route, dim3(1), dim3(1024), 4 * (size_t)nw * (p->L + 1), s, ids, T,
+  const int32_t G = p->L + 1, nw = std::max(1, std::min(16, 15360 / G));
+  hipLaunchKernelGGL(k_lora_route, dim3(1), dim3(1024), 4 * ((size_t)(nw + 2) * G + 2), s, ids, T,
                      p->L, nw, w.slot_tiles, (int32_t*)r.order, (tile_t*)r.tile, (slot_t*)r.slot,
                      (join_t*)r.join, (int32_t*)r.count);
   return r;
 }
 
+// a with the expansion e (split workgroups a tile), b if `both`.
 template <typename T>
-void launch_reduce(const lora_dev& d, const route_t& r, const plan_t& w, const reduce_arg<T>& q0,
-                   const reduce_arg<T>& q1, int32_t problems, hipStream_t s) {
-  const int32_t nr = w.NT >= 3 ? 4 : w.NT, rbs = (int32_t)cdiv(w.NT, nr);
-  const dim3 grid(w.tiles, problems > 1 ? std::max(q0.ks, q1.ks) : q0.ks, rbs * problems);
+void launch_apply(const lora_dev& d, const route_t& r, const plan_t& w, bool with_a,
+                  const reduce_arg<T>& a, bool with_b, const reduce_arg<T>& b,
+                  const expand_arg<T>& e, uint32_t* mask, hipStream_t s) {
+  // Workgroups of a tile: enough to have two on every CU, each with columns
+  // for all its waves.
+  int32_t split = 0;
+  if (with_a) {
+    const int32_t tiles = r.order ? w.whole + std::min(d.L, r.Tn) / 2 : w.whole;
+    split = e.Y ? (int32_t)std::max<int64_t>(1, std::min<int64_t>(512 / std::max(tiles, 1),
+                                                                  cdiv(e.M, 16 * EL<T> * WAVES)))
+                : 1;
+  }
+  const int32_t roles = split + (with_b ? 1 : 0), R16 = w.NT * 16;
+  const size_t ts = 4 * ((size_t)(TILE * (R16 + 1) + 3) / 4 * 4);
+  const int32_t nr = w.NT >= 3 ? 4 : w.NT;
+  const size_t red = std::max<size_t>((size_t)WAVES * (2 + nr) * 2048, (size_t)cdiv(d.R, 32) * 4096);
+  const dim3 grid((unsigned)(NUM_XCD * cdiv(w.tiles, NUM_XCD) * roles));
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(RED_WAVES * 64), 0, s, d, r, q0, q1, rbs);
+    hipLaunchKernelGGL(kernel, grid, dim3(WAVES * 64), ts + red, s, d, r, a, b, e, split, roles,
+                       mask);
   };
-  if (nr == 1) go(k_lora_reduce<T, 1>);
-  else if (nr == 2) go(k_lora_reduce<T, 2>);
-  else go(k_lora_reduce<T, 4>);
-}
-
-template <typename T>
-void launch_expand(const lora_dev& d, const route_t& r, const plan_t& w, const void* F, int32_t M,
-                   const float* t, int32_t ks, float* t_out, const void* base, int64_t ldb,
-                   void* Y, int64_t ldy, hipStream_t s) {
-  const dim3 grid(w.tiles, (unsigned)cdiv(M, EXP_WAVES * 16 * EL<T>));
-  hipLaunchKernelGGL(k_lora_expand<T>, grid, dim3(EXP_WAVES * 64), expand_lds<T>::bytes(d.R), s, d,
-                     r, (const T*)F, M, t, ks, t_out, (const T*)base, ldb, (T*)Y, ldy);
+  if (w.NT == 1) go(k_lora_apply<T, 1>);
+  else if (w.NT == 2) go(k_lora_apply<T, 2>);
+  else go(k_lora_apply<T, 4>);
 }
 
 template <typename T>
@@ -904,18 +1162,19 @@ void run_fwd(const snack_lora* p, const lora_dev& d, const int32_t* ids, int32_t
              int64_t ldx, const void* base, int64_t ldb, void* Y, int64_t ldy, float* t, char* ws,
              snack_dtype dt, hipStream_t s) {
   if (Tn <= FEW_TOKENS) {
-    const dim3 grid((unsigned)cdiv(p->M, 64 * EL<T>), Tn);
-    hipLaunchKernelGGL((k_lora_few<T, 3>), grid, dim3(FEW_WAVES * 64), 0, s, d, ids, (const T*)p->A,
-                       p->K, (const T*)X, ldx, (const T*)p->B, p->M, (const T*)base, ldb, (T*)Y,
-                       ldy, t);
+    const int32_t blocks = (int32_t)cdiv(p->M, 64 * EL<T>);
+    const int32_t split = std::max(1, std::min(blocks, 512 / Tn));
+    const int32_t rows = Tn < NUM_XCD ? Tn : (int32_t)(cdiv(Tn, NUM_XCD) * NUM_XCD);
+    hipLaunchKernelGGL(k_lora_few<T>, dim3((unsigned)(rows * split)), dim3(FEW_WAVES * 64), 0, s, d,
+                       ids, Tn, split, (const T*)p->A, p->K, (const T*)X, ldx, (const T*)p->B, p->M,
+                       (const T*)base, ldb, (T*)Y, ldy, t);
     return;
   }
   const plan_t w = plan_of(p, dt, Tn, false);
   const route_t r = launch_route(p, w, ids, Tn, ws, s);
-  float* parts = (float*)(ws + w.t);
-  const reduce_arg<T> q{(const T*)p->A, (const T*)X, ldx, p->K, w.ksK, parts};
-  launch_reduce<T>(d, r, w, q, q, 1, s);
-  launch_expand<T>(d, r, w, p->B, p->M, parts, w.ksK, t, base, ldb, Y, ldy, s);
+  const reduce_arg<T> a{(const T*)p->A, (const T*)X, ldx, p->K, nullptr, t, nullptr};
+  const expand_arg<T> e{(const T*)p->B, p->M, (const T*)base, ldb, (T*)Y, ldy};
+  launch_apply<T>(d, r, w, true, a, false, a, e, nullptr, s);
 }
 
 template <typename T>
@@ -925,31 +1184,28 @@ void run_bwd(const snack_lora* p, const lora_dev& d, const int32_t* ids, const f
              snack_dtype dt, hipStream_t s) {
   const plan_t w = plan_of(p, dt, Tn, true);
   route_t r{};
-  float *tp = (float*)(ws + w.t), *up = (float*)(ws + w.u);
-  if (Tn > 0) {
+  uint32_t* mask = (uint32_t*)(ws + w.mask);
+  if (Tn > 0 && (dX || dA || dB)) {
     r = launch_route(p, w, ids, Tn, ws, s);
-    const reduce_arg<T> qt{(const T*)p->A, (const T*)X, ldx, p->K, w.ksK, tp};
-    const reduce_arg<T> qu{(const T*)p->B, (const T*)dY, lddy, p->M, w.ksM, up};
-    const bool need_u = dX || dA, need_t = dB && !t;
-    if (need_u && need_t) launch_reduce<T>(d, r, w, qu, qt, 2, s);
-    else if (need_u) launch_reduce<T>(d, r, w, qu, qu, 1, s);
-    else if (need_t) launch_reduce<T>(d, r, w, qt, qt, 1, s);
-    if (dX) launch_expand<T>(d, r, w, p->A, p->K, up, w.ksM, nullptr, base, ldb, dX, lddx, s);
+    const reduce_arg<T> u{(const T*)p->B, (const T*)dY, lddy, p->M, nullptr, nullptr,
+                          dA ? ws + w.pack_u : nullptr};
+    const reduce_arg<T> v{(const T*)p->A, (const T*)X, ldx, p->K, t, nullptr, ws + w.pack_t};
+    const expand_arg<T> e{(const T*)p->A, p->K, (const T*)base, ldb, (T*)dX, lddx};
+    launch_apply<T>(d, r, w, dX || dA, u, dB != nullptr, v, e, mask, s);
   }
   if (!dA && !dB) return;
-  int32_t* full = (int32_t*)(ws + w.full);
   grad_arg<T> qa{(const T*)X, ldx, p->K, ws + w.pack_u, (T*)dA, (float*)(ws + w.partA)};
   grad_arg<T> qb{(const T*)dY, lddy, p->M, ws + w.pack_t, (T*)dB, (float*)(ws + w.partB)};
   const int32_t na = dA ? w.blocksA : 0, nb = dB ? w.blocksB : 0;
   if (Tn > 0) {
-    const float* t_src = dB ? (t ? t : tp) : nullptr;
-    hipLaunchKernelGGL(k_lora_pack<T>, dim3(w.tiles, 2), dim3(256), 0, s, d, r,
-                       dA ? (const float*)up : nullptr, w.ksM, (void*)(ws + w.pack_u), t_src,
-                       t ? 1 : w.ksK, (void*)(ws + w.pack_t), full);
     const int32_t nr = w.NT >= 3 ? 4 : w.NT;
-    const dim3 grid(na + nb, w.slots, (unsigned)cdiv(w.NT, nr));
+    const int32_t gw = grad_waves(nr);
+    const dim3 grid((unsigned)(w.tw == 1 ? cdiv(na + nb, gw) : na + nb), w.slots,
+                    (unsigned)cdiv(w.NT, nr));
+    const size_t lds = w.tw == 1 ? 0 : 4 * (size_t)gw * 16 * 16 * EL<T>;
     auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, grid, dim3(GRAD_WAVES * 64), 0, s, d, r, qa, qb, na, full);
+      hipLaunchKernelGGL(kernel, grid, dim3(gw * 64), lds, s, d, r, qa, qb, na, na + nb, w.tw,
+                         mask);
     };
     if (nr == 1) go(k_lora_grad<T, 1>);
     else if (nr == 2) go(k_lora_grad<T, 2>);
