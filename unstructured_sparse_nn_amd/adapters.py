@@ -11,58 +11,7 @@ from __future__ import annotations
 
 import torch
 
-from . import binding as _b
-
-_TYPES = {torch.float32: _b.F32, torch.bfloat16: _b.BF16}
-
-
-def _rows(x, name, T, n, like, must=False):
-    """x as a T x n matrix with contiguous rows, and its row stride."""
-    if x.dtype is not like.dtype or x.device != like.device:
-        raise TypeError(f"{name}: expected {like.dtype} on {like.device}, "
-                        f"got {x.dtype} on {x.device}")
-    if x.dim() != 2 or x.shape[0] != T or x.shape[1] != n:
-        raise ValueError(f"{name}: expected shape ({T}, {n}), got {tuple(x.shape)}")
-    ld, inner = x.stride()
-    if (inner != 1 and n > 1) or (ld < n and T > 1):
-        if must:
-            raise ValueError(f"{name}: rows must be contiguous and must not overlap")
-        x = x.contiguous()
-        ld = n
-    return x, ld if T > 1 else n
-
-
-def _bank(x, ids, A, B, scale, ranks, T):
-    """The argument struct of the adapters, after checks."""
-    if A.dim() != 3 or B.dim() != 3 or A.shape[:2] != B.shape[:2]:
-        raise ValueError(f"A (L, R, K) and B (L, R, M) expected, got {tuple(A.shape)} and "
-                         f"{tuple(B.shape)}")
-    L, R, K = A.shape
-    if x.dtype not in _TYPES:
-        raise TypeError(f"unsupported dtype {x.dtype}")
-    if not x.is_cuda:
-        raise TypeError("the adapters run on the GPU only")
-    if A.dtype is not x.dtype or B.dtype is not x.dtype or A.device != x.device \
-            or B.device != x.device:
-        raise TypeError("A and B must have the activations' dtype and device")
-    if not (A.is_contiguous() and B.is_contiguous()):
-        raise ValueError("A and B must be contiguous")
-    if ids.dtype is not torch.int32 or ids.device != x.device or ids.dim() != 1 \
-            or ids.shape[0] != T or not ids.is_contiguous():
-        raise ValueError(f"ids: expected a contiguous int32 tensor of {T} on {x.device}")
-    if scale is not None and (scale.dtype is not torch.float32 or scale.numel() != L
-                              or scale.device != x.device or not scale.is_contiguous()):
-        raise ValueError(f"scale: expected {L} contiguous float32 on {x.device}")
-    if ranks is not None and (ranks.dtype is not torch.int32 or ranks.numel() != L
-                              or ranks.device != x.device or not ranks.is_contiguous()):
-        raise ValueError(f"ranks: expected {L} contiguous int32 on {x.device}")
-    return _b.snack_lora(A, B, B.shape[2], K, L, R, scale, ranks)
-
-
-def _check_t(t, T, R, like):
-    if t.dtype is not torch.float32 or t.shape != (T, R) or not t.is_contiguous() \
-            or t.device != like.device:
-        raise ValueError(f"t: expected a contiguous float32 ({T}, {R}) tensor on {like.device}")
+from .native import calls as _calls
 
 
 def lora_fwd(x, ids, A, B, scale=None, ranks=None, base=None, out=None, t=None):
@@ -71,27 +20,7 @@ def lora_fwd(x, ids, A, B, scale=None, ranks=None, base=None, out=None, t=None):
     x (T, K); base (T, M) or None; out (T, M), may be base; t (T, R) float32
     receives ``x @ A[a].T`` for :func:`lora_bwd`.  Rows of x, base and out may
     be strided."""
-    if x.dim() != 2:
-        raise ValueError(f"x: expected a matrix, got {tuple(x.shape)}")
-    T = x.shape[0]
-    bank = _bank(x, ids, A, B, scale, ranks, T)
-    M = bank.M
-    x, ldx = _rows(x, "x", T, bank.K, x)
-    ldb = M
-    if out is None:
-        out = torch.empty(T, M, dtype=x.dtype, device=x.device)
-        ldy = M
-    else:
-        _, ldy = _rows(out, "out", T, M, x, must=True)
-    if base is not None:
-        base, ldb = _rows(base, "base", T, M, x)
-    if t is not None:
-        _check_t(t, T, bank.R, x)
-    dt = _TYPES[x.dtype]
-    n = _b.snack_lora_workspace(bank, dt, T)
-    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-    _b.snack_lora_fwd(bank, ids, T, x, ldx, base, ldb, out, ldy, t, ws, ws_bytes=n, dtype=dt)
-    return out
+    return _calls.lora_fwd(x, ids, A, B, scale, ranks, base, out, t)
 
 
 def lora_bwd(dy, x, ids, A, B, scale=None, ranks=None, t=None, base=None, out=None,
@@ -101,34 +30,7 @@ def lora_bwd(dy, x, ids, A, B, scale=None, ranks=None, t=None, base=None, out=No
     t: what the forward stored (computed again without it).  base (T, K): the
     shared projection's input gradient, added to dx.  out (T, K) receives dx
     and may be base.  want: which of the three to compute (None for others)."""
-    if x.dim() != 2:
-        raise ValueError(f"x: expected a matrix, got {tuple(x.shape)}")
-    T = x.shape[0]
-    bank = _bank(x, ids, A, B, scale, ranks, T)
-    K, M = bank.K, bank.M
-    x, ldx = _rows(x, "x", T, K, x)
-    dy, lddy = _rows(dy, "dy", T, M, x)
-    if t is not None:
-        _check_t(t, T, bank.R, x)
-    dx, lddx, ldb = None, K, K
-    if want[0]:
-        if out is None:
-            dx = torch.empty(T, K, dtype=x.dtype, device=x.device)
-        else:
-            dx = out
-            _, lddx = _rows(out, "out", T, K, x, must=True)
-        if base is not None:
-            base, ldb = _rows(base, "base", T, K, x)
-    else:
-        base = None
-    dA = torch.empty_like(A) if want[1] else None
-    dB = torch.empty_like(B) if want[2] else None
-    dt = _TYPES[x.dtype]
-    n = _b.snack_lora_workspace(bank, dt, T, True)
-    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-    _b.snack_lora_bwd(bank, ids, t, T, x, ldx, dy, lddy, base, ldb, dx, lddx, dA, dB, ws,
-                      ws_bytes=n, dtype=dt)
-    return dx, dA, dB
+    return _calls.lora_bwd(dy, x, ids, A, B, scale, ranks, t, base, out, *want)
 
 
 class _LoraFn(torch.autograd.Function):

@@ -1,7 +1,8 @@
 """Build the HIP library (libsnack.so) for gfx950 with hipcc, in-tree.
 
 Every source under csrc/ is compiled to an object in parallel, then linked
-into ``unstructured_sparse_nn_amd/libsnack.so``.  Packed fp32 instructions
+into ``unstructured_sparse_nn_amd/libsnack.so``; the torch-facing calls become the
+extension module ``_torch_calls.so``.  Packed fp32 instructions
 are disabled for all device code (``-target-feature -packed-fp32-ops``).
 """
 from __future__ import annotations
@@ -47,6 +48,30 @@ def _link(objs, lib: str) -> None:
     os.replace(tmp, lib)
 
 
+# torch_calls.cpp: a Python extension module on torch's headers, which reaches
+# the HIP library through addresses that it is given.
+CALLS = os.path.join(HERE, "_torch_calls.so")
+
+
+def _build_calls() -> str:
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = CALLS + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+           "-D__HIP_PLATFORM_AMD__", "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"),
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(HERE, "..", "include"),
+           os.path.join(CSRC, "torch_calls.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for torch_calls.cpp:\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 # The debug build: the same library with SNACK_DEBUG_CHECKS defined in
 # api.hip, whose product entry points then check every plan array and COO
 # index on the device (within the arrays' sizes) before launching, and
@@ -57,7 +82,7 @@ DEBUG_LIB = os.path.join(HERE, "libsnack_debug.so")
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    jobs = min(len(SOURCES) + 1, int(os.environ.get("MAX_JOBS", "8")))
+    jobs = min(len(SOURCES) + 2, int(os.environ.get("MAX_JOBS", "8")))
 
     def debug_api():
         obj = os.path.join(BUILD, "api_debug.o")
@@ -70,12 +95,14 @@ def build(verbose: bool = False) -> str:
 
     with ThreadPoolExecutor(jobs) as ex:
         dbg = ex.submit(debug_api)
+        calls = ex.submit(_build_calls)
         objs = list(ex.map(_compile, SOURCES))
         dbg_obj = dbg.result()
+        calls.result()
     _link(objs, LIB)
     _link([dbg_obj if os.path.basename(o) == "api.o" else o for o in objs], DEBUG_LIB)
     if verbose:
-        print(f"built {LIB} and {DEBUG_LIB}", file=sys.stderr)
+        print(f"built {LIB}, {DEBUG_LIB} and {CALLS}", file=sys.stderr)
     return LIB
 
 
