@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import torch
 
-from .native import calls as _calls
+from .native import calls
 
 
 def lora_fwd(x, ids, A, B, scale=None, ranks=None, base=None, out=None, t=None):
@@ -20,7 +20,7 @@ def lora_fwd(x, ids, A, B, scale=None, ranks=None, base=None, out=None, t=None):
     x (T, K); base (T, M) or None; out (T, M), may be base; t (T, R) float32
     receives ``x @ A[a].T`` for :func:`lora_bwd`.  Rows of x, base and out may
     be strided."""
-    return _calls.lora_fwd(x, ids, A, B, scale, ranks, base, out, t)
+    return calls().lora_fwd(x, ids, A, B, scale, ranks, base, out, t)
 
 
 def lora_bwd(dy, x, ids, A, B, scale=None, ranks=None, t=None, base=None, out=None,
@@ -30,7 +30,7 @@ def lora_bwd(dy, x, ids, A, B, scale=None, ranks=None, t=None, base=None, out=No
     t: what the forward stored (computed again without it).  base (T, K): the
     shared projection's input gradient, added to dx.  out (T, K) receives dx
     and may be base.  want: which of the three to compute (None for others)."""
-    return _calls.lora_bwd(dy, x, ids, A, B, scale, ranks, t, base, out, *want)
+    return calls().lora_bwd(dy, x, ids, A, B, scale, ranks, t, base, out, *want)
 
 
 class _LoraFn(torch.autograd.Function):

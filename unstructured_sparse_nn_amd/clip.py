@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import torch
 
-from .native import calls as _calls
+from .native import calls
 
 
 def grad_norm(grads):
@@ -17,7 +17,7 @@ def grad_norm(grads):
     grads = list(grads)
     if not grads:
         return torch.zeros(())
-    return _calls.clip(grads, None, None, 0.0)
+    return calls().clip(grads, None, None, 0.0)
 
 
 def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None):
@@ -30,7 +30,7 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None):
         if outs:
             raise ValueError(f"0 gradients but {len(outs)} outputs")
         return torch.zeros(())
-    return _calls.clip(grads, outs, max_norm, eps)
+    return calls().clip(grads, outs, max_norm, eps)
 
 
 def clip_grad_norm_(parameters, max_norm: float, eps: float = 1e-6):
