@@ -45,6 +45,11 @@ __device__ __forceinline__ float scale_of(const lora_dev& d, int32_t l) {
   return d.scale ? d.scale[l] : 1.f;
 }
 
+// The wave's number in its workgroup, known to be the same for all lanes.
+__device__ __forceinline__ int wave_id() {
+  return __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
+}
+
 // ------------------------------------------------------------- 16-byte pieces
 // Rows start at any element, so pieces are loaded and stored without an
 // alignment claim; the hardware takes a 16-byte access at any address.
@@ -62,28 +67,46 @@ __device__ __forceinline__ frag<T> load_frag(const T* p) {
   __builtin_memcpy(&f, p, 16);
   return f;
 }
-// The first n elements at p (n may be <= 0 or past a piece), zeros after them.
+__device__ __forceinline__ uint32_t pick(bool first, uint32_t a, uint32_t b) { return first ? a : b; }
+
+// f moved down by sh elements, zeros behind.
+__device__ __forceinline__ frag<bf16> move_down(const frag<bf16>& f, int32_t sh) {
+  const uint32_t a0 = pick(sh & 1, __builtin_amdgcn_alignbit(f.w[1], f.w[0], 16), f.w[0]),
+                 a1 = pick(sh & 1, __builtin_amdgcn_alignbit(f.w[2], f.w[1], 16), f.w[1]),
+                 a2 = pick(sh & 1, __builtin_amdgcn_alignbit(f.w[3], f.w[2], 16), f.w[2]),
+                 a3 = pick(sh & 1, f.w[3] >> 16, f.w[3]);
+  const uint32_t b0 = pick(sh & 2, a1, a0), b1 = pick(sh & 2, a2, a1), b2 = pick(sh & 2, a3, a2),
+                 b3 = pick(sh & 2, 0, a3);
+  const bool none = sh >= 8;
+  return frag<bf16>{{pick(none, 0, pick(sh & 4, b2, b0)), pick(none, 0, pick(sh & 4, b3, b1)),
+                     pick(none || (sh & 4), 0, b2), pick(none || (sh & 4), 0, b3)}};
+}
+__device__ __forceinline__ frag<float> move_down(const frag<float>& f, int32_t sh) {
+  const uint32_t b0 = pick(sh & 1, f.w[1], f.w[0]), b1 = pick(sh & 1, f.w[2], f.w[1]),
+                 b2 = pick(sh & 1, f.w[3], f.w[2]), b3 = pick(sh & 1, 0, f.w[3]);
+  const bool none = sh >= 4;
+  return frag<float>{{pick(none, 0, pick(sh & 2, b2, b0)), pick(none, 0, pick(sh & 2, b3, b1)),
+                      pick(none || (sh & 2), 0, b2), pick(none || (sh & 2), 0, b3)}};
+}
+// The piece at p of a row of `row` elements, of which n are left there (n may
+// be <= 0), zeros after them.  One load: a piece that ends early is taken from
+// the row's last EL elements.
 template <typename T>
-__device__ __forceinline__ frag<T> load_frag(const T* p, int32_t n) {
-  if (n >= EL<T>) return load_frag(p);
+__device__ __forceinline__ frag<T> load_frag(const T* p, int32_t n, int64_t row) {
+  if (row >= EL<T>) {
+    const int32_t sh = max(EL<T> - n, 0);
+    return move_down(load_frag(p - sh), sh);
+  }
   frag<T> f{};
-  if (n > 0) {
-    uint32_t v[EL<T> - 1];
+#pragma unroll 1
+  for (int e = (int)row - 1; e >= 0; --e) {  // the row is shorter than a piece: p is its start
+    uint32_t v = 0;
+    if (e < n) __builtin_memcpy(&v, p + e, sizeof(T));
 #pragma unroll
-    for (int e = 0; e < EL<T> - 1; ++e) {
-      v[e] = 0;
-      __builtin_memcpy(&v[e], p + min(e, n - 1), sizeof(T));
-    }
-#pragma unroll
-    for (int e = 0; e < EL<T> - 1; ++e)
-      if (e < n) f.w[e * sizeof(T) / 4] |= v[e] << (8 * (e * sizeof(T) % 4));
+    for (int q = 0; q < 4; ++q)
+      if (e * (int)sizeof(T) / 4 == q) f.w[q] |= v << (8 * (e * sizeof(T) % 4));
   }
   return f;
-}
-// The same where `full` says, for the whole wave, that no piece ends early.
-template <typename T>
-__device__ __forceinline__ frag<T> load_frag(const T* p, int32_t n, bool full) {
-  return full ? load_frag(p) : load_frag(p, n);
 }
 template <typename T>
 __device__ __forceinline__ void store_frag(T* p, const frag<T>& f, int32_t n) {
@@ -202,9 +225,9 @@ __device__ __forceinline__ void few_dots(const T* x, const T* __restrict__ F, in
     for (int q = 0; q < RW; ++q) acc[q] = dot_frag(xv, load_frag(F + q * next + k), acc[q]);
   }
   if (k < K) {
-    const frag<T> xv = load_frag(x + k, K - k);
+    const frag<T> xv = load_frag(x + k, K - k, K);
 #pragma unroll
-    for (int q = 0; q < RW; ++q) acc[q] = dot_frag(xv, load_frag(F + q * next + k, K - k), acc[q]);
+    for (int q = 0; q < RW; ++q) acc[q] = dot_frag(xv, load_frag(F + q * next + k, K - k, K), acc[q]);
   }
 #pragma unroll
   for (int q = 0; q < RW; ++q) {
@@ -232,7 +255,7 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void k_lora_few(
   }
   if (i >= Tn) return;
   const int32_t a = ids[i];
-  const int w = threadIdx.x / 64, l = lane_id();
+  const int w = wave_id(), l = lane_id();
   const int32_t r = a >= 0 && a < d.L ? rank_of(d, a) : 0;
   const float s = a >= d.L ? __builtin_nanf("") : r > 0 ? scale_of(d, a) : 1.f;
   const int64_t row0 = r > 0 ? (int64_t)a * d.R : 0;
@@ -240,7 +263,7 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void k_lora_few(
   const int c = threadIdx.x;
   frag<T> b0{};
   T base0 = 0;
-  if (w < r) b0 = load_frag(Bw + (int64_t)cb * C + l * E, M - cb * C - l * E);
+  if (w < r) b0 = load_frag(Bw + cb * C + l * E, M - cb * C - l * E, M);
   if (base && c < C && cb * C + c < M) base0 = base[i * ldb + cb * C + c];
   const T* x = X + i * ldx;
   for (int32_t j = w; j < r;) {
@@ -262,7 +285,7 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void k_lora_few(
     const int32_t col = cb * C + l * E;
     float y[E] = {};
     if (!first) {
-      if (w < r) b0 = load_frag(Bw + col, M - col);
+      if (w < r) b0 = load_frag(Bw + col, M - col, M);
       if (base && c < C && cb * C + c < M) base0 = base[i * ldb + cb * C + c];
     }
     if (w < r)
@@ -270,7 +293,7 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void k_lora_few(
       for (int e = 0; e < E; ++e) y[e] = ts[w] * at(b0, e);
 #pragma unroll 4
     for (int32_t j = w + FEW_WAVES; j < r; j += FEW_WAVES) {
-      const frag<T> bv = load_frag(B + (row0 + j) * M + col, M - col);
+      const frag<T> bv = load_frag(B + (row0 + j) * M + col, M - col, M);
 #pragma unroll
       for (int e = 0; e < E; ++e) y[e] = fmaf(ts[j], at(bv, e), y[e]);
     }
@@ -330,7 +353,7 @@ __device__ __forceinline__ int32_t row_at(const route_t& p, int32_t i) {
 // receives the sums.  Contains barriers.
 struct four_t { int32_t v[4]; };
 __device__ __forceinline__ four_t scan_four(four_t x, four_t* lds, four_t& total) {
-  const int w = threadIdx.x / 64;
+  const int w = wave_id();
   four_t inc, out;
 #pragma unroll
   for (int q = 0; q < 4; ++q) inc.v[q] = wave_incl_scan_i32(x.v[q]);
@@ -365,7 +388,7 @@ __global__ __launch_bounds__(1024) void k_lora_route(const int32_t* __restrict__
   __shared__ four_t lds[16];
   constexpr int RUN = 8;
   const int32_t G = L + 1;
-  const int w = threadIdx.x / 64, l = lane_id();
+  const int w = wave_id(), l = lane_id();
   int32_t *first = cnt + nw * G, *first_tile = first + G + 1;
   for (int32_t i = threadIdx.x; i < nw * G; i += 1024) cnt[i] = 0;
   __syncthreads();
@@ -482,6 +505,125 @@ struct tile_lds {
   int8_t kind[TILE];
 };
 
+// Which tile and role a workgroup has.  From 64 tiles on each die takes a run
+// of tiles, so that an adapter's factors fill few L2s.
+__device__ __forceinline__ bool place_of(int32_t tiles, int32_t roles, int32_t& ti, int32_t& role) {
+  ti = blockIdx.x / roles;
+  role = blockIdx.x % roles;
+  if (tiles >= 64) {
+    const int32_t each = (tiles + NUM_XCD - 1) / NUM_XCD, at = blockIdx.x / NUM_XCD / roles;
+    role = blockIdx.x / NUM_XCD % roles;
+    ti = at < each ? blockIdx.x % NUM_XCD * each + at : tiles;
+  }
+  return ti < tiles;
+}
+
+// Up to SELF_TOKENS tokens and SELF_GROUPS - 1 adapters, every workgroup finds
+// the tokens of its tile itself: it counts the groups in LDS (whole numbers:
+// the order of the additions does not matter), finds its tile's group and
+// collects that group's tokens.  SELF_BYTES: LDS that it takes.
+constexpr int32_t SELF_TOKENS = 8192, SELF_GROUPS = 1024;
+constexpr size_t SELF_BYTES = 4 * (SELF_GROUPS + WAVES + 4 + WAVES);
+
+struct tables_t {  // what the gradients need of it; all NULL: nothing
+  int32_t* order;  // tile i's tokens at i * TILE
+  tile_t* tile;
+  slot_t* slot;
+  join_t* join;
+  int32_t* count;
+};
+
+__device__ __forceinline__ bool self_route(const lora_dev& d, const route_t& p, const tables_t& out,
+                                           int32_t roles, char* lds, tile_lds& tk, int32_t& ti,
+                                           int32_t& role, tile_t& tl) {
+  constexpr int Q = SELF_TOKENS / (WAVES * 64);
+  int32_t* cnt = reinterpret_cast<int32_t*>(lds);
+  int32_t *scan = cnt + SELF_GROUPS, *found = scan + WAVES, *matches = found + 4;
+  const int32_t G = d.L + 1;
+  const int w = wave_id(), l = lane_id(), t = threadIdx.x;
+  const int32_t chunks = (p.Tn + WAVES * 64 - 1) / (WAVES * 64), i0 = w * chunks * 64 + l;
+  int32_t id[Q];  // then the token's group, -1 past the last token
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    if (q < chunks) id[q] = p.ids[min(i0 + q * 64, p.Tn - 1)];
+  for (int32_t g = t; g < G; g += WAVES * 64) cnt[g] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    if (q >= chunks) break;
+    id[q] = i0 + q * 64 >= p.Tn ? -1 : id[q] >= 0 && id[q] < d.L ? id[q] : d.L;
+    const int32_t same = __builtin_amdgcn_readfirstlane(id[q]);
+    if (__all(id[q] == same)) {
+      if (l == 0 && same >= 0) atomicAdd(&cnt[same], 64);
+    } else if (id[q] >= 0) {
+      atomicAdd(&cnt[id[q]], 1);
+    }
+  }
+  __syncthreads();
+  int32_t n[2], nt[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    n[h] = 2 * t + h < G ? cnt[2 * t + h] : 0;
+    nt[h] = (n[h] + TILE - 1) / TILE;
+  }
+  int32_t tiles;
+  const int32_t before = block_excl_scan_i32<WAVES * 64>(nt[0] + nt[1], scan, &tiles);
+  if (!place_of(tiles, roles, ti, role)) return false;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int32_t k = ti - before - h * nt[0];
+    if (k >= 0 && k < nt[h]) found[0] = 2 * t + h, found[1] = k, found[2] = n[h];
+  }
+  if (out.order && ti == 0 && role == 0) {
+    int32_t ns[2], at = before, slots, parts;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      ns[h] = 2 * t + h < d.L ? (nt[h] + p.slot_tiles - 1) / p.slot_tiles : 0;
+    const int32_t np[2] = {ns[0] > 1 ? ns[0] : 0, ns[1] > 1 ? ns[1] : 0};
+    int32_t bs = block_excl_scan_i32<WAVES * 64>(ns[0] + ns[1], scan, &slots);
+    int32_t bp = block_excl_scan_i32<WAVES * 64>(np[0] + np[1], scan, &parts);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (2 * t + h < d.L) out.join[2 * t + h] = join_t{ns[h], bp};
+      for (int32_t k = 0; k < ns[h]; ++k)
+        out.slot[bs + k] = slot_t{2 * t + h, at + k * p.slot_tiles,
+                                  min(p.slot_tiles, nt[h] - k * p.slot_tiles),
+                                  ns[h] > 1 ? bp + k : -1};
+      bs += ns[h];
+      bp += np[h];
+      at += nt[h];
+    }
+    if (t == 0) out.count[0] = tiles, out.count[1] = slots;
+  }
+  __syncthreads();
+  const int32_t g = found[0], k = found[1];
+  tl = tile_t{g, ti * TILE, min(TILE, found[2] - k * TILE), 0};
+  int32_t m = 0;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    if (q >= chunks) break;
+    m += __popcll(__ballot(id[q] == g));
+  }
+  if (l == 0) matches[w] = m;
+  __syncthreads();
+  int32_t at = -k * TILE;
+  for (int q = 0; q < w; ++q) at += matches[q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    if (q >= chunks) break;
+    const uint64_t mine = __ballot(id[q] == g);
+    const int32_t to = at + __popcll(mine & lanemask_lt());
+    if (id[q] == g && to >= 0 && to < TILE) tk.row[to] = i0 + q * 64;
+    at += __popcll(mine);
+  }
+  __syncthreads();
+  if (out.order && role == 0) {
+    if (t < TILE) out.order[ti * TILE + t] = tk.row[min(t, tl.n - 1)];
+    if (t == 0) out.tile[ti] = tl;
+  }
+  return true;
+}
+
 // ts[token][rank < r] = t, 0 for tokens without the adapter; ld: ts's stride.
 // A wave brings 128 bytes of each row at a time: eight lanes a row, so that a
 // load touches 8 lines (16 rows of 64 bytes, as the products take them, would
@@ -494,8 +636,8 @@ __device__ __forceinline__ void reduce_tile(const lora_dev& d, const reduce_arg<
                                             char* lds, float* ts, int32_t ld) {
   constexpr int E = EL<T>, KS = 8 * E;       // contraction of a step
   constexpr int NI = 2 * (RT + NR);          // loads of a step
-  constexpr int U = NI <= 6 ? 2 : 1;         // steps whose loads are under way together
-  const int w = threadIdx.x / 64, l = lane_id(), c = l & 15, g = l >> 4;
+  constexpr int D = NI <= 4 ? 4 : 2;  // steps whose loads are under way
+  const int w = wave_id(), l = lane_id(), c = l & 15, g = l >> 4;
   const int row8 = l >> 3, slot = l & 7;
   frag<T>* mine = reinterpret_cast<frag<T>*>(lds) + w * (NI * 64);
   frag<T>* put = mine + row8 * 8 + (slot ^ row8);
@@ -508,10 +650,11 @@ __device__ __forceinline__ void reduce_tile(const lora_dev& d, const reduce_arg<
     const T* src[NI];
 #pragma unroll
     for (int i = 0; i < 2 * RT; ++i)
-      src[i] = q.X + (int64_t)tk.row[i * 8 + row8] * q.ldx + slot * E;
+      src[i] = q.X + (int64_t)tk.row[i * 8 + row8] * q.ldx + slot * E + s0 * KS;
 #pragma unroll
     for (int i = 0; i < 2 * NR; ++i)  // rows past the rank: results not used
-      src[2 * RT + i] = q.F + ((int64_t)tl.l * d.R + min(rb + i * 8 + row8, r - 1)) * q.K + slot * E;
+      src[2 * RT + i] =
+          q.F + ((int64_t)tl.l * d.R + min(rb + i * 8 + row8, r - 1)) * q.K + slot * E + s0 * KS;
     f4 acc[RT][NR];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
@@ -538,22 +681,34 @@ __device__ __forceinline__ void reduce_tile(const lora_dev& d, const reduce_arg<
           for (int j = 0; j < NR; ++j) acc[i][j] = mma(xv[i], fv[j], acc[i][j]);
       }
     };
+    frag<T> v[D][NI];
+    auto load = [&](int u) {  // the next step
+#pragma unroll
+      for (int i = 0; i < NI; ++i) v[u][i] = load_frag(src[i]), src[i] += KS;
+    };
     int32_t s = s0;
-    for (; s + U <= full; s += U) {
-      frag<T> v[U][NI];
+    if (s + D <= full) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int u = 0; u < D; ++u) load(u);
+      for (; s + 2 * D <= full; s += D)
 #pragma unroll
-        for (int i = 0; i < NI; ++i) v[u][i] = load_frag(src[i] + (int64_t)(s + u) * KS);
+        for (int u = 0; u < D; ++u) {
+          turn(v[u]);
+          load(u);
+        }
 #pragma unroll
-      for (int u = 0; u < U; ++u) turn(v[u]);
+      for (int u = 0; u < D; ++u) turn(v[u]);
+      s += D;
     }
-    for (; s < s1; ++s) {  // what is left, and the step that ends past K
-      const int32_t left = q.K - s * KS - slot * E;
-      frag<T> v[NI];
+    for (; s < full; ++s) {
+      load(0);
+      turn(v[0]);
+    }
+    if (full < s1) {  // the step that ends past K
+      const int32_t left = q.K - full * KS - slot * E;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) v[i] = load_frag(src[i] + (int64_t)s * KS, left, s < full);
-      turn(v);
+      for (int i = 0; i < NI; ++i) v[0][i] = load_frag(src[i], left, q.K);
+      turn(v[0]);
     }
     float* red = reinterpret_cast<float*>(lds);  // over the operands of all waves
 #pragma unroll
@@ -631,7 +786,7 @@ __device__ __forceinline__ void expand_tile(const expand_arg<T>& q, const T* __r
                                             const tile_lds& tk, const float* ts, int32_t ld,
                                             const frag<bf16>* op, int32_t role, int32_t split) {
   constexpr int E = EL<T>, CW = 16 * E;
-  const int w = threadIdx.x / 64, l = lane_id(), c = l & 15, g = l >> 4;
+  const int w = wave_id(), l = lane_id(), c = l & 15, g = l >> 4;
   const int32_t blocks = (q.M + CW - 1) / CW;
   frag<bf16> t1[RT];
   if constexpr (sizeof(T) == 2 && ONE) {
@@ -663,6 +818,10 @@ __device__ __forceinline__ void expand_tile(const expand_arg<T>& q, const T* __r
     constexpr bool full = decltype(whole_block)::value;
     const int32_t col = b * CW + c * E, left = q.M - col;
     frag<T> bv[RT][4];
+    auto piece = [&](const T* p) {
+      if constexpr (full) return load_frag(p);
+      else return load_frag(p, left, q.M);
+    };
     // The row's number, read anew for each block (and the factor's row below):
     // addresses kept over the loop cost more registers than there are.
     auto row_of_tile = [&](int32_t tok) {
@@ -674,7 +833,7 @@ __device__ __forceinline__ void expand_tile(const expand_arg<T>& q, const T* __r
       if (q.base)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          bv[i][k] = load_frag(q.base + row_of_tile(i * 16 + 4 * g + k) * q.ldb + col, left, full);
+          bv[i][k] = piece(q.base + row_of_tile(i * 16 + 4 * g + k) * q.ldb + col);
     };
     auto put = [&](int i, f4 (&acc)[E]) {
       if (!whole) {  // rows without an adapter get base alone, wrong ids NaN
@@ -711,7 +870,7 @@ __device__ __forceinline__ void expand_tile(const expand_arg<T>& q, const T* __r
       auto load_rows = [&](int32_t j0) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          rows[k] = load_frag(F + (int64_t)min(j0 + j_of + k, r - 1) * q.M + col, left, full);
+          rows[k] = piece(F + (int64_t)min(j0 + j_of + k, r - 1) * q.M + col);
       };
       auto turn = [&](int32_t j0) {
         if (!even)
@@ -754,7 +913,7 @@ __device__ __forceinline__ void expand_tile(const expand_arg<T>& q, const T* __r
       for (int32_t j0 = 0; j0 < r; j0 += 4) {
         const int32_t j = j0 + g;
         const frag<T> row =
-            keep_if(j < r, load_frag(F + (int64_t)min(j, r - 1) * q.M + col, left, full));
+            keep_if(j < r, piece(F + (int64_t)min(j, r - 1) * q.M + col));
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           const float tv = j < r ? s * ts[(i * 16 + c) * ld + j] : 0.f;
@@ -776,35 +935,35 @@ __device__ __forceinline__ void expand_tile(const expand_arg<T>& q, const T* __r
 // grid: 8 * (tiles of a die) * roles.  Roles 0 to split - 1 of a tile compute t
 // of problem a and a share of the columns each, role 0 writes what is wanted
 // of t; role `split`, if launched, does the same for problem b, which has no
-// expansion.  From 64 tiles on each die takes a run of tiles, so that an
-// adapter's factors fill few L2s.
+// expansion.  self: no tables are there yet, see self_route.
 template <typename T, int NR>
 __global__ __launch_bounds__(WAVES * 64, NR == 1 ? 4 : 2) void k_lora_apply(
-    lora_dev d, route_t p, reduce_arg<T> a, reduce_arg<T> b, expand_arg<T> e, int32_t split,
-    int32_t roles, uint32_t* __restrict__ mask) {
+    lora_dev d, route_t p, tables_t out, bool self, reduce_arg<T> a, reduce_arg<T> b,
+    expand_arg<T> e, int32_t split, int32_t roles, uint32_t* __restrict__ mask) {
   extern __shared__ char lds[];
   __shared__ tile_lds tk;
-  const int32_t tiles = tiles_of(p), NT = (d.R + 15) / 16, ld = NT * 16 + 1;
-  int32_t ti = blockIdx.x / roles, role = blockIdx.x % roles;
-  if (tiles >= 64) {
-    const int32_t each = (tiles + NUM_XCD - 1) / NUM_XCD, at = blockIdx.x / NUM_XCD / roles;
-    if (at >= each) return;
-    role = blockIdx.x / NUM_XCD % roles;
-    ti = blockIdx.x % NUM_XCD * each + at;
+  const int32_t NT = (d.R + 15) / 16, ld = NT * 16 + 1;
+  int32_t ti, role;
+  tile_t tl;
+  if (self) {
+    if (!self_route(d, p, out, roles, lds, tk, ti, role, tl)) return;
+  } else {
+    if (!place_of(tiles_of(p), roles, ti, role)) return;
+    tl = tile_at(p, ti);
   }
-  if (ti >= tiles) return;
-  const tile_t tl = tile_at(p, ti);
   const int32_t r = tl.l < d.L ? rank_of(d, tl.l) : 0;
   const float s = r > 0 ? scale_of(d, tl.l) : 0.f;
-  if (threadIdx.x < TILE) {
-    const int32_t tok = threadIdx.x;
-    const int32_t row = row_at(p, tl.begin + min(tok, tl.n - 1));
-    const int32_t id = p.order && tl.l < d.L ? tl.l : p.ids[row];
+  if (threadIdx.x < 64) {
+    const int32_t tok = threadIdx.x & (TILE - 1), in = min(tok, tl.n - 1);
+    const int32_t row = self ? tk.row[in] : row_at(p, tl.begin + in);
+    const int32_t id = (self || p.order) && tl.l < d.L ? tl.l : p.ids[row];
     const int8_t kind = tok >= tl.n ? ROW_NONE : id >= d.L ? ROW_BAD : id >= 0 ? ROW_HAS : ROW_NONE;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // rows are read before they are set
+    __builtin_amdgcn_wave_barrier();
     tk.row[tok] = row;
     tk.kind[tok] = kind;
     const uint64_t has = __ballot(kind == ROW_HAS);
-    if (mask && role == 0 && tok == 0) mask[ti] = (uint32_t)has;
+    if (mask && role == 0 && threadIdx.x == 0) mask[ti] = (uint32_t)has;
   }
   __syncthreads();
   float* ts = reinterpret_cast<float*>(lds);
@@ -882,10 +1041,18 @@ __device__ __forceinline__ void grad_sum(const route_t& p, const grad_arg<T>& q,
   const T* X = q.X + col;
   auto fetch = [&](int32_t ti, frag<T> (&rows)[8]) {
     const tile_t tl = tile_at(p, ti);
-    const uint32_t has = mask[ti];
     int32_t row[8];
-    if (p.order) {  // `order` goes on for a tile past its last token
-      __builtin_memcpy(row, p.order + tl.begin + 8 * g, 32);
+    if (p.order) {
+      // The tile's tokens come as scalars (`order` goes on for a tile past its
+      // last token): loads of theirs among the rows' would have to be waited
+      // for together with them.
+      int32_t all[TILE];
+      __builtin_memcpy(all, p.order + tl.begin, sizeof(all));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int32_t a = pick(g & 1, all[8 + k], all[k]), b = pick(g & 1, all[24 + k], all[16 + k]);
+        row[k] = pick(g & 2, b, a);
+      }
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) row[k] = tl.begin + 8 * g + k;
@@ -893,18 +1060,36 @@ __device__ __forceinline__ void grad_sum(const route_t& p, const grad_arg<T>& q,
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int64_t at = 8 * g + k < tl.n ? row[k] : 0;
-      rows[k] = load_frag(X + at * q.ldx, left, FULL);
-      if (has != ~0u) rows[k] = keep_if((has >> (8 * g + k)) & 1, rows[k]);
+      if constexpr (FULL) rows[k] = load_frag(X + at * q.ldx);
+      else rows[k] = load_frag(X + at * q.ldx, left, q.K);
     }
   };
-  auto use = [&](int32_t ti, const frag<T> (&rows)[8]) {
-    if constexpr (sizeof(T) == 2) {
-      const frag<bf16>* o =
-          reinterpret_cast<const frag<bf16>*>(q.pack) + ((int64_t)ti * NT + rt0) * 128 + l;
-      frag<bf16> hi[NR], lo[NR];
+  // The tile's operands of t (bf16: hi and lo pieces; fp32: one rank of the
+  // lane's 8 tokens).
+  constexpr int PN = 8;  // dwords of a rank tile
+  auto fetch_pack = [&](int32_t ti, uint32_t (&t)[NR][PN]) {
 #pragma unroll
-      for (int j = 0; j < NR; ++j)
-        if (rt0 + j < nt) hi[j] = o[j * 128], lo[j] = o[j * 128 + 64];
+    for (int j = 0; j < NR; ++j) {
+      if (rt0 + j >= nt) break;
+      if constexpr (sizeof(T) == 2) {
+        const frag<bf16>* o =
+            reinterpret_cast<const frag<bf16>*>(q.pack) + ((int64_t)ti * NT + rt0 + j) * 128 + l;
+        __builtin_memcpy(t[j], o, 16);
+        __builtin_memcpy(t[j] + 4, o + 64, 16);
+      } else {
+        const uint32_t* o = reinterpret_cast<const uint32_t*>(q.pack) +
+                            (((int64_t)ti * TILE + 8 * g) * NT + rt0 + j) * 16 + c;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t[j][k] = o[k * NT * 16];
+      }
+    }
+  };
+  auto use = [&](int32_t ti, frag<T> (&rows)[8], const uint32_t (&t)[NR][PN]) {
+    const uint32_t has = mask[ti];
+    if (has != ~0u)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) rows[k] = keep_if((has >> (8 * g + k)) & 1, rows[k]);
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
         frag<bf16> a, b;  // columns e and e + 1
@@ -917,34 +1102,38 @@ __device__ __forceinline__ void grad_sum(const route_t& p, const grad_arg<T>& q,
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
           if (rt0 + j >= nt) break;
-          acc[j][e] = mma(lo[j], a, mma(hi[j], a, acc[j][e]));
-          acc[j][e + 1] = mma(lo[j], b, mma(hi[j], b, acc[j][e + 1]));
+          const frag<bf16> hi{{t[j][0], t[j][1], t[j][2], t[j][3]}},
+              lo{{t[j][4], t[j][5], t[j][6], t[j][7]}};
+          acc[j][e] = mma(lo, a, mma(hi, a, acc[j][e]));
+          acc[j][e + 1] = mma(lo, b, mma(hi, b, acc[j][e + 1]));
         }
       }
     } else {
-      const float* o =
-          reinterpret_cast<const float*>(q.pack) + ((int64_t)ti * TILE + 8 * g) * NT * 16 + c;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
           if (rt0 + j >= nt) break;
-          const float u = o[(k * NT + rt0 + j) * 16];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            acc[j][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(u, at(rows[k], e), acc[j][e], 0, 0, 0);
+            acc[j][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(t[j][k]),
+                                                             at(rows[k], e), acc[j][e], 0, 0, 0);
         }
     }
   };
   if (h >= sl.n || rt0 >= nt) return;
   frag<T> now[8], next[8];
+  uint32_t t[NR][PN];
   fetch(sl.tile + h, now);
-  for (; h < sl.n; h += tw) {
-    if (h + tw < sl.n) fetch(sl.tile + h + tw, next);
-    use(sl.tile + h, now);
+  for (; h + tw < sl.n; h += tw) {
+    fetch_pack(sl.tile + h, t);  // before the next rows: waiting for it does not wait for them
+    fetch(sl.tile + h + tw, next);
+    use(sl.tile + h, now, t);
 #pragma unroll
     for (int k = 0; k < 8; ++k) now[k] = next[k];
   }
+  fetch_pack(sl.tile + h, t);
+  use(sl.tile + h, now, t);
 }
 
 template <typename T, int NR>
@@ -953,7 +1142,7 @@ __global__ __launch_bounds__(grad_waves(NR) * 64, NR == 1 ? 4 : 2) void k_lora_g
     int32_t tw, const uint32_t* __restrict__ mask) {
   constexpr int E = EL<T>, CW = 16 * E, GW = grad_waves(NR);
   extern __shared__ char lds[];
-  const int w = threadIdx.x / 64, l = lane_id(), c = l & 15, g = l >> 4;
+  const int w = wave_id(), l = lane_id(), c = l & 15, g = l >> 4;
   const int32_t b = tw == 1 ? (int32_t)blockIdx.x * GW + w : (int32_t)blockIdx.x;
   if (b >= blocks) return;
   const bool first = b < blocks0;
@@ -1018,31 +1207,35 @@ __global__ __launch_bounds__(grad_waves(NR) * 64, NR == 1 ? 4 : 2) void k_lora_g
 }
 
 // The gradients of adapters without a slot (zeros) or with several (the sum of
-// their partial sums, in slot order).  grid: (adapter, rank) x column blocks.
+// their partial sums, in slot order).  grid: adapters x shares of the elements
+// of dA (blocks0 of them), then of dB.
 template <typename T>
 __global__ __launch_bounds__(256) void k_lora_join(lora_dev d, route_t p, int32_t slots,
                                                    grad_arg<T> q0, grad_arg<T> q1,
                                                    int32_t blocks0) {
-  const bool first = (int32_t)blockIdx.y < blocks0;
-  const grad_arg<T> q = first ? q0 : q1;
-  const int32_t l = blockIdx.x / d.R, j = blockIdx.x % d.R;
-  const int32_t m = (((int32_t)blockIdx.y - (first ? 0 : blocks0)) * 256 + threadIdx.x) * 4;
+  const int32_t l = blockIdx.x;
   const join_t jn = p.order ? p.join[l] : join_t{slots, 0};
-  if (m >= q.K || jn.slots == 1) return;
-  const int32_t n = q.K - m;
-  float v[4] = {};
-  const float* o = q.part + ((int64_t)jn.part * d.R + j) * q.K + m;
-  const int64_t next = (int64_t)d.R * q.K;
+  if (jn.slots == 1) return;
+  const bool first = (int32_t)blockIdx.y < blocks0;
+  const grad_arg<T>& q = first ? q0 : q1;
+  const int32_t at = (int32_t)blockIdx.y - (first ? 0 : blocks0);
+  const int32_t of = first ? blocks0 : (int32_t)gridDim.y - blocks0;
+  const int64_t size = (int64_t)d.R * q.K;
+  const float* part = q.part + jn.part * size;
+  T* out = q.dF + l * size;
+  for (int64_t m = ((int64_t)at * 256 + threadIdx.x) * 4; m < size; m += (int64_t)of * 1024) {
+    const int32_t n = (int32_t)min(size - m, (int64_t)4);
+    float v[4] = {};
 #pragma unroll 8
-  for (int32_t s = 0; s < jn.slots; ++s) {
-    const frag<float> f = load_frag(o + s * next, n);
+    for (int32_t s = 0; s < jn.slots; ++s) {
+      const frag<float> f = load_frag(part + s * size + m, n, size);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] += at(f, e);
+      for (int e = 0; e < 4; ++e) v[e] += __uint_as_float(f.w[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) out[m + e] = elem<T>::from_f(v[e]);
   }
-  T* out = q.dF + ((int64_t)l * d.R + j) * q.K + m;
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < n) out[e] = elem<T>::from_f(v[e]);
 }
 
 // --------------------------------------------------------------------- host
@@ -1063,6 +1256,7 @@ struct plan_t {
   int32_t whole;  // tiles if all tokens had one adapter
   int32_t tiles, slots, slot_tiles, part_slots, blocksA, blocksB, NT;
   int32_t tw;     // waves that share a slot's tokens: 1 or all of a workgroup
+  bool self;      // the workgroups find their tokens themselves
   size_t order, tile, slot, join, count, pack_t, pack_u, mask, partA, partB, total;
 };
 
@@ -1094,8 +1288,9 @@ plan_t plan_of(const snack_lora* p, snack_dtype dt, int32_t T, bool backward) {
     o = align_up(o + b, 256);
     return at;
   };
-  if (p->L > 1) {
-    w.order = take(4 * ((size_t)T + TILE));
+  w.self = p->L > 1 && T <= SELF_TOKENS && p->L < SELF_GROUPS;
+  if (p->L > 1 && (backward || !w.self)) {
+    w.order = take(4 * ((w.self ? (size_t)w.tiles * TILE : (size_t)T) + TILE));
     w.tile = take(sizeof(tile_t) * (size_t)w.tiles);
     w.slot = take(sizeof(slot_t) * (size_t)w.slots);
     w.join = take(sizeof(join_t) * (size_t)p->L);
@@ -1113,15 +1308,18 @@ plan_t plan_of(const snack_lora* p, snack_dtype dt, int32_t T, bool backward) {
   return w;
 }
 
+// The tokens' order, or (self) where k_lora_apply will put it.
 route_t launch_route(const snack_lora* p, const plan_t& w, const int32_t* ids, int32_t T, char* ws,
-                     hipStream_t s) {
+                     bool backward, hipStream_t s) {
   route_t r{ids, T, w.slot_tiles, nullptr, nullptr, nullptr, nullptr, nullptr};
   if (p->L == 1) return r;
+  if (w.self && !backward) return r;
   r.order = (const int32_t*)(ws + w.order);
   r.tile = (const tile_t*)(ws + w.tile);
   r.slot = (const slot_t*)(ws + w.slot);
   r.join = (const join_t*)(ws + w.join);
   r.count = (const int32_t*)(ws + w.count);
+  if (w.self) return r;
   const int32_t G = p->L + 1, nw = std::max(1, std::min(16, 15360 / G));
   hipLaunchKernelGGL(k_lora_route, dim3(1), dim3(1024), 4 * ((size_t)(nw + 2) * G + 2), s, ids, T,
                      p->L, nw, w.slot_tiles, (int32_t*)r.order, (tile_t*)r.tile, (slot_t*)r.slot,
@@ -1138,7 +1336,7 @@ void launch_apply(const lora_dev& d, const route_t& r, const plan_t& w, bool wit
   // for all its waves.
   int32_t split = 0;
   if (with_a) {
-    const int32_t tiles = r.order ? w.whole + std::min(d.L, r.Tn) / 2 : w.whole;
+    const int32_t tiles = d.L > 1 ? w.whole + std::min(d.L, r.Tn) / 2 : w.whole;
     split = e.Y ? (int32_t)std::max<int64_t>(1, std::min<int64_t>(512 / std::max(tiles, 1),
                                                                   cdiv(e.M, 16 * EL<T> * WAVES)))
                 : 1;
@@ -1147,10 +1345,14 @@ void launch_apply(const lora_dev& d, const route_t& r, const plan_t& w, bool wit
   const size_t ts = 4 * ((size_t)(TILE * (R16 + 1) + 3) / 4 * 4);
   const int32_t nr = w.NT >= 3 ? 4 : w.NT;
   const size_t red = std::max<size_t>((size_t)WAVES * (2 + nr) * 2048, (size_t)cdiv(d.R, 32) * 4096);
+  static_assert(SELF_BYTES <= (size_t)WAVES * 3 * 2048, "self_route's LDS lies within the operands'");
+  const tables_t out{const_cast<int32_t*>(r.order), const_cast<tile_t*>(r.tile),
+                     const_cast<slot_t*>(r.slot), const_cast<join_t*>(r.join),
+                     const_cast<int32_t*>(r.count)};
   const dim3 grid((unsigned)(NUM_XCD * cdiv(w.tiles, NUM_XCD) * roles));
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(WAVES * 64), ts + red, s, d, r, a, b, e, split, roles,
-                       mask);
+    hipLaunchKernelGGL(kernel, grid, dim3(WAVES * 64), ts + red, s, d, r, out, w.self, a, b, e, split,
+                       roles, mask);
   };
   if (w.NT == 1) go(k_lora_apply<T, 1>);
   else if (w.NT == 2) go(k_lora_apply<T, 2>);
@@ -1163,7 +1365,7 @@ void run_fwd(const snack_lora* p, const lora_dev& d, const int32_t* ids, int32_t
              snack_dtype dt, hipStream_t s) {
   if (Tn <= FEW_TOKENS) {
     const int32_t blocks = (int32_t)cdiv(p->M, 64 * EL<T>);
-    const int32_t split = std::max(1, std::min(blocks, 512 / Tn));
+    const int32_t split = std::max(1, std::min(blocks, 256 / Tn));
     const int32_t rows = Tn < NUM_XCD ? Tn : (int32_t)(cdiv(Tn, NUM_XCD) * NUM_XCD);
     hipLaunchKernelGGL(k_lora_few<T>, dim3((unsigned)(rows * split)), dim3(FEW_WAVES * 64), 0, s, d,
                        ids, Tn, split, (const T*)p->A, p->K, (const T*)X, ldx, (const T*)p->B, p->M,
@@ -1171,7 +1373,7 @@ void run_fwd(const snack_lora* p, const lora_dev& d, const int32_t* ids, int32_t
     return;
   }
   const plan_t w = plan_of(p, dt, Tn, false);
-  const route_t r = launch_route(p, w, ids, Tn, ws, s);
+  const route_t r = launch_route(p, w, ids, Tn, ws, false, s);
   const reduce_arg<T> a{(const T*)p->A, (const T*)X, ldx, p->K, nullptr, t, nullptr};
   const expand_arg<T> e{(const T*)p->B, p->M, (const T*)base, ldb, (T*)Y, ldy};
   launch_apply<T>(d, r, w, true, a, false, a, e, nullptr, s);
@@ -1186,7 +1388,7 @@ void run_bwd(const snack_lora* p, const lora_dev& d, const int32_t* ids, const f
   route_t r{};
   uint32_t* mask = (uint32_t*)(ws + w.mask);
   if (Tn > 0 && (dX || dA || dB)) {
-    r = launch_route(p, w, ids, Tn, ws, s);
+    r = launch_route(p, w, ids, Tn, ws, true, s);
     const reduce_arg<T> u{(const T*)p->B, (const T*)dY, lddy, p->M, nullptr, nullptr,
                           dA ? ws + w.pack_u : nullptr};
     const reduce_arg<T> v{(const T*)p->A, (const T*)X, ldx, p->K, t, nullptr, ws + w.pack_t};
@@ -1198,24 +1400,22 @@ void run_bwd(const snack_lora* p, const lora_dev& d, const int32_t* ids, const f
   grad_arg<T> qb{(const T*)dY, lddy, p->M, ws + w.pack_t, (T*)dB, (float*)(ws + w.partB)};
   const int32_t na = dA ? w.blocksA : 0, nb = dB ? w.blocksB : 0;
   if (Tn > 0) {
-    const int32_t nr = w.NT >= 3 ? 4 : w.NT;
-    const int32_t gw = grad_waves(nr);
+    const int32_t nr = std::min(w.NT, 2), gw = grad_waves(nr);
     const dim3 grid((unsigned)(w.tw == 1 ? cdiv(na + nb, gw) : na + nb), w.slots,
                     (unsigned)cdiv(w.NT, nr));
     const size_t lds = w.tw == 1 ? 0 : 4 * (size_t)gw * 16 * 16 * EL<T>;
-    auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, grid, dim3(gw * 64), lds, s, d, r, qa, qb, na, na + nb, w.tw,
-                         mask);
-    };
-    if (nr == 1) go(k_lora_grad<T, 1>);
-    else if (nr == 2) go(k_lora_grad<T, 2>);
-    else go(k_lora_grad<T, 4>);
+    auto kernel = nr == 1 ? k_lora_grad<T, 1> : k_lora_grad<T, 2>;
+    hipLaunchKernelGGL(kernel, grid, dim3(gw * 64), lds, s, d, r, qa, qb, na, na + nb, w.tw, mask);
   }
   const int32_t slots = Tn > 0 ? w.slots : 0;
   if (p->L == 1 && slots == 1) return;
-  const int32_t ja = dA ? (int32_t)cdiv(p->K, 1024) : 0, jb = dB ? (int32_t)cdiv(p->M, 1024) : 0;
-  hipLaunchKernelGGL(k_lora_join<T>, dim3((unsigned)(p->L * p->R), ja + jb), dim3(256), 0, s, d, r,
-                     slots, qa, qb, ja);
+  // workgroups for about 2,048 of them to be under way, the adapters' alike
+  auto shares = [&](int32_t F) {
+    return (int32_t)std::min<int64_t>(cdiv((int64_t)p->R * F, 1024), cdiv(2048, p->L));
+  };
+  const int32_t ja = dA ? shares(p->K) : 0, jb = dB ? shares(p->M) : 0;
+  hipLaunchKernelGGL(k_lora_join<T>, dim3((unsigned)p->L, ja + jb), dim3(256), 0, s, d, r, slots, qa,
+                     qb, ja);
 }
 
 }  // namespace
