@@ -27,7 +27,7 @@ namespace {
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 
-constexpr int32_t TILE = 32;  // tokens of a tile
+constexpr int32_t TILE = 32;  // tokens of a tile at most
 constexpr int32_t MAX_RANK = 256;
 constexpr int32_t MAX_ADAPTERS = 8192;
 constexpr int32_t MAX_FEATURES = 1 << 23;  // column blocks are a grid's y
@@ -121,6 +121,42 @@ __device__ __forceinline__ void store_frag(T* p, const frag<T>& f, int32_t n) {
       }
   }
 }
+// Pieces of E elements, loaded and stored likewise.
+template <typename T, int E> struct piece { uint32_t w[E * sizeof(T) / 4]; };
+template <typename T, int E>
+__device__ __forceinline__ uint32_t bits_at(const piece<T, E>& f, int e) {
+  return sizeof(T) == 4 ? f.w[e] : f.w[e / 2] >> (16 * (e & 1));
+}
+template <typename T, int E>
+__device__ __forceinline__ float at(const piece<T, E>& f, int e) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(f.w[e]);
+  else return __uint_as_float(e & 1 ? f.w[e / 2] & 0xFFFF0000u : f.w[e / 2] << 16);
+}
+template <typename T, int E>  // the first n elements at p, zeros after them
+__device__ __forceinline__ piece<T, E> load_piece(const T* p, int32_t n) {
+  piece<T, E> f{};
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    uint32_t v = 0;
+    if (e < n) __builtin_memcpy(&v, p + e, sizeof(T));
+    f.w[e * sizeof(T) / 4] |= v << (8 * (e * sizeof(T) % 4));
+  }
+  return f;
+}
+template <typename T, int E>  // elements from `from` up to `to`
+__device__ __forceinline__ void store_piece(T* p, const piece<T, E>& f, int32_t from, int32_t to) {
+  if (from <= 0 && to >= E) {
+    __builtin_memcpy(p, &f, sizeof(f));
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (e >= from && e < to) {
+        const uint32_t v = bits_at(f, e);
+        __builtin_memcpy(p + e, &v, sizeof(T));
+      }
+  }
+}
+
 // f, or zeros.
 template <typename T>
 __device__ __forceinline__ frag<T> keep_if(bool keep, const frag<T>& f) {
@@ -157,6 +193,17 @@ __device__ __forceinline__ frag<float> to_frag(const float (&v)[4]) {
                       __float_as_uint(v[3])}};
 }
 
+template <int E>
+__device__ __forceinline__ void round_to(const float (&v)[E], piece<bf16, E>& o) {
+#pragma unroll
+  for (int e = 0; e < E; e += 2) o.w[e / 2] = bf16_pair(v[e], v[e + 1]);
+}
+template <int E>
+__device__ __forceinline__ void round_to(const float (&v)[E], piece<float, E>& o) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) o.w[e] = __float_as_uint(v[e]);
+}
+
 // v as two bf16 parts, hi + lo: off by at most 2^-16 of v.  Infinities and NaN
 // are hi alone.
 __device__ __forceinline__ void split_frag(const float (&v)[8], frag<bf16>& hi, frag<bf16>& lo) {
@@ -168,18 +215,6 @@ __device__ __forceinline__ void split_frag(const float (&v)[8], frag<bf16>& hi, 
     rest[e] = fabsf(h) < __builtin_inff() ? v[e] - h : 0.f;
   }
   lo = to_frag(rest);
-}
-
-// out[c] = column c of the 8 x 8 matrix whose row q is rows[q].
-__device__ __forceinline__ void transpose8(const frag<bf16> (&rows)[8], frag<bf16> (&out)[8]) {
-#pragma unroll
-  for (int d = 0; d < 4; ++d)
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const uint32_t a = rows[2 * p].w[d], b = rows[2 * p + 1].w[d];
-      out[2 * d].w[p] = __builtin_amdgcn_perm(b, a, 0x05040100u);
-      out[2 * d + 1].w[p] = __builtin_amdgcn_perm(b, a, 0x07060302u);
-    }
 }
 
 // --------------------------------------------------------------- a few tokens
@@ -313,7 +348,7 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void k_lora_few(
 }
 
 // ------------------------------------------------------- tokens in adapter order
-// A tile is a run of up to TILE tokens of one adapter in that order; group L
+// A tile is a run of up to `size` (16 or 32) tokens of one adapter in that order; group L
 // holds the tokens without an adapter.  A slot is a run of tiles of one
 // adapter whose gradient is summed in one go; the slots of an adapter that has
 // several leave partial sums at `part`, part + 1, ...
@@ -324,6 +359,7 @@ struct join_t { int32_t slots, part; };
 struct route_t {
   const int32_t* ids;
   int32_t Tn;
+  int32_t size;            // tokens of a tile at most
   int32_t slot_tiles;      // tiles of a slot
   const int32_t* order;    // NULL: one adapter, tokens in their own order
   const tile_t* tile;
@@ -333,15 +369,15 @@ struct route_t {
 };
 
 __device__ __forceinline__ int32_t tiles_of(const route_t& p) {
-  return p.order ? p.count[0] : (p.Tn + TILE - 1) / TILE;
+  return p.order ? p.count[0] : (p.Tn + p.size - 1) / p.size;
 }
 __device__ __forceinline__ tile_t tile_at(const route_t& p, int32_t i) {
   if (p.order) return p.tile[i];
-  return tile_t{0, i * TILE, min(TILE, p.Tn - i * TILE), 0};
+  return tile_t{0, i * p.size, min(p.size, p.Tn - i * p.size), 0};
 }
 __device__ __forceinline__ slot_t slot_at(const route_t& p, int32_t i) {
   if (p.order) return i < p.count[1] ? p.slot[i] : slot_t{0, 0, 0, 0};
-  const int32_t tiles = (p.Tn + TILE - 1) / TILE;
+  const int32_t tiles = (p.Tn + p.size - 1) / p.size;
   return slot_t{0, i * p.slot_tiles, min(p.slot_tiles, tiles - i * p.slot_tiles),
                 tiles > p.slot_tiles ? i : -1};
 }
@@ -378,7 +414,8 @@ __device__ __forceinline__ four_t scan_four(four_t x, four_t* lds, four_t& total
 // count and once to place; lanes that hold the same adapter find each other by
 // one ballot per bit.  A walk loads RUN x 64 ids before it uses the first.
 __global__ __launch_bounds__(1024) void k_lora_route(const int32_t* __restrict__ ids, int32_t Tn,
-                                                     int32_t L, int32_t nw, int32_t slot_tiles,
+                                                     int32_t L, int32_t nw, int32_t size,
+                                                     int32_t slot_tiles,
                                                      int32_t* __restrict__ order,
                                                      tile_t* __restrict__ tile,
                                                      slot_t* __restrict__ slot,
@@ -433,7 +470,7 @@ __global__ __launch_bounds__(1024) void k_lora_route(const int32_t* __restrict__
     int32_t n = 0;
     if (g < G)
       for (int32_t q = 0; q < nw; ++q) n += cnt[q * G + g];
-    const int32_t nt = (n + TILE - 1) / TILE;
+    const int32_t nt = (n + size - 1) / size;
     const int32_t ns = g < L ? (nt + slot_tiles - 1) / slot_tiles : 0;
     four_t total;
     four_t b = scan_four(four_t{{n, nt, ns, ns > 1 ? ns : 0}}, lds, total);
@@ -468,8 +505,8 @@ __global__ __launch_bounds__(1024) void k_lora_route(const int32_t* __restrict__
       if (first_tile[mid] <= i) lo = mid;
       else hi = mid;
     }
-    const int32_t at = first[lo] + (i - first_tile[lo]) * TILE;
-    tile[i] = tile_t{lo, at, min(TILE, first[lo + 1] - at), 0};
+    const int32_t at = first[lo] + (i - first_tile[lo]) * size;
+    tile[i] = tile_t{lo, at, min(size, first[lo + 1] - at), 0};
   }
 }
 
@@ -486,7 +523,8 @@ struct reduce_arg {  // t[i, j] = sum_k F[a, j, k] X[i, k]
   const T* X;
   int64_t ldx;
   int32_t K;
-  const float* given;  // t itself, if it is there already
+  const float* given;  // t, if it is there already, as `parts` sums to be added
+  int32_t parts;
   float* t;            // nullable: where t goes
   void* pack;          // nullable: where t goes as the gradient's operand
 };
@@ -564,7 +602,7 @@ __device__ __forceinline__ bool self_route(const lora_dev& d, const route_t& p, 
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     n[h] = 2 * t + h < G ? cnt[2 * t + h] : 0;
-    nt[h] = (n[h] + TILE - 1) / TILE;
+    nt[h] = (n[h] + p.size - 1) / p.size;
   }
   int32_t tiles;
   const int32_t before = block_excl_scan_i32<WAVES * 64>(nt[0] + nt[1], scan, &tiles);
@@ -597,7 +635,7 @@ __device__ __forceinline__ bool self_route(const lora_dev& d, const route_t& p, 
   }
   __syncthreads();
   const int32_t g = found[0], k = found[1];
-  tl = tile_t{g, ti * TILE, min(TILE, found[2] - k * TILE), 0};
+  tl = tile_t{g, ti * TILE, min(p.size, found[2] - k * p.size), 0};
   int32_t m = 0;
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
@@ -606,14 +644,14 @@ __device__ __forceinline__ bool self_route(const lora_dev& d, const route_t& p, 
   }
   if (l == 0) matches[w] = m;
   __syncthreads();
-  int32_t at = -k * TILE;
+  int32_t at = -k * p.size;
   for (int q = 0; q < w; ++q) at += matches[q];
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
     if (q >= chunks) break;
     const uint64_t mine = __ballot(id[q] == g);
     const int32_t to = at + __popcll(mine & lanemask_lt());
-    if (id[q] == g && to >= 0 && to < TILE) tk.row[to] = i0 + q * 64;
+    if (id[q] == g && to >= 0 && to < p.size) tk.row[to] = i0 + q * 64;
     at += __popcll(mine);
   }
   __syncthreads();
@@ -625,6 +663,7 @@ __device__ __forceinline__ bool self_route(const lora_dev& d, const route_t& p, 
 }
 
 // ts[token][rank < r] = t, 0 for tokens without the adapter; ld: ts's stride.
+// Of `parts` equal ranges of k, only range `part` is summed.
 // A wave brings 128 bytes of each row at a time: eight lanes a row, so that a
 // load touches 8 lines (16 rows of 64 bytes, as the products take them, would
 // cost a look-up in the cache for every lane).  LDS of its own turns them into
@@ -633,18 +672,19 @@ __device__ __forceinline__ bool self_route(const lora_dev& d, const route_t& p, 
 template <typename T, int RT, int NR>
 __device__ __forceinline__ void reduce_tile(const lora_dev& d, const reduce_arg<T>& q,
                                             const tile_t& tl, int32_t r, const tile_lds& tk,
-                                            char* lds, float* ts, int32_t ld) {
+                                            char* lds, float* ts, int32_t ld, int32_t part,
+                                            int32_t parts) {
   constexpr int E = EL<T>, KS = 8 * E;       // contraction of a step
   constexpr int NI = 2 * (RT + NR);          // loads of a step
-  constexpr int D = NI <= 4 ? 4 : 2;  // steps whose loads are under way
+  constexpr int D = NI <= 4 ? 4 : NI == 8 ? 1 : 2;  // steps whose loads are under way
   const int w = wave_id(), l = lane_id(), c = l & 15, g = l >> 4;
   const int row8 = l >> 3, slot = l & 7;
   frag<T>* mine = reinterpret_cast<frag<T>*>(lds) + w * (NI * 64);
   frag<T>* put = mine + row8 * 8 + (slot ^ row8);
   const frag<T>* get = mine + c * 8;
   const int32_t steps = (q.K + KS - 1) / KS;
-  const int32_t s0 = (int32_t)((int64_t)steps * w / WAVES),
-                s1 = (int32_t)((int64_t)steps * (w + 1) / WAVES);
+  const int64_t at0 = (int64_t)part * WAVES + w, of = (int64_t)parts * WAVES;
+  const int32_t s0 = (int32_t)(steps * at0 / of), s1 = (int32_t)(steps * (at0 + 1) / of);
   const int32_t full = min(s1, q.K / KS);
   for (int32_t rb = 0; rb < r; rb += 16 * NR) {
     const T* src[NI];
@@ -732,14 +772,15 @@ __device__ __forceinline__ void reduce_tile(const lora_dev& d, const reduce_arg<
   }
 }
 
-// NR: rank tiles of the largest rank; an adapter takes as many as it has.
+// NR: rank tiles at a time, 1 where no adapter has more.
 template <typename T, int RT, int NR>
 __device__ __forceinline__ void reduce_ranks(const lora_dev& d, const reduce_arg<T>& q,
                                              const tile_t& tl, int32_t r, const tile_lds& tk,
-                                             char* lds, float* ts, int32_t ld) {
-  if (NR == 1 || r <= 16) reduce_tile<T, RT, 1>(d, q, tl, r, tk, lds, ts, ld);
-  else if (NR == 2 || r <= 32) reduce_tile<T, RT, 2>(d, q, tl, r, tk, lds, ts, ld);
-  else reduce_tile<T, RT, 4>(d, q, tl, r, tk, lds, ts, ld);
+                                             char* lds, float* ts, int32_t ld, int32_t part,
+                                             int32_t parts) {
+  if (NR == 1 || r <= 16) reduce_tile<T, RT, 1>(d, q, tl, r, tk, lds, ts, ld, part, parts);
+  else if (NR == 2 || r <= 32) reduce_tile<T, RT, 2>(d, q, tl, r, tk, lds, ts, ld, part, parts);
+  else reduce_tile<T, RT, NR == 4 ? 4 : 1>(d, q, tl, r, tk, lds, ts, ld, part, parts);
 }
 
 // The scaled t of a tile as the operand of the products over tokens:
@@ -773,70 +814,72 @@ __device__ __forceinline__ void write_pack(void* pack, int32_t ti, int32_t NT, i
   }
 }
 
-// Columns of a wave at a time: 16 pieces.  The factor's rows lie along m, so a
-// lane's pieces of 8 rows (bf16) are transposed in registers into 8 operands
-// of 8 ranks each; the results leave each lane with EL columns side by side,
-// one 16-byte piece of base in and one of Y out.  bf16 takes t in two parts
-// (hi + lo, whose products sum to fp32's accuracy): up to 16 ranks both parts
-// share one product (contraction 0-15 hi, 16-31 lo), above them each part has
-// its own, 32 ranks a step, staged in LDS (op).
-template <typename T, int RT, bool ONE>
+// A wave takes 16 E columns at a time, E side by side of a lane.  The factor's
+// rows lie along m, so (bf16) a lane's pieces of 8 rows are transposed in
+// registers into E operands of 8 ranks each.  bf16 takes t in two parts (hi +
+// lo, whose products sum to fp32's accuracy): up to 16 ranks both parts share
+// one product (contraction 0-15 hi, 16-31 lo), above them each part has its
+// own, 32 ranks a step; they lie in LDS (op).  With E = 4 the factor's rows of
+// the next step or block are under way while one is summed; E = 8 (one step a
+// block) has no registers for that, but accesses twice as wide.
+// E = 8 needs a rank.
+// WIDE: M >= 16 E, and a last block that would end past M begins earlier; what
+// the block before it has is not stored again.
+template <typename T, int RT, bool ONE, int E, bool WIDE>
 __device__ __forceinline__ void expand_tile(const expand_arg<T>& q, const T* __restrict__ F,
                                             const tile_t& tl, int32_t r, float s,
                                             const tile_lds& tk, const float* ts, int32_t ld,
                                             const frag<bf16>* op, int32_t role, int32_t split) {
-  constexpr int E = EL<T>, CW = 16 * E;
+  constexpr int CW = 16 * E;
+  constexpr bool H = sizeof(T) == 2, AHEAD = E == 4;
+  constexpr int NROW = H ? 8 : 4;             // the factor's rows of a lane in a step
+  constexpr int JS = H && !ONE ? 32 : 16;     // ranks of a step
+  constexpr int RG = AHEAD ? RT : 1;          // groups of 16 tokens summed at a time
+  static_assert(AHEAD || (H && ONE && WIDE), "wide pieces: one step a block");
   const int w = wave_id(), l = lane_id(), c = l & 15, g = l >> 4;
   const int32_t blocks = (q.M + CW - 1) / CW;
-  frag<bf16> t1[RT];
-  if constexpr (sizeof(T) == 2 && ONE) {
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int32_t j = 8 * (g & 1) + e;
-        v[e] = j < r ? s * ts[(i * 16 + c) * ld + j] : 0.f;
-      }
-      frag<bf16> hi, lo;
-      split_frag(v, hi, lo);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) t1[i].w[q] = g < 2 ? hi.w[q] : lo.w[q];
-    }
-  }
+  const bool even = r % JS == 0;
   bool whole = tl.n == RT * 16;  // every row of the tile has the adapter
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int k = 0; k < 4; ++k) whole = whole && tk.kind[i * 16 + 4 * g + k] == ROW_HAS;
   whole = __all(whole);
-  // r rows of the factor, JS a step; rows past the rank count as zeros
-  constexpr int JS = sizeof(T) == 4 ? 4 : ONE ? 16 : 32;
-  constexpr int RG = sizeof(T) == 2 && ONE ? 1 : RT;  // groups of 16 rows summed at a time
-  const bool even = r % JS == 0;
-  auto block = [&](int32_t b, auto whole_block) {
-    constexpr bool full = decltype(whole_block)::value;
-    const int32_t col = b * CW + c * E, left = q.M - col;
-    frag<T> bv[RT][4];
-    auto piece = [&](const T* p) {
-      if constexpr (full) return load_frag(p);
-      else return load_frag(p, left, q.M);
-    };
-    // The row's number, read anew for each block (and the factor's row below):
-    // addresses kept over the loop cost more registers than there are.
-    auto row_of_tile = [&](int32_t tok) {
-      int32_t row = tk.row[tok];
-      asm volatile("" : "+v"(row));
-      return (int64_t)row;
-    };
+
+  auto column = [&](int32_t b) { return (WIDE ? min(b * CW, q.M - CW) : b * CW) + c * E; };
+  auto load = [&](const T* p, int32_t col) {
+    piece<T, E> f;
+    if constexpr (WIDE) __builtin_memcpy(&f, p + col, sizeof(f));
+    else f = load_piece<T, E>(p + min(col, q.M - 1), q.M - col);
+    return f;
+  };
+  auto row_of_tile = [&](int32_t tok) {
+    int32_t row = tk.row[tok];
+    asm volatile("" : "+v"(row));  // addresses kept over the loops cost too many registers
+    return (int64_t)row;
+  };
+  piece<T, E> rows[NROW];
+  auto load_rows = [&](int32_t b, int32_t j0) {
+    int32_t j = j0 + (H ? 8 * (ONE ? g & 1 : g) : g);
+    asm volatile("" : "+v"(j));  // as above
+    const int32_t col = column(b);
+#pragma unroll
+    for (int k = 0; k < NROW; ++k)
+      rows[k] = load(F + (int64_t)min(j + (H ? k : 4 * k), r - 1) * q.M, col);
+  };
+  const int32_t next = split * WAVES, b0 = role * WAVES + w;
+  if (AHEAD && r > 0 && b0 < blocks) load_rows(b0, 0);
+  for (int32_t b = b0; b < blocks; b += next) {
+    const int32_t col = column(b);
+    piece<T, E> bv[RT][4];
     auto load_base = [&](int i) {
       if (q.base)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          bv[i][k] = piece(q.base + row_of_tile(i * 16 + 4 * g + k) * q.ldb + col);
+          bv[i][k] = load(q.base + row_of_tile(i * 16 + 4 * g + k) * q.ldb, col);
     };
     auto put = [&](int i, f4 (&acc)[E]) {
-      if (!whole) {  // rows without an adapter get base alone, wrong ids NaN
+      if (!whole)  // rows without an adapter get base alone, wrong ids NaN
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int8_t has = tk.kind[i * 16 + 4 * g + k];
@@ -844,18 +887,19 @@ __device__ __forceinline__ void expand_tile(const expand_arg<T>& q, const T* __r
 #pragma unroll
           for (int e = 0; e < E; ++e) acc[e][k] = has == ROW_HAS ? acc[e][k] : v;
         }
-      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int32_t tok = i * 16 + 4 * g + k;
-        if (tok >= tl.n || (!full && left <= 0)) continue;
+        if (tok >= tl.n) continue;
         float v[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           v[e] = acc[e][k];
           if (q.base) v[e] += at(bv[i][k], e);
         }
-        store_frag(q.Y + row_of_tile(tok) * q.ldy + col, to_frag(v), full ? E : left);
+        piece<T, E> o;
+        round_to(v, o);
+        store_piece(q.Y + row_of_tile(tok) * q.ldy + col, o, b * CW - col, WIDE ? E : q.M - col);
       }
     };
     f4 acc[RG][E];
@@ -863,83 +907,116 @@ __device__ __forceinline__ void expand_tile(const expand_arg<T>& q, const T* __r
     for (int i = 0; i < RG; ++i)
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[i][e] = f4{0.f, 0.f, 0.f, 0.f};
-    if constexpr (sizeof(T) == 2) {
-      int32_t j_of = 8 * (ONE ? g & 1 : g);
-      asm volatile("" : "+v"(j_of));
-      frag<T> rows[8], cols[8];
-      auto load_rows = [&](int32_t j0) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          rows[k] = piece(F + (int64_t)min(j0 + j_of + k, r - 1) * q.M + col);
+    if (!AHEAD) load_rows(b, 0);
+    load_base(0);
+    if constexpr (AHEAD && RT > 1) load_base(1);
+    // one step at most where ONE, exactly one for E = 8
+    for (int32_t j0 = 0; j0 < (!AHEAD ? 1 : ONE ? min(r, 1) : r); j0 += JS) {
+      auto load_next = [&]() {
+        const bool more = !ONE && j0 + JS < r;
+        if (more || b + next < blocks) load_rows(more ? b : b + next, more ? j0 + JS : 0);
       };
-      auto turn = [&](int32_t j0) {
-        if (!even)
+      if constexpr (H) {
+        frag<bf16> cols[E];
+        if (!even)  // rows past the rank count as zeros
 #pragma unroll
-          for (int k = 0; k < 8; ++k) rows[k] = keep_if(j0 + j_of + k < r, rows[k]);
-        transpose8(rows, cols);
-      };
-      if (r > 0) load_rows(0);
-      load_base(0);
-      if constexpr (ONE) {
-        if (r > 0) turn(0);
-        if constexpr (RT > 1) load_base(1);  // the rows' registers are free now
+          for (int k = 0; k < 8; ++k) {
+            const bool keep = j0 + 8 * (ONE ? g & 1 : g) + k < r;
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          if (r > 0)
+            for (int x = 0; x < E / 2; ++x) rows[k].w[x] = pick(keep, rows[k].w[x], 0u);
+          }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[0][e] = mma(t1[i], cols[e], f4{0.f, 0.f, 0.f, 0.f});
-          put(i, acc[0]);
-        }
-      } else {
-        if constexpr (RT > 1) load_base(1);
-        for (int32_t j0 = 0; j0 < r; j0 += JS) {
-          turn(j0);
-          if (j0 + JS < r) load_rows(j0 + JS);
+        for (int x = 0; x < E / 2; ++x)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a0 = rows[2 * k].w[x], a1 = rows[2 * k + 1].w[x];
+            cols[2 * x].w[k] = __builtin_amdgcn_perm(a1, a0, 0x05040100u);
+            cols[2 * x + 1].w[k] = __builtin_amdgcn_perm(a1, a0, 0x07060302u);
+          }
+        if constexpr (!AHEAD) {
+          if constexpr (RT > 1) load_base(1);  // the rows' registers are free now
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
-            const frag<bf16>* o = op + ((j0 / 32 * 2 + i) * 2) * 64 + l;
-            const frag<bf16> hi = o[0], lo = o[64];
+            const frag<bf16> t1 = op[i * 64 + l];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[i][e] = mma(lo, cols[e], mma(hi, cols[e], acc[i][e]));
+            for (int e = 0; e < E; ++e) acc[0][e] = mma(t1, cols[e], f4{0.f, 0.f, 0.f, 0.f});
+            put(i, acc[0]);
+          }
+        } else {
+          load_next();
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            if constexpr (ONE) {
+              const frag<bf16> t1 = op[i * 64 + l];
+#pragma unroll
+              for (int e = 0; e < E; ++e) acc[i][e] = mma(t1, cols[e], acc[i][e]);
+            } else {
+              const frag<bf16>* o = op + ((j0 / 32 * 2 + i) * 2) * 64 + l;
+              const frag<bf16> hi = o[0], lo = o[64];
+#pragma unroll
+              for (int e = 0; e < E; ++e) acc[i][e] = mma(lo, cols[e], mma(hi, cols[e], acc[i][e]));
+            }
           }
         }
+      } else {
+        piece<T, E> cols[4];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) put(i, acc[i]);
-      }
-    } else {
-      load_base(0);
-      if constexpr (RT > 1) load_base(1);
-#pragma unroll 4
-      for (int32_t j0 = 0; j0 < r; j0 += 4) {
-        const int32_t j = j0 + g;
-        const frag<T> row =
-            keep_if(j < r, piece(F + (int64_t)min(j, r - 1) * q.M + col));
+        for (int k = 0; k < 4; ++k) {
+          const bool keep = even || j0 + g + 4 * k < r;
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const float tv = j < r ? s * ts[(i * 16 + c) * ld + j] : 0.f;
+          for (int x = 0; x < E; ++x) cols[k].w[x] = pick(keep, rows[k].w[x], 0u);
+        }
+        load_next();
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(tv, at(row, e), acc[i][e], 0, 0, 0);
+        for (int k = 0; k < 4; ++k) {
+          const int32_t j = j0 + g + 4 * k;
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            const float tv = j < r ? s * ts[(i * 16 + c) * ld + j] : 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(tv, at(cols[k], e), acc[i][e], 0, 0, 0);
+          }
         }
       }
+    }
+    if constexpr (AHEAD) {
 #pragma unroll
       for (int i = 0; i < RT; ++i) put(i, acc[i]);
     }
-  };
-  for (int32_t b = role * WAVES + w; b < blocks; b += split * WAVES) {
-    if ((b + 1) * CW <= q.M) block(b, std::true_type());
-    else block(b, std::false_type());
   }
+}
+
+// Width of a lane's piece in the expansion.
+template <typename T>
+__device__ __host__ constexpr int expand_width(bool one, int32_t M) {
+  return sizeof(T) == 2 && one && M >= 128 ? 8 : 4;
+}
+
+template <typename T, int RT, bool ONE>
+__device__ __forceinline__ void expand_any(const expand_arg<T>& q, const T* __restrict__ F,
+                                           const tile_t& tl, int32_t r, float s,
+                                           const tile_lds& tk, const float* ts, int32_t ld,
+                                           const frag<bf16>* op, int32_t role, int32_t split) {
+  if constexpr (sizeof(T) == 2 && ONE)
+    if (r > 0 && expand_width<T>(ONE, q.M) == 8)
+      return expand_tile<T, RT, ONE, 8, true>(q, F, tl, r, s, tk, ts, ld, op, role, split);
+  if (q.M >= 64) expand_tile<T, RT, ONE, 4, true>(q, F, tl, r, s, tk, ts, ld, op, role, split);
+  else expand_tile<T, RT, ONE, 4, false>(q, F, tl, r, s, tk, ts, ld, op, role, split);
 }
 
 // grid: 8 * (tiles of a die) * roles.  Roles 0 to split - 1 of a tile compute t
 // of problem a and a share of the columns each, role 0 writes what is wanted
 // of t; role `split`, if launched, does the same for problem b, which has no
-// expansion.  self: no tables are there yet, see self_route.
-template <typename T, int NR>
-__global__ __launch_bounds__(WAVES * 64, NR == 1 ? 4 : 2) void k_lora_apply(
+// expansion.  cut: there is no expansion, and the roles of a and of b compute
+// and write a share of the sum over k each.  self: no tables are there yet, see
+// self_route.
+enum { BOTH, REDUCE, EXPAND };
+
+template <typename T, int NR, int MODE>
+__global__ __launch_bounds__(WAVES * 64, MODE == REDUCE && NR == 4 ? 2 : 4) void k_lora_apply(
     lora_dev d, route_t p, tables_t out, bool self, reduce_arg<T> a, reduce_arg<T> b,
-    expand_arg<T> e, int32_t split, int32_t roles, uint32_t* __restrict__ mask) {
+    expand_arg<T> e, int32_t split, int32_t roles, bool cut, uint32_t* __restrict__ mask) {
   extern __shared__ char lds[];
   __shared__ tile_lds tk;
   const int32_t NT = (d.R + 15) / 16, ld = NT * 16 + 1;
@@ -968,28 +1045,51 @@ __global__ __launch_bounds__(WAVES * 64, NR == 1 ? 4 : 2) void k_lora_apply(
   __syncthreads();
   float* ts = reinterpret_cast<float*>(lds);
   char* room = lds + (TILE * ld + 3) / 4 * 16;  // the waves' operands, their sums, the scaled t
-  const reduce_arg<T>& q = role < split ? a : b;
+  const bool is_a = role < split;
+  const reduce_arg<T>& q = is_a ? a : b;
+  const int32_t part = cut ? is_a ? role : role - split : 0;
+  const int32_t parts = cut ? is_a ? split : roles - split : 1;
   if (q.given) {
+    const int64_t next = (int64_t)p.Tn * d.R;
     for (int32_t k = threadIdx.x; k < tl.n * d.R; k += WAVES * 64) {
       const int32_t tok = k / d.R, j = k % d.R;
-      ts[tok * ld + j] = tk.kind[tok] == ROW_HAS ? q.given[(int64_t)tk.row[tok] * d.R + j] : 0.f;
+      const float* from = q.given + (int64_t)tk.row[tok] * d.R + j;
+      float v = 0.f;
+#pragma unroll 4
+      for (int32_t i = 0; i < q.parts; ++i) v += from[i * next];
+      ts[tok * ld + j] = tk.kind[tok] == ROW_HAS ? v : 0.f;
     }
-  } else if (tl.n <= 16) {
-    reduce_ranks<T, 1, NR>(d, q, tl, r, tk, room, ts, ld);
-  } else {
-    reduce_ranks<T, 2, NR>(d, q, tl, r, tk, room, ts, ld);
+  } else if constexpr (MODE != EXPAND) {
+    if (tl.n <= 16) reduce_ranks<T, 1, NR>(d, q, tl, r, tk, room, ts, ld, part, parts);
+    else reduce_ranks<T, 2, NR>(d, q, tl, r, tk, room, ts, ld, part, parts);
   }
   __syncthreads();
-  if (role == 0 || role == split) {
-    if (q.t)
+  if (cut || role == 0 || role == split) {
+    if (q.t) {
+      float* to = q.t + (int64_t)part * p.Tn * d.R;
       for (int32_t k = threadIdx.x; k < tl.n * d.R; k += WAVES * 64) {
         const int32_t tok = k / d.R, j = k % d.R;
-        q.t[(int64_t)tk.row[tok] * d.R + j] = j < r ? ts[tok * ld + j] : 0.f;
+        to[(int64_t)tk.row[tok] * d.R + j] = j < r ? ts[tok * ld + j] : 0.f;
       }
+    }
     if (q.pack && tl.l < d.L) write_pack<T>(q.pack, ti, NT, tl.n, r, s, ts, ld);
   }
+  if constexpr (MODE == REDUCE) return;
   if (role >= split || !e.Y) return;
   frag<bf16>* op = reinterpret_cast<frag<bf16>*>(room);
+  if constexpr (sizeof(T) == 2 && NR == 1) {
+    if (threadIdx.x < TILE * 4) {
+      const int32_t l = threadIdx.x & 63, tok = threadIdx.x / 64 * 16 + (l & 15), j0 = (l >> 4 & 1) * 8;
+      float v[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] = j0 + x < r ? s * ts[tok * ld + j0 + x] : 0.f;
+      frag<bf16> hi, lo;
+      split_frag(v, hi, lo);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) op[threadIdx.x].w[k] = pick(l < 32, hi.w[k], lo.w[k]);
+    }
+    __syncthreads();
+  }
   if constexpr (sizeof(T) == 2 && NR > 1) {
     const int32_t rts = tl.n <= 16 ? 1 : 2;
     for (int32_t k = threadIdx.x; k < (r + 31) / 32 * 128; k += WAVES * 64) {
@@ -1007,8 +1107,8 @@ __global__ __launch_bounds__(WAVES * 64, NR == 1 ? 4 : 2) void k_lora_apply(
     __syncthreads();
   }
   const T* F = e.F + (r > 0 ? (int64_t)tl.l * d.R * e.M : 0);
-  if (tl.n <= 16) expand_tile<T, 1, NR == 1>(e, F, tl, r, s, tk, ts, ld, op, role, split);
-  else expand_tile<T, 2, NR == 1>(e, F, tl, r, s, tk, ts, ld, op, role, split);
+  if (tl.n <= 16) expand_any<T, 1, NR == 1>(e, F, tl, r, s, tk, ts, ld, op, role, split);
+  else expand_any<T, 2, NR == 1>(e, F, tl, r, s, tk, ts, ld, op, role, split);
 }
 
 // --------------------------------------------------------------------- grad
@@ -1253,19 +1353,34 @@ snack_status check_lora(const snack_lora* p, snack_dtype dt, int32_t T) {
 constexpr int32_t FEW_TOKENS = 64;
 
 struct plan_t {
+  int32_t size;   // tokens of a tile at most
   int32_t whole;  // tiles if all tokens had one adapter
   int32_t tiles, slots, slot_tiles, part_slots, blocksA, blocksB, NT;
   int32_t tw;     // waves that share a slot's tokens: 1 or all of a workgroup
   bool self;      // the workgroups find their tokens themselves
-  size_t order, tile, slot, join, count, pack_t, pack_u, mask, partA, partB, total;
+  bool two;       // t in a launch of its own, K and M cut into ksK and ksM parts
+  int32_t ksK, ksM;
+  size_t order, tile, slot, join, count, t, u, pack_t, pack_u, mask, partA, partB, total;
 };
+
+// Tiles to be expected: about half the adapters have one that is not full.
+int64_t tiles_guess(int32_t L, int32_t T, int32_t size) {
+  return cdiv(T, size) + (L > 1 ? std::min(L, T) / 2 : 0);
+}
 
 plan_t plan_of(const snack_lora* p, snack_dtype dt, int32_t T, bool backward) {
   plan_t w{};
   const int32_t e = dt == SNACK_BF16 ? 8 : 4;
-  w.whole = (int32_t)cdiv(T, TILE);
-  w.tiles = p->L == 1 ? w.whole : (int32_t)std::min<int64_t>(T, (int64_t)T / TILE + p->L + 1);
   w.NT = (int32_t)cdiv(p->R, 16);
+  w.size = TILE;
+  // Forward, too few tiles for every CU to have a workgroup: smaller ones, as
+  // long as those are under way together (300 tokens of one adapter of rank 16,
+  // 4096 to 4096: 8.8 us, 11.3 us with tiles of 32).
+  if (!backward && tiles_guess(p->L, T, TILE) * std::min<int64_t>(8, cdiv(p->M, 512)) < 256 &&
+      (w.NT < 3 || tiles_guess(p->L, T, 16) <= 256))
+    w.size = 16;
+  w.whole = (int32_t)cdiv(T, w.size);
+  w.tiles = p->L == 1 ? w.whole : (int32_t)std::min<int64_t>(T, (int64_t)T / w.size + p->L + 1);
   w.blocksA = (int32_t)cdiv(p->K, 16 * e);
   w.blocksB = (int32_t)cdiv(p->M, 16 * e);
   // One wave sums a slot where adapters and columns make waves enough;
@@ -1289,12 +1404,33 @@ plan_t plan_of(const snack_lora* p, snack_dtype dt, int32_t T, bool backward) {
     return at;
   };
   w.self = p->L > 1 && T <= SELF_TOKENS && p->L < SELF_GROUPS;
-  if (p->L > 1 && (backward || !w.self)) {
+  const int64_t tiles = tiles_guess(p->L, T, w.size);
+  // More than 16 ranks: two launches, as the expansion then needs fewer
+  // registers than the sums.  Up to 16: two where the rows that t is summed
+  // over are long and the tiles few, so that several workgroups of a tile would
+  // each sum t anew (fp32, 1,024 tokens, 4096 to 4096: 28.9 us in one launch,
+  // 18.5 us in two; bf16 at 4096: 16.1 us either way).
+  const int64_t row = (int64_t)(backward ? p->M : p->K) * (16 / e);
+  w.two = p->R > 16 || (row >= 12288 && tiles < (backward ? 300 : 160));
+  // Two workgroups on every CU (one, where 64 ranks at a time leave registers
+  // for one), one step for each wave at least.
+  auto cut = [&](int32_t F) {
+    return (int32_t)std::max<int64_t>(
+        1, std::min<int64_t>((w.NT >= 3 ? 256 : 512) / std::max<int64_t>(tiles * (backward ? 2 : 1), 1),
+                             F / (8 * e * WAVES)));
+  };
+  w.ksK = cut(p->K);
+  w.ksM = cut(p->M);
+  if (p->L > 1 && (backward || !w.self || w.two)) {
     w.order = take(4 * ((w.self ? (size_t)w.tiles * TILE : (size_t)T) + TILE));
     w.tile = take(sizeof(tile_t) * (size_t)w.tiles);
     w.slot = take(sizeof(slot_t) * (size_t)w.slots);
     w.join = take(sizeof(join_t) * (size_t)p->L);
     w.count = take(8);
+  }
+  if (w.two) {
+    w.t = take(4 * (size_t)T * p->R * w.ksK);
+    if (backward) w.u = take(4 * (size_t)T * p->R * w.ksM);
   }
   if (backward) {
     const size_t pk = 4 * (size_t)w.tiles * TILE * w.NT * 16;
@@ -1311,9 +1447,9 @@ plan_t plan_of(const snack_lora* p, snack_dtype dt, int32_t T, bool backward) {
 // The tokens' order, or (self) where k_lora_apply will put it.
 route_t launch_route(const snack_lora* p, const plan_t& w, const int32_t* ids, int32_t T, char* ws,
                      bool backward, hipStream_t s) {
-  route_t r{ids, T, w.slot_tiles, nullptr, nullptr, nullptr, nullptr, nullptr};
+  route_t r{ids, T, w.size, w.slot_tiles, nullptr, nullptr, nullptr, nullptr, nullptr};
   if (p->L == 1) return r;
-  if (w.self && !backward) return r;
+  if (w.self && !backward && !w.two) return r;
   r.order = (const int32_t*)(ws + w.order);
   r.tile = (const tile_t*)(ws + w.tile);
   r.slot = (const slot_t*)(ws + w.slot);
@@ -1322,41 +1458,58 @@ route_t launch_route(const snack_lora* p, const plan_t& w, const int32_t* ids, i
   if (w.self) return r;
   const int32_t G = p->L + 1, nw = std::max(1, std::min(16, 15360 / G));
   hipLaunchKernelGGL(k_lora_route, dim3(1), dim3(1024), 4 * ((size_t)(nw + 2) * G + 2), s, ids, T,
-                     p->L, nw, w.slot_tiles, (int32_t*)r.order, (tile_t*)r.tile, (slot_t*)r.slot,
+                     p->L, nw, w.size, w.slot_tiles, (int32_t*)r.order, (tile_t*)r.tile, (slot_t*)r.slot,
                      (join_t*)r.join, (int32_t*)r.count);
   return r;
 }
 
-// a with the expansion e (split workgroups a tile), b if `both`.
 template <typename T>
-void launch_apply(const lora_dev& d, const route_t& r, const plan_t& w, bool with_a,
-                  const reduce_arg<T>& a, bool with_b, const reduce_arg<T>& b,
+void launch_apply(const lora_dev& d, const route_t& r, const plan_t& w, bool self, int32_t split,
+                  int32_t roles, bool cut, const reduce_arg<T>& a, const reduce_arg<T>& b,
                   const expand_arg<T>& e, uint32_t* mask, hipStream_t s) {
-  // Workgroups of a tile: enough to have two on every CU, each with columns
-  // for all its waves.
-  int32_t split = 0;
-  if (with_a) {
-    const int32_t tiles = d.L > 1 ? w.whole + std::min(d.L, r.Tn) / 2 : w.whole;
-    split = e.Y ? (int32_t)std::max<int64_t>(1, std::min<int64_t>(512 / std::max(tiles, 1),
-                                                                  cdiv(e.M, 16 * EL<T> * WAVES)))
-                : 1;
-  }
-  const int32_t roles = split + (with_b ? 1 : 0), R16 = w.NT * 16;
-  const size_t ts = 4 * ((size_t)(TILE * (R16 + 1) + 3) / 4 * 4);
+  const size_t ts = 4 * ((size_t)(TILE * (w.NT * 16 + 1) + 3) / 4 * 4);
   const int32_t nr = w.NT >= 3 ? 4 : w.NT;
-  const size_t red = std::max<size_t>((size_t)WAVES * (2 + nr) * 2048, (size_t)cdiv(d.R, 32) * 4096);
-  static_assert(SELF_BYTES <= (size_t)WAVES * 3 * 2048, "self_route's LDS lies within the operands'");
+  const bool sums = cut || w.NT == 1;  // whether sums over k are made here
+  const size_t red = std::max<size_t>(sums ? (size_t)WAVES * (2 + nr) * 2048 : SELF_BYTES,
+                                      (size_t)cdiv(d.R, 32) * 4096);
   const tables_t out{const_cast<int32_t*>(r.order), const_cast<tile_t*>(r.tile),
                      const_cast<slot_t*>(r.slot), const_cast<join_t*>(r.join),
                      const_cast<int32_t*>(r.count)};
   const dim3 grid((unsigned)(NUM_XCD * cdiv(w.tiles, NUM_XCD) * roles));
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(WAVES * 64), ts + red, s, d, r, out, w.self, a, b, e, split,
-                       roles, mask);
-  };
-  if (w.NT == 1) go(k_lora_apply<T, 1>);
-  else if (w.NT == 2) go(k_lora_apply<T, 2>);
-  else go(k_lora_apply<T, 4>);
+  auto kernel = w.NT == 1 ? k_lora_apply<T, 1, BOTH>
+                : !cut    ? k_lora_apply<T, 2, EXPAND>
+                : nr == 2 ? k_lora_apply<T, 2, REDUCE>
+                          : k_lora_apply<T, 4, REDUCE>;
+  hipLaunchKernelGGL(kernel, grid, dim3(WAVES * 64), ts + red, s, d, r, out, self, a, b, e, split,
+                     roles, cut, mask);
+}
+
+// Problem a (ksA parts) with the expansion e, and problem b (ksB parts), each
+// if wanted; ta, tb: room for the parts.
+template <typename T>
+void run_apply(const lora_dev& d, const route_t& r, const plan_t& w, bool with_a, reduce_arg<T> a,
+               int32_t ksA, float* ta, bool with_b, reduce_arg<T> b, int32_t ksB, float* tb,
+               const expand_arg<T>& e, uint32_t* mask, hipStream_t s) {
+  bool self = w.self;
+  if (w.two) {
+    reduce_arg<T> a1 = a, b1 = b;
+    a1.t = ta, a1.pack = nullptr, b1.t = tb, b1.pack = nullptr;
+    const int32_t na = with_a ? ksA : 0, nb = with_b && !b.given ? ksB : 0;
+    if (na + nb > 0) {
+      launch_apply<T>(d, r, w, self, na, na + nb, true, a1, b1, {}, nullptr, s);
+      self = false;
+    }
+    if (with_a) a.given = ta, a.parts = ksA;
+    if (nb > 0) b.given = tb, b.parts = ksB;
+  }
+  // Workgroups of a tile: enough to have two on every CU, each with columns
+  // for all its waves.
+  int32_t split = with_a ? 1 : 0;
+  if (with_a && e.Y)
+    split = (int32_t)std::max<int64_t>(
+        1, std::min<int64_t>(512 / std::max<int64_t>(tiles_guess(d.L, r.Tn, w.size), 1),
+                             cdiv(e.M, 16 * expand_width<T>(w.NT == 1, e.M) * WAVES)));
+  launch_apply<T>(d, r, w, self, split, split + (with_b ? 1 : 0), false, a, b, e, mask, s);
 }
 
 template <typename T>
@@ -1374,9 +1527,9 @@ void run_fwd(const snack_lora* p, const lora_dev& d, const int32_t* ids, int32_t
   }
   const plan_t w = plan_of(p, dt, Tn, false);
   const route_t r = launch_route(p, w, ids, Tn, ws, false, s);
-  const reduce_arg<T> a{(const T*)p->A, (const T*)X, ldx, p->K, nullptr, t, nullptr};
+  const reduce_arg<T> a{(const T*)p->A, (const T*)X, ldx, p->K, nullptr, 0, t, nullptr};
   const expand_arg<T> e{(const T*)p->B, p->M, (const T*)base, ldb, (T*)Y, ldy};
-  launch_apply<T>(d, r, w, true, a, false, a, e, nullptr, s);
+  run_apply<T>(d, r, w, true, a, w.ksK, (float*)(ws + w.t), false, a, 0, nullptr, e, nullptr, s);
 }
 
 template <typename T>
@@ -1389,11 +1542,12 @@ void run_bwd(const snack_lora* p, const lora_dev& d, const int32_t* ids, const f
   uint32_t* mask = (uint32_t*)(ws + w.mask);
   if (Tn > 0 && (dX || dA || dB)) {
     r = launch_route(p, w, ids, Tn, ws, true, s);
-    const reduce_arg<T> u{(const T*)p->B, (const T*)dY, lddy, p->M, nullptr, nullptr,
+    const reduce_arg<T> u{(const T*)p->B, (const T*)dY, lddy, p->M, nullptr, 0, nullptr,
                           dA ? ws + w.pack_u : nullptr};
-    const reduce_arg<T> v{(const T*)p->A, (const T*)X, ldx, p->K, t, nullptr, ws + w.pack_t};
+    const reduce_arg<T> v{(const T*)p->A, (const T*)X, ldx, p->K, t, 1, nullptr, ws + w.pack_t};
     const expand_arg<T> e{(const T*)p->A, p->K, (const T*)base, ldb, (T*)dX, lddx};
-    launch_apply<T>(d, r, w, dX || dA, u, dB != nullptr, v, e, mask, s);
+    run_apply<T>(d, r, w, dX || dA, u, w.ksM, (float*)(ws + w.u), dB != nullptr, v, w.ksK,
+                 (float*)(ws + w.t), e, mask, s);
   }
   if (!dA && !dB) return;
   grad_arg<T> qa{(const T*)X, ldx, p->K, ws + w.pack_u, (T*)dA, (float*)(ws + w.partA)};
