@@ -1376,21 +1376,26 @@ plan_t plan_of(const snack_lora* p, snack_dtype dt, int32_t T, bool backward) {
   // Forward, too few tiles for every CU to have a workgroup: smaller ones, as
   // long as those are under way together (300 tokens of one adapter of rank 16,
   // 4096 to 4096: 8.8 us, 11.3 us with tiles of 32).
-  if (!backward && tiles_guess(p->L, T, TILE) * std::min<int64_t>(8, cdiv(p->M, 512)) < 256 &&
+  if (tiles_guess(p->L, T, TILE) * std::min<int64_t>(8, cdiv(backward ? p->K : p->M, 512)) <
+          (backward ? 64 : 256) &&
       (w.NT < 3 || tiles_guess(p->L, T, 16) <= 256))
     w.size = 16;
   w.whole = (int32_t)cdiv(T, w.size);
   w.tiles = p->L == 1 ? w.whole : (int32_t)std::min<int64_t>(T, (int64_t)T / w.size + p->L + 1);
   w.blocksA = (int32_t)cdiv(p->K, 16 * e);
   w.blocksB = (int32_t)cdiv(p->M, 16 * e);
-  // One wave sums a slot where adapters and columns make waves enough;
-  // elsewhere the waves of a workgroup share it.
-  const int32_t gw = grad_waves(w.NT);
-  const int64_t blocks = w.blocksA + w.blocksB;
-  w.tw = blocks * std::min(p->L, w.whole) >= 2048 ? 1 : gw;
+  // One wave sums a slot where adapters and columns make waves enough, or
+  // adapters have too few tiles to share; elsewhere the waves of a workgroup
+  // share it.
+  const int32_t gw = grad_waves(w.NT), users = std::max(1, std::min(p->L, w.whole));
+  const int64_t blocks = w.blocksA + w.blocksB, alone = blocks * users * cdiv(w.NT, 2);
+  const int32_t per = w.whole / users;  // tiles of an adapter
+  w.tw = alone < 4096 && (per >= 2 * gw || (alone < 1024 && per >= 3)) ? gw : 1;
   const int64_t runs = std::max<int64_t>(1, cdiv(4096 / gw, blocks));
-  w.slot_tiles = w.tw == 1 ? (int32_t)std::max<int64_t>(16, cdiv(w.whole, 32))
-                           : (int32_t)std::max<int64_t>(gw, cdiv(w.whole, runs));
+  const int32_t even = (int32_t)cdiv(w.whole, runs);  // tiles of a slot, all slots alike
+  w.slot_tiles = w.tw == 1    ? (int32_t)std::max<int64_t>(16, cdiv(w.whole, 32))
+                 : p->L == 1 ? std::max(gw, even)
+                             : 2 * std::max(gw, even);  // few adapters have more than one
   w.slots = p->L == 1 ? (int32_t)cdiv(w.whole, w.slot_tiles)
                       : (int32_t)std::min<int64_t>(w.tiles, w.whole / w.slot_tiles + p->L);
   // an adapter with several slots has more than slot_tiles tiles, so its
