@@ -88,15 +88,18 @@ __device__ __forceinline__ frag<float> move_down(const frag<float>& f, int32_t s
   return frag<float>{{pick(none, 0, pick(sh & 2, b2, b0)), pick(none, 0, pick(sh & 2, b3, b1)),
                       pick(none || (sh & 2), 0, b2), pick(none || (sh & 2), 0, b3)}};
 }
-// The piece at p of a row of `row` elements, of which n are left there (n may
-// be <= 0), zeros after them.  One load: a piece that ends early is taken from
-// the row's last EL elements.
+// The piece at p of a row of EL elements or more, of which n are left there (n
+// may be <= 0), zeros after them.  One load: a piece that ends early is taken
+// from the row's last EL elements.
+template <typename T>
+__device__ __forceinline__ frag<T> load_end(const T* p, int32_t n) {
+  const int32_t sh = max(EL<T> - n, 0);
+  return move_down(load_frag(p - sh), sh);
+}
+// The same for a row of `row` elements, which may be fewer.
 template <typename T>
 __device__ __forceinline__ frag<T> load_frag(const T* p, int32_t n, int64_t row) {
-  if (row >= EL<T>) {
-    const int32_t sh = max(EL<T> - n, 0);
-    return move_down(load_frag(p - sh), sh);
-  }
+  if (row >= EL<T>) return load_end(p, n);
   frag<T> f{};
 #pragma unroll 1
   for (int e = (int)row - 1; e >= 0; --e) {  // the row is shorter than a piece: p is its start
@@ -218,11 +221,12 @@ __device__ __forceinline__ void split_frag(const float (&v)[8], frag<bf16>& hi, 
 }
 
 // --------------------------------------------------------------- a few tokens
-// A workgroup has one token and every split-th block of 64 pieces of columns.
-// Its sixteen waves share the ranks, first for t (each workgroup of the token
-// computes all of t again: the factor comes from the caches), then for the
-// expansion, whose parts meet in LDS.  What the expansion reads first is
-// loaded before t, so one trip to memory covers both.
+// A workgroup has one token and nb blocks of 64 pieces of columns at a time.
+// Its sixteen waves share the ranks of t (each workgroup of the token computes
+// all of t again: the factor comes from the caches).  Then 16 / nb waves share
+// the ranks of a block's expansion, whose parts meet in LDS.  What the
+// expansion reads first is loaded before t, so one trip to memory covers both.
+// K and M hold a piece at least.
 constexpr int FEW_WAVES = 16;
 
 template <typename T>
@@ -260,9 +264,9 @@ __device__ __forceinline__ void few_dots(const T* x, const T* __restrict__ F, in
     for (int q = 0; q < RW; ++q) acc[q] = dot_frag(xv, load_frag(F + q * next + k), acc[q]);
   }
   if (k < K) {
-    const frag<T> xv = load_frag(x + k, K - k, K);
+    const frag<T> xv = load_end(x + k, K - k);
 #pragma unroll
-    for (int q = 0; q < RW; ++q) acc[q] = dot_frag(xv, load_frag(F + q * next + k, K - k, K), acc[q]);
+    for (int q = 0; q < RW; ++q) acc[q] = dot_frag(xv, load_end(F + q * next + k, K - k), acc[q]);
   }
 #pragma unroll
   for (int q = 0; q < RW; ++q) {
@@ -274,19 +278,19 @@ __device__ __forceinline__ void few_dots(const T* x, const T* __restrict__ F, in
 
 template <typename T>
 __global__ __launch_bounds__(FEW_WAVES * 64) void k_lora_few(
-    lora_dev d, const int32_t* __restrict__ ids, int32_t Tn, int32_t split,
+    lora_dev d, const int32_t* __restrict__ ids, int32_t Tn, int32_t split, int32_t log_nb,
     const T* __restrict__ A, int32_t K, const T* X, int64_t ldx, const T* __restrict__ B, int32_t M,
     const T* base, int64_t ldb, T* Y, int64_t ldy, float* t) {
-  constexpr int E = EL<T>, C = 64 * E;
+  constexpr int E = EL<T>, C = 64 * E, AHEAD = 2;
   __shared__ float ts[MAX_RANK];
   __shared__ float red[FEW_WAVES][C];
   // From 8 tokens on a token's workgroups share a die, whose L2 then holds
   // the token's factor once.
-  int32_t i = blockIdx.x / split, cb = blockIdx.x % split;
+  int32_t i = blockIdx.x / split, share = blockIdx.x % split;
   if (Tn >= NUM_XCD) {
     const int32_t at = blockIdx.x / NUM_XCD;
     i = at / split * NUM_XCD + blockIdx.x % NUM_XCD;
-    cb = at % split;
+    share = at % split;
   }
   if (i >= Tn) return;
   const int32_t a = ids[i];
@@ -294,12 +298,21 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void k_lora_few(
   const int32_t r = a >= 0 && a < d.L ? rank_of(d, a) : 0;
   const float s = a >= d.L ? __builtin_nanf("") : r > 0 ? scale_of(d, a) : 1.f;
   const int64_t row0 = r > 0 ? (int64_t)a * d.R : 0;
-  const T* Bw = B + (row0 + w) * M;
-  const int c = threadIdx.x;
-  frag<T> b0{};
-  T base0 = 0;
-  if (w < r) b0 = load_frag(Bw + cb * C + l * E, M - cb * C - l * E, M);
-  if (base && c < C && cb * C + c < M) base0 = base[i * ldb + cb * C + c];
+  const int32_t nb = 1 << log_nb;
+  const int32_t groups = FEW_WAVES >> log_nb, j0 = w >> log_nb;  // of the expansion's ranks
+  int32_t col0 = share * nb * C;                       // the workgroup's first column
+  // A piece that would end past M is the row's last one; what lies before the
+  // lane's column is not stored.
+  auto column = [&]() { return min(col0 + (w & (nb - 1)) * C + l * E, M - E); };
+  frag<T> ahead[AHEAD], base0{};
+  auto load_ahead = [&]() {
+    const int32_t col = column();
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q)
+      if (j0 + q * groups < r) ahead[q] = load_frag(B + (row0 + j0 + q * groups) * M + col);
+    if (base && w < nb) base0 = load_frag(base + i * ldb + col);
+  };
+  load_ahead();
   const T* x = X + i * ldx;
   for (int32_t j = w; j < r;) {
     const T* F = A + (row0 + j) * K;
@@ -315,35 +328,45 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void k_lora_few(
     }
   }
   __syncthreads();
-  if (t && cb == 0 && c < d.R) t[(int64_t)i * d.R + c] = c < r ? ts[c] : 0.f;
-  for (bool first = true; cb * C < M; cb += split, first = false) {
-    const int32_t col = cb * C + l * E;
+  if (t && share == 0 && (int32_t)threadIdx.x < d.R)
+    t[(int64_t)i * d.R + threadIdx.x] = (int32_t)threadIdx.x < r ? ts[threadIdx.x] : 0.f;
+  while (true) {
+    const int32_t col = column();
     float y[E] = {};
-    if (!first) {
-      if (w < r) b0 = load_frag(Bw + col, M - col, M);
-      if (base && c < C && cb * C + c < M) base0 = base[i * ldb + cb * C + c];
-    }
-    if (w < r)
 #pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = ts[w] * at(b0, e);
+    for (int q = 0; q < AHEAD; ++q)
+      if (j0 + q * groups < r) {
+        const float tv = ts[j0 + q * groups];
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = fmaf(tv, at(ahead[q], e), y[e]);
+      }
 #pragma unroll 4
-    for (int32_t j = w + FEW_WAVES; j < r; j += FEW_WAVES) {
-      const frag<T> bv = load_frag(B + (row0 + j) * M + col, M - col, M);
+    for (int32_t j = j0 + AHEAD * groups; j < r; j += groups) {
+      const frag<T> bv = load_frag(B + (row0 + j) * M + col);
 #pragma unroll
       for (int e = 0; e < E; ++e) y[e] = fmaf(ts[j], at(bv, e), y[e]);
     }
-    if (!first) __syncthreads();
 #pragma unroll
     for (int e = 0; e < E; ++e) red[w][l * E + e] = y[e];
     __syncthreads();
-    if (c < C && cb * C + c < M) {
-      float v = 0.f;
+    if (w < nb) {
+      float v[E] = {};
+      for (int32_t q = 0; q < groups; ++q)
 #pragma unroll
-      for (int q = 0; q < FEW_WAVES; ++q) v += red[q][c];
-      v *= s;
-      if (base) v += elem<T>::to_f(base0);
-      Y[i * ldy + cb * C + c] = elem<T>::from_f(v);
+        for (int e = 0; e < E; ++e) v[e] += red[q * nb + w][l * E + e];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        v[e] *= s;
+        if (base) v[e] += at(base0, e);
+      }
+      piece<T, E> o;
+      round_to(v, o);
+      store_piece(Y + i * ldy + col, o, col0 + w * C + l * E - col, M - col);
     }
+    col0 += split * nb * C;
+    if (col0 >= M) break;
+    load_ahead();
+    __syncthreads();
   }
 }
 
@@ -351,7 +374,8 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void k_lora_few(
 // A tile is a run of up to `size` (16 or 32) tokens of one adapter in that order; group L
 // holds the tokens without an adapter.  A slot is a run of tiles of one
 // adapter whose gradient is summed in one go; the slots of an adapter that has
-// several leave partial sums at `part`, part + 1, ...
+// several leave partial sums at `part`, part + 1, ...; an adapter without
+// tokens has one slot of no tiles.
 struct tile_t { int32_t l, begin, n, pad; };
 struct slot_t { int32_t l, tile, n, part; };  // part < 0: the adapter's only slot
 struct join_t { int32_t slots, part; };
@@ -376,7 +400,7 @@ __device__ __forceinline__ tile_t tile_at(const route_t& p, int32_t i) {
   return tile_t{0, i * p.size, min(p.size, p.Tn - i * p.size), 0};
 }
 __device__ __forceinline__ slot_t slot_at(const route_t& p, int32_t i) {
-  if (p.order) return i < p.count[1] ? p.slot[i] : slot_t{0, 0, 0, 0};
+  if (p.order) return i < p.count[1] ? p.slot[i] : slot_t{0, 0, -1, 0};
   const int32_t tiles = (p.Tn + p.size - 1) / p.size;
   return slot_t{0, i * p.slot_tiles, min(p.slot_tiles, tiles - i * p.slot_tiles),
                 tiles > p.slot_tiles ? i : -1};
@@ -471,7 +495,7 @@ __global__ __launch_bounds__(1024) void k_lora_route(const int32_t* __restrict__
     if (g < G)
       for (int32_t q = 0; q < nw; ++q) n += cnt[q * G + g];
     const int32_t nt = (n + size - 1) / size;
-    const int32_t ns = g < L ? (nt + slot_tiles - 1) / slot_tiles : 0;
+    const int32_t ns = g < L ? max(1, (nt + slot_tiles - 1) / slot_tiles) : 0;
     four_t total;
     four_t b = scan_four(four_t{{n, nt, ns, ns > 1 ? ns : 0}}, lds, total);
 #pragma unroll
@@ -616,7 +640,7 @@ __device__ __forceinline__ bool self_route(const lora_dev& d, const route_t& p, 
     int32_t ns[2], at = before, slots, parts;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      ns[h] = 2 * t + h < d.L ? (nt[h] + p.slot_tiles - 1) / p.slot_tiles : 0;
+      ns[h] = 2 * t + h < d.L ? max(1, (nt[h] + p.slot_tiles - 1) / p.slot_tiles) : 0;
     const int32_t np[2] = {ns[0] > 1 ? ns[0] : 0, ns[1] > 1 ? ns[1] : 0};
     int32_t bs = block_excl_scan_i32<WAVES * 64>(ns[0] + ns[1], scan, &slots);
     int32_t bp = block_excl_scan_i32<WAVES * 64>(np[0] + np[1], scan, &parts);
@@ -1248,7 +1272,7 @@ __global__ __launch_bounds__(grad_waves(NR) * 64, NR == 1 ? 4 : 2) void k_lora_g
   const bool first = b < blocks0;
   const grad_arg<T>& q = first ? q0 : q1;
   const slot_t sl = slot_at(p, blockIdx.y);
-  if (sl.n <= 0) return;
+  if (sl.n < 0) return;
   const int32_t c0 = (b - (first ? 0 : blocks0)) * CW, col = c0 + c * E;
   const int32_t NT = (d.R + 15) / 16, rt0 = blockIdx.z * NR, nt = (rank_of(d, sl.l) + 15) / 16;
   f4 acc[NR][E];
@@ -1306,8 +1330,8 @@ __global__ __launch_bounds__(grad_waves(NR) * 64, NR == 1 ? 4 : 2) void k_lora_g
   }
 }
 
-// The gradients of adapters without a slot (zeros) or with several (the sum of
-// their partial sums, in slot order).  grid: adapters x shares of the elements
+// The gradients of adapters with several slots: the sum of their partial sums,
+// in slot order.  grid: adapters x shares of the elements
 // of dA (blocks0 of them), then of dB.
 template <typename T>
 __global__ __launch_bounds__(256) void k_lora_join(lora_dev d, route_t p, int32_t slots,
@@ -1377,7 +1401,7 @@ plan_t plan_of(const snack_lora* p, snack_dtype dt, int32_t T, bool backward) {
   // long as those are under way together (300 tokens of one adapter of rank 16,
   // 4096 to 4096: 8.8 us, 11.3 us with tiles of 32).
   if (tiles_guess(p->L, T, TILE) * std::min<int64_t>(8, cdiv(backward ? p->K : p->M, 512)) <
-          (backward ? 64 : 256) &&
+          256 &&
       (w.NT < 3 || tiles_guess(p->L, T, 16) <= 256))
     w.size = 16;
   w.whole = (int32_t)cdiv(T, w.size);
@@ -1394,10 +1418,10 @@ plan_t plan_of(const snack_lora* p, snack_dtype dt, int32_t T, bool backward) {
   const int64_t runs = std::max<int64_t>(1, cdiv(4096 / gw, blocks));
   const int32_t even = (int32_t)cdiv(w.whole, runs);  // tiles of a slot, all slots alike
   w.slot_tiles = w.tw == 1    ? (int32_t)std::max<int64_t>(16, cdiv(w.whole, 32))
-                 : p->L == 1 ? std::max(gw, even)
+                 : p->L == 1 ? (w.whole <= 4 * gw ? std::max(w.whole, 1) : std::max(gw, even))
                              : 2 * std::max(gw, even);  // few adapters have more than one
   w.slots = p->L == 1 ? (int32_t)cdiv(w.whole, w.slot_tiles)
-                      : (int32_t)std::min<int64_t>(w.tiles, w.whole / w.slot_tiles + p->L);
+                      : w.whole / w.slot_tiles + p->L;
   // an adapter with several slots has more than slot_tiles tiles, so its
   // slots are at most three times its share of the tokens
   w.part_slots = p->L == 1 ? w.slots
@@ -1521,12 +1545,19 @@ template <typename T>
 void run_fwd(const snack_lora* p, const lora_dev& d, const int32_t* ids, int32_t Tn, const void* X,
              int64_t ldx, const void* base, int64_t ldb, void* Y, int64_t ldy, float* t, char* ws,
              snack_dtype dt, hipStream_t s) {
-  if (Tn <= FEW_TOKENS) {
+  if (Tn <= FEW_TOKENS && p->K >= EL<T> && p->M >= EL<T>) {
     const int32_t blocks = (int32_t)cdiv(p->M, 64 * EL<T>);
-    const int32_t split = std::max(1, std::min(blocks, 256 / Tn));
+    // About one workgroup on every CU at most (37 tokens, 4096 to 11008, ranks 8
+    // to 32: 10.9 us; 20 us with two), and two ranks at least for each wave.
+    const int32_t most = std::max(1, 256 / Tn);
+    int32_t log_nb = 0;
+    while (log_nb < 4 && (1 << log_nb) < blocks &&
+           ((most << log_nb) < blocks || (2 * FEW_WAVES >> log_nb) > p->R))
+      ++log_nb;
+    const int32_t split = (int32_t)std::min<int64_t>(cdiv(blocks, 1 << log_nb), most);
     const int32_t rows = Tn < NUM_XCD ? Tn : (int32_t)(cdiv(Tn, NUM_XCD) * NUM_XCD);
     hipLaunchKernelGGL(k_lora_few<T>, dim3((unsigned)(rows * split)), dim3(FEW_WAVES * 64), 0, s, d,
-                       ids, Tn, split, (const T*)p->A, p->K, (const T*)X, ldx, (const T*)p->B, p->M,
+                       ids, Tn, split, log_nb, (const T*)p->A, p->K, (const T*)X, ldx, (const T*)p->B, p->M,
                        (const T*)base, ldb, (T*)Y, ldy, t);
     return;
   }
@@ -1567,7 +1598,7 @@ void run_bwd(const snack_lora* p, const lora_dev& d, const int32_t* ids, const f
     hipLaunchKernelGGL(kernel, grid, dim3(gw * 64), lds, s, d, r, qa, qb, na, na + nb, w.tw, mask);
   }
   const int32_t slots = Tn > 0 ? w.slots : 0;
-  if (p->L == 1 && slots == 1) return;
+  if (Tn > 0 && w.whole <= w.slot_tiles) return;  // one slot for each
   // workgroups for about 2,048 of them to be under way, the adapters' alike
   auto shares = [&](int32_t F) {
     return (int32_t)std::min<int64_t>(cdiv((int64_t)p->R * F, 1024), cdiv(2048, p->L));
