@@ -141,6 +141,67 @@ def test_gradients(size, dt):
     assert torch.equal(snk.lora_bwd(*args, t=t, want=(False, False, True))[2], dB)
 
 
+# More tokens than a workgroup sorts itself, more adapters than it counts, and
+# long or lopsided runs of one adapter, whose gradients are summed in parts.
+MANY = [(9000, 40, 72, 3, 8, "mixed"), (8300, 72, 40, 40, 20, "runs"), (20011, 24, 136, 5, 40, "1"),
+        (300, 48, 64, 1500, 4, "mixed"), (100, 16, 24, 8192, 3, "mixed"),
+        (2500, 264, 80, 9, 24, "4"), (8192, 64, 64, 2, 16, "mixed"), (6000, 136, 264, 1, 40, "0")]
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("size", MANY, ids=str)
+def test_many_tokens_and_many_adapters(size, dt):
+    *sizes, order = size
+    s = make(*sizes, dt, seed=sum(sizes), ids=order)
+    s["ids"][5] = -1
+    ref, tol = reference(s, dt, grads=True)
+    args = (s["ids"], s["A"], s["B"], s["scale"], s["ranks"])
+    t = torch.full((sizes[0], sizes[4]), float("nan"), device="cuda")
+    y = snk.lora_fwd(s["x"], *args, s["base"], t=t)
+    close(t, ref["t"], tol["t"], "t")
+    close(y, ref["y"], tol["y"], "y")
+    for kept in (t, None):
+        got = snk.lora_bwd(s["dy"], s["x"], *args, t=kept, base=s["gbase"])
+        for k, v in zip(("dx", "dA", "dB"), got):
+            close(v, ref[k], tol[k], k)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("K,M", [(3, 200), (200, 3), (7, 7), (8, 9), (63, 65), (127, 130), (66, 191)])
+@pytest.mark.parametrize("T", [2, 90, 260])
+def test_narrow_features(T, K, M, dt):
+    """Rows shorter than a piece or a block, and last pieces and blocks that
+    overlap the ones before them."""
+    s = make(T, K, M, 2, 20, dt, seed=T + K + M)
+    ref, tol = reference(s, dt, grads=True)
+    args = (s["ids"], s["A"], s["B"], s["scale"], s["ranks"])
+    z = s["base"].clone()
+    snk.lora_fwd(s["x"], *args, z, out=z)
+    close(z, ref["y"], tol["y"], "y in place")
+    g = s["gbase"].clone()
+    _, dA, dB = snk.lora_bwd(s["dy"], s["x"], *args, base=g, out=g)
+    for k, v in (("dx", g), ("dA", dA), ("dB", dB)):
+        close(v, ref[k], tol[k], k)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,R,r", [(3, 8, 5), (100, 16, 9), (100, 64, 33), (600, 40, 24)])
+def test_infinity_in_the_last_rank(T, R, r, dt):
+    """A rank count inside a step of the products: what stands in for the ranks
+    past it adds nothing, not even to an infinite sum."""
+    s = make(T, 72, 80, 1, R, dt, seed=T + r, ids="0", ranks=False)
+    s["ranks"] = torch.tensor([r], dtype=torch.int32, device="cuda")
+    s["A"], s["x"] = s["A"].abs() + 0.01, s["x"].abs() + 0.01
+    s["B"][0, r - 1, 7] = float("inf")
+    y = snk.lora_fwd(s["x"], s["ids"], s["A"], s["B"], s["scale"], s["ranks"], s["base"])
+    assert (y[:, 7] == float("inf")).all()
+    keep = torch.arange(80, device="cuda") != 7
+    assert torch.isfinite(y[:, keep]).all()
+
+
 @gpu
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("ids", ["runs", "0", "-1", "2"])
@@ -403,6 +464,59 @@ def test_module_and_autograd():
     m(x.detach(), ids).backward(gy)
     close(m.B.grad, ref["dB"], tol["dB"], "dB alone")
     assert m.A.grad is None
+
+
+@gpu
+def test_a_training_step_captured_into_a_graph():
+    """Forward, backward and clipping of the module in one graph, with no eager
+    graph of the same parameters alive while it is captured."""
+    torch.manual_seed(1)
+    m = snk.LoraAdapters(96, 80, 3, 8, dtype=torch.bfloat16)
+    with torch.no_grad():
+        m.B.normal_(std=0.1)
+    x = torch.randn(200, 96, device="cuda").bfloat16()
+    ids = torch.randint(-1, 3, (200,), device="cuda").int()
+    gy = torch.randn(200, 80, device="cuda").bfloat16()
+
+    def step():
+        m(x, ids).backward(gy)
+        norm = snk.clip_grad_norm_(m.parameters(), 0.5)
+        return norm
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    m.zero_grad(set_to_none=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm = step()
+    kept = m.A.grad, m.B.grad
+    for k in range(3):
+        x.copy_(torch.randn(200, 96, device="cuda"))
+        ids.copy_(torch.randint(-1, 3, (200,), device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [v.clone() for v in (norm, *kept)]
+        t = torch.empty(200, 8, device="cuda")
+        snk.lora_fwd(x, ids, m.A.detach(), m.B.detach(), m.scale, t=t)
+        _, dA, dB = snk.lora_bwd(gy, x, ids, m.A.detach(), m.B.detach(), m.scale, t=t)
+        want = snk.clip_grads([dA, dB], 0.5)
+        for p, q in zip(got, (want, dA, dB)):
+            assert torch.equal(p, q), k
+
+
+@gpu
+def test_example():
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(__file__), "..", "examples"))
+    import adapters
+    first, last = adapters.finetune(steps=30)
+    assert last < 0.5 * first
+    adapters.serve()
 
 
 # ------------------------------------------------------------------ refusals
