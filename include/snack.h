@@ -592,8 +592,8 @@ SNACK_API snack_status snack_conv1x1(const snack_plan* plan, const void* vals, s
  * for ranks it does not have.  dX must not overlap X or dY.
  *
  * snack_lora_workspace: bytes of ws for T tokens (backward 0 or 1).
- * Both calls are asynchronous, allocate nothing, use no atomics and give the
- * same bits for the same inputs.  Errors: SNACK_E_NULL, SNACK_E_DTYPE,
+ * Both calls are asynchronous, allocate nothing, add no floats by atomics and
+ * give the same bits for the same inputs.  Errors: SNACK_E_NULL, SNACK_E_DTYPE,
  * SNACK_E_SHAPE (sizes, strides, overlap), SNACK_E_OVERFLOW (M or K > 2^23,
  * T within 64 of 2^31), SNACK_E_WORKSPACE.
  */
