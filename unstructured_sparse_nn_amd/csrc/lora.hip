@@ -413,7 +413,8 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void k_lora_few(
 
 // ------------------------------------------------------- tokens in adapter order
 // A tile is a run of up to `size` (16 or 32) tokens of one adapter in that
-// order; group L holds the tokens without an adapter.  A slot is a run of tiles
+// order, which gives tile i the places from i * size on; group L holds the
+// tokens without an adapter.  A slot is a run of tiles
 // of one adapter whose gradient is summed in one go; the slots of an adapter
 // that has several leave partial sums at `part`, part + 1, ...; an adapter
 // without tokens has one slot of no tiles.
@@ -559,7 +560,7 @@ __global__ __launch_bounds__(1024) void k_lora_route(const int32_t* __restrict__
         slot[b.v[2] + k] = slot_t{g, b.v[1] + k * slot_tiles,
                                   min(slot_tiles, nt - k * slot_tiles), ns > 1 ? b.v[3] + k : -1};
       if (g < L) join[g] = join_t{ns, b.v[3]};
-      int32_t at = b.v[0];
+      int32_t at = b.v[1] * size;
       for (int32_t q = 0; q < nw; ++q) {
         const int32_t c = cnt[q * G + g];
         cnt[q * G + g] = at;
@@ -582,7 +583,7 @@ __global__ __launch_bounds__(1024) void k_lora_route(const int32_t* __restrict__
       else hi = mid;
     }
     const int32_t at = first[lo] + (i - first_tile[lo]) * size;
-    tile[i] = tile_t{lo, at, min(size, first[lo + 1] - at), 0};
+    tile[i] = tile_t{lo, i * size, min(size, first[lo + 1] - at), 0};
   }
 }
 
@@ -646,7 +647,7 @@ constexpr int32_t SELF_TOKENS = 8192, SELF_GROUPS = 1024;
 constexpr size_t SELF_BYTES = 4 * (SELF_GROUPS + WAVES + 4 + WAVES);
 
 struct tables_t {  // what the gradients need of it; all NULL: nothing
-  int32_t* order;  // tile i's tokens at i * TILE
+  int32_t* order;  // tile i's tokens from i * size on
   tile_t* tile;
   slot_t* slot;
   join_t* join;
@@ -717,7 +718,7 @@ __device__ __forceinline__ bool self_route(const lora_dev& d, const route_t& p, 
   }
   __syncthreads();
   const int32_t g = found[0], k = found[1];
-  tl = tile_t{g, ti * TILE, min(p.size, found[2] - k * p.size), 0};
+  tl = tile_t{g, ti * p.size, min(p.size, found[2] - k * p.size), 0};
   int32_t m = 0;
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
@@ -738,7 +739,7 @@ __device__ __forceinline__ bool self_route(const lora_dev& d, const route_t& p, 
   }
   __syncthreads();
   if (out.order && role == 0) {
-    if (t < TILE) out.order[ti * TILE + t] = tk.row[min(t, tl.n - 1)];
+    if (t < p.size) out.order[ti * p.size + t] = tk.row[min(t, tl.n - 1)];
     if (t == 0) out.tile[ti] = tl;
   }
   return true;
@@ -1232,15 +1233,17 @@ __device__ __forceinline__ void grad_sum(const route_t& p, const grad_arg<T>& q,
   const int l = lane_id(), c = l & 15, g = l >> 4;
   const int32_t left = q.K - col;
   const T* X = q.X + col;
-  auto fetch = [&](int32_t ti, frag<T> (&rows)[8]) {
-    const tile_t tl = tile_at(p, ti);
+  // has: which of the tile's tokens count.
+  auto fetch = [&](int32_t ti, frag<T> (&rows)[8], uint32_t& has) {
+    const int32_t n = tile_at(p, ti).n;
+    has = mask[ti];
     int32_t row[8];
     if (p.order) {
-      // The tile's tokens come as scalars (`order` goes on for a tile past its
-      // last token): loads of theirs among the rows' would have to be waited
-      // for together with them.
+      // The tile's tokens come as scalars (`order` goes on for a tile past the
+      // last place): loads of theirs among the rows' would have to be waited for
+      // together with them.
       int32_t all[TILE];
-      __builtin_memcpy(all, p.order + tl.begin, sizeof(all));
+      __builtin_memcpy(all, p.order + ti * p.size, sizeof(all));
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int32_t a = pick(g & 1, all[8 + k], all[k]), b = pick(g & 1, all[24 + k], all[16 + k]);
@@ -1248,11 +1251,11 @@ __device__ __forceinline__ void grad_sum(const route_t& p, const grad_arg<T>& q,
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) row[k] = tl.begin + 8 * g + k;
+      for (int k = 0; k < 8; ++k) row[k] = ti * p.size + 8 * g + k;
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int64_t at = 8 * g + k < tl.n ? row[k] : 0;
+      const int64_t at = 8 * g + k < n ? row[k] : 0;
       if constexpr (FULL) rows[k] = load_frag(X + at * q.ldx);
       else rows[k] = load_frag(X + at * q.ldx, left, q.K);
     }
@@ -1277,8 +1280,7 @@ __device__ __forceinline__ void grad_sum(const route_t& p, const grad_arg<T>& q,
       }
     }
   };
-  auto use = [&](int32_t ti, frag<T> (&rows)[8], const uint32_t (&t)[NR][PN]) {
-    const uint32_t has = mask[ti];
+  auto use = [&](uint32_t has, frag<T> (&rows)[8], const uint32_t (&t)[NR][PN]) {
     if (has != ~0u)
 #pragma unroll
       for (int k = 0; k < 8; ++k) rows[k] = keep_if((has >> (8 * g + k)) & 1, rows[k]);
@@ -1334,17 +1336,18 @@ __device__ __forceinline__ void grad_sum(const route_t& p, const grad_arg<T>& q,
   };
   if (h >= sl.n || rt0 >= nt) return;
   frag<T> now[8], next[8];
-  uint32_t t[NR][PN];
-  fetch(sl.tile + h, now);
+  uint32_t t[NR][PN], has_now, has_next;
+  fetch(sl.tile + h, now, has_now);
   for (; h + tw < sl.n; h += tw) {
     fetch_pack(sl.tile + h, t);  // before the next rows: waiting for it does not wait for them
-    fetch(sl.tile + h + tw, next);
-    use(sl.tile + h, now, t);
+    fetch(sl.tile + h + tw, next, has_next);
+    use(has_now, now, t);
 #pragma unroll
     for (int k = 0; k < 8; ++k) now[k] = next[k];
+    has_now = has_next;
   }
   fetch_pack(sl.tile + h, t);
-  use(sl.tile + h, now, t);
+  use(has_now, now, t);
 }
 
 template <typename T, int NR>
@@ -1456,7 +1459,7 @@ snack_status check_lora(const snack_lora* p, snack_dtype dt, int32_t T) {
   if (p->M < 1 || p->K < 1 || p->L < 1 || p->L > MAX_ADAPTERS || p->R < 1 || p->R > MAX_RANK ||
       T < 0)
     return SNACK_E_SHAPE;
-  if (T > INT32_MAX - 64 || p->M > MAX_FEATURES || p->K > MAX_FEATURES) return SNACK_E_OVERFLOW;
+  if (T > INT32_MAX - (1 << 20) || p->M > MAX_FEATURES || p->K > MAX_FEATURES) return SNACK_E_OVERFLOW;
   return SNACK_OK;
 }
 
@@ -1495,19 +1498,23 @@ plan_t plan_of(const snack_lora* p, snack_dtype dt, int32_t T, bool backward) {
   w.tiles = p->L == 1 ? w.whole : (int32_t)std::min<int64_t>(T, (int64_t)T / w.size + p->L + 1);
   w.blocksA = (int32_t)cdiv(p->K, 16 * e);
   w.blocksB = (int32_t)cdiv(p->M, 16 * e);
-  // One wave sums a slot where adapters and columns make waves enough, or
-  // adapters have too few tiles to share; elsewhere the waves of a workgroup
-  // share it.
+  // The waves of a workgroup share a slot where all workgroups are under way
+  // together, for tokens may all have one adapter (164 fp32 tokens that do, of 7,
+  // 2344 to 2525: 63 us with one wave a slot, 28 us shared), and where adapters
+  // have tiles enough for all waves.  Elsewhere one wave sums it alone (300
+  // tokens of 16 adapters of rank 64, 4096 to 4096: 8 us, 35 us shared).
   const int32_t gw = grad_waves(w.NT), users = std::max(1, std::min(p->L, w.whole));
   const int64_t blocks = w.blocksA + w.blocksB, alone = blocks * users * cdiv(w.NT, 2);
   const int32_t per = w.whole / users;  // tiles of an adapter
-  w.tw = alone < 4096 && (per >= 2 * gw || (alone < 1024 && per >= 3)) ? gw : 1;
+  w.tw = w.whole > 1 && (alone <= 1024 || (alone < 4096 && per >= 2 * gw)) ? gw : 1;
   const int64_t runs = std::max<int64_t>(1, cdiv(4096 / gw, blocks));
   const int32_t even = (int32_t)cdiv(w.whole, runs);  // tiles of a slot, all slots alike
-  // Few tiles: one slot for each adapter, which needs no joining (1,024 tokens of
-  // 4 adapters, 768 to 2304, fp32: 28.5 us with it, 27.2 us without; 1,000 of 8:
-  // 28.2 us and 23.1 us).
-  if (w.tw > 1 && w.whole <= 8 * gw) w.slot_tiles = std::max(w.whole, 1);
+  // About one tile for each wave (four, where there is one adapter alone): one
+  // slot for each adapter, which needs no joining (1,000 tokens of 8 adapters, 768
+  // to 2304, fp32: 28.2 us with it, 23.1 us without; 1,024 of 4, lopsided: 26.8 us
+  // and 28.2 us).
+  if (w.tw > 1 && (p->L == 1 ? w.whole <= 4 * gw : w.whole <= 8 * gw && per <= gw))
+    w.slot_tiles = std::max(w.whole, 1);
   else if (w.tw > 1) w.slot_tiles = std::max(gw, even) * (p->L == 1 ? 1 : 2);
   else w.slot_tiles = (int32_t)std::max<int64_t>(16, cdiv(w.whole, 32));
   w.slots = p->L == 1 ? (int32_t)cdiv(w.whole, w.slot_tiles)
@@ -1541,7 +1548,7 @@ plan_t plan_of(const snack_lora* p, snack_dtype dt, int32_t T, bool backward) {
   w.ksK = cut(p->K);
   w.ksM = cut(p->M);
   if (p->L > 1 && (backward || !w.self || w.two)) {
-    w.order = take(4 * ((w.self ? (size_t)w.tiles * TILE : (size_t)T) + TILE));
+    w.order = take(4 * ((size_t)w.tiles * w.size + TILE));
     w.tile = take(sizeof(tile_t) * (size_t)w.tiles);
     w.slot = take(sizeof(slot_t) * (size_t)w.slots);
     w.join = take(sizeof(join_t) * (size_t)p->L);
