@@ -1335,8 +1335,18 @@ __device__ __forceinline__ void grad_sum(const route_t& p, const grad_arg<T>& q,
     }
   };
   if (h >= sl.n || rt0 >= nt) return;
-  frag<T> now[8], next[8];
-  uint32_t t[NR][PN], has_now, has_next;
+  frag<T> now[8];
+  uint32_t t[NR][PN], has_now;
+  if constexpr (!FULL) {  // the last columns: no registers for a second tile's rows
+    for (; h < sl.n; h += tw) {
+      fetch_pack(sl.tile + h, t);
+      fetch(sl.tile + h, now, has_now);
+      use(has_now, now, t);
+    }
+    return;
+  }
+  frag<T> next[8];
+  uint32_t has_next;
   fetch(sl.tile + h, now, has_now);
   for (; h + tw < sl.n; h += tw) {
     fetch_pack(sl.tile + h, t);  // before the next rows: waiting for it does not wait for them
