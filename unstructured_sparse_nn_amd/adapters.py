@@ -57,7 +57,12 @@ class LoraAdapters(torch.nn.Module):
 
     A starts normal with standard deviation 1/sqrt(in_features), B at zero, so
     an untrained adapter changes nothing.  ``ranks`` (a list) may give each
-    adapter its own rank up to ``rank``; ``alpha / rank`` is the scale."""
+    adapter its own rank up to ``rank``; ``alpha / rank`` is the scale.
+
+    Forward and backward can be captured into a graph.  As with any torch
+    module, no output of an eager step may still hold these parameters' autograd
+    graph while the backward is captured: torch would join the eager stream to
+    the capture and end the process."""
 
     def __init__(self, in_features: int, out_features: int, adapters: int, rank: int,
                  alpha: float = 16.0, ranks=None, dtype=torch.float32, device="cuda"):
