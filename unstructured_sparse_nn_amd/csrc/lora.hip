@@ -1374,7 +1374,8 @@ __global__ __launch_bounds__(grad_waves(NR) * 64, NR == 1 ? 4 : 2) void k_lora_g
   const slot_t sl = slot_at(p, blockIdx.y);
   if (sl.n < 0) return;
   const int32_t c0 = (b - (first ? 0 : blocks0)) * CW, col = c0 + c * E;
-  const int32_t NT = (d.R + 15) / 16, rt0 = blockIdx.z * NR, nt = (rank_of(d, sl.l) + 15) / 16;
+  const int32_t r = rank_of(d, sl.l);
+  const int32_t NT = (d.R + 15) / 16, rt0 = blockIdx.z * NR, nt = (r + 15) / 16;
   f4 acc[NR][E];
 #pragma unroll
   for (int j = 0; j < NR; ++j)
@@ -1383,8 +1384,12 @@ __global__ __launch_bounds__(grad_waves(NR) * 64, NR == 1 ? 4 : 2) void k_lora_g
   const int32_t h = tw == 1 ? 0 : w;
   if (c0 + CW <= q.K) grad_sum<T, NR, true>(p, q, sl, NT, nt, rt0, col, h, tw, mask, acc);
   else grad_sum<T, NR, false>(p, q, sl, NT, nt, rt0, col, h, tw, mask, acc);
-  auto put = [&](int32_t rank, int32_t m, const float (&v)[E]) {
+  auto put = [&](int32_t rank, int32_t m, float (&v)[E]) {
     if (rank >= d.R || m >= q.K) return;
+    // The products gave a rank that the adapter lacks zeros times the rows: NaN
+    // where those are infinite or NaN.
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = rank < r ? v[e] : 0.f;
     if (sl.part < 0) {
       store_frag(q.dF + ((int64_t)sl.l * d.R + rank) * q.K + m, to_frag(v), q.K - m);
     } else {
