@@ -67,3 +67,37 @@ def test_infinities_in_the_gradients(case, where, dt):
             assert int(dA[l, r:].count_nonzero()) == 0 == int(dB[l, r:].count_nonzero()), (l, r)
         same_pattern(dA, want["dA"], ref["dA"], tol["dA"], "dA")
         same_pattern(dB, want["dB"], ref["dB"], tol["dB"], "dB")
+
+
+@gpu
+@pytest.mark.parametrize("T", [5, 100])
+def test_written_tensors_count_as_changed(T):
+    """What a call writes into its caller's tensors moves their version, so that
+    a backward that has saved them raises instead of using the new values."""
+    s = make(T, 24, 24, 2, 8, "f32", seed=T, ranks=False)
+    args = (s["ids"], s["A"], s["B"])
+
+    def saved(n):  # sigmoid's backward uses its output
+        return torch.sigmoid(torch.zeros(T, n, device="cuda", requires_grad=True))
+
+    calls = [(24, lambda v: snk.lora_fwd(s["x"], *args, base=v, out=v)),
+             (24, lambda v: snk.lora_fwd(s["x"], *args, out=v)),
+             (8, lambda v: snk.lora_fwd(s["x"], *args, t=v)),
+             (24, lambda v: snk.lora_bwd(s["dy"], s["x"], *args, base=v, out=v)),
+             (24, lambda v: snk.lora_bwd(s["dy"], s["x"], *args, out=v, want=(True, False, False)))]
+    for n, call in calls:
+        v = saved(n)
+        version = v._version
+        with torch.no_grad():
+            call(v)
+        assert v._version > version
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            v.sum().backward()
+    v = saved(24)  # only read: as before
+    with torch.no_grad():
+        snk.lora_fwd(s["x"], *args, base=v)
+        snk.lora_bwd(s["dy"], s["x"], *args, base=v)
+    v.sum().backward()
+    with torch.inference_mode():  # has no versions
+        v = torch.zeros(T, 24, device="cuda")
+        assert snk.lora_fwd(s["x"], *args, out=v) is v

@@ -19,7 +19,8 @@ def lora_fwd(x, ids, A, B, scale=None, ranks=None, base=None, out=None, t=None):
 
     x (T, K); base (T, M) or None; out (T, M), may be base; t (T, R) float32
     receives ``x @ A[a].T`` for :func:`lora_bwd`.  Rows of x, base and out may
-    be strided."""
+    be strided.  Autograd does not record this call (:class:`LoraAdapters` does);
+    out and t count as changed in place."""
     return calls().lora_fwd(x, ids, A, B, scale, ranks, base, out, t)
 
 
@@ -29,7 +30,8 @@ def lora_bwd(dy, x, ids, A, B, scale=None, ranks=None, t=None, base=None, out=No
 
     t: what the forward stored (computed again without it).  base (T, K): the
     shared projection's input gradient, added to dx.  out (T, K) receives dx
-    and may be base.  want: which of the three to compute (None for others)."""
+    and may be base, and counts as changed in place.  want: which of the three to
+    compute (None for others).  Autograd does not record this call."""
     return calls().lora_bwd(dy, x, ids, A, B, scale, ranks, t, base, out, *want)
 
 

@@ -72,6 +72,12 @@ Tensor bytes_on(const Tensor& like, size_t n) {
   return at::empty({(int64_t)n}, like.options().dtype(at::kByte));
 }
 
+// t has been written past torch: autograd has to know (inference tensors have
+// no version).
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // Calls f without the interpreter's lock.
 template <typename F> snack_status unlocked(F f) {
   snack_status st;
@@ -184,6 +190,8 @@ PyObject* lora_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 need, s);
           }),
           "snack_lora_fwd");
+    if (a[7] != Py_None) written(out);
+    if (t.defined()) written(t);
     return wrap(out);
   });
 }
@@ -225,6 +233,7 @@ PyObject* lora_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 base.ld, ptr(dx), lddx, ptr(dA), ptr(dB), ptr(ws), need, s);
           }),
           "snack_lora_bwd");
+    if (want_dx && a[9] != Py_None) written(dx);
     PyObject* r = PyTuple_New(3);
     if (!r) throw refused();
     PyTuple_SET_ITEM(r, 0, wrap(dx));
@@ -308,12 +317,9 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
                          : lib.grad_norm(tab.data(), count, (float*)ptr(norm), ptr(ws), need, s);
           }),
           scale ? "snack_grad_clip" : "snack_grad_norm");
-    if (scale) {  // written past torch: autograd has to know
-      const list_t& written = outs ? *outs : grads;
-      for (Py_ssize_t i = 0; i < written.size(); ++i) {
-        const Tensor& t = written[i];
-        if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
-      }
+    if (scale) {
+      const list_t& to = outs ? *outs : grads;
+      for (Py_ssize_t i = 0; i < to.size(); ++i) written(to[i]);
     }
     return wrap(norm);
   });
