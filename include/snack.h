@@ -578,8 +578,7 @@ SNACK_API snack_status snack_conv1x1(const snack_plan* plan, const void* vals, s
  *     Y[i, m] = base[i, m] + s_a sum_j t[i, j] B[a, j, m]
  * one rounding to the output type.  base (nullable: zeros) is the shared
  * projection's output and may be Y itself (same stride).  t (nullable,
- * T x R floats, contiguous) receives t for snack_lora_bwd.  X and Y must not
- * overlap.
+ * T x R floats, contiguous) receives t for snack_lora_bwd.
  *
  * snack_lora_bwd: with u[i, j] = sum_m B[a, j, m] dY[i, m],
  *     dX[i, k] = base[i, k] + s_a sum_j u[i, j] A[a, j, k]
@@ -589,7 +588,11 @@ SNACK_API snack_status snack_conv1x1(const snack_plan* plan, const void* vals, s
  * itself.  Any of dX, dA, dB may be NULL (not wanted).  t (nullable) is what
  * the forward stored; without it t is computed again.  dA and dB (L x R x K,
  * L x R x M) are overwritten, with zeros where an adapter has no token or
- * for ranks it does not have.  dX must not overlap X or dY.
+ * for ranks it does not have.
+ *
+ * Y, t, dX, dA and dB must not share memory with each other or with an input
+ * (except Y or dX with base, if it is base); rows of one may lie between
+ * another's.
  *
  * snack_lora_workspace: bytes of ws for T tokens (backward 0 or 1).
  * Both calls are asynchronous, allocate nothing, add no floats by atomics and

@@ -2,10 +2,14 @@
 the gradients, outputs that other tensors share, moves of the module between
 types, sizes past what a launch holds.  Formulas and tolerances are those of
 the adapters' other tests."""
+import ctypes
+import random
+
 import pytest
 import torch
 
 import unstructured_sparse_nn_amd as snk
+from unstructured_sparse_nn_amd import binding as b
 from test_lora import close, make, reference
 
 gpu = pytest.mark.gpu
@@ -101,3 +105,85 @@ def test_written_tensors_count_as_changed(T):
     with torch.inference_mode():  # has no versions
         v = torch.zeros(T, 24, device="cuda")
         assert snk.lora_fwd(s["x"], *args, out=v) is v
+
+
+# Addresses far apart: nothing here is read, for every call is refused.
+PLACES = dict(X=1 << 30, Y=2 << 30, base=3 << 30, A=4 << 30, B=5 << 30, ids=6 << 30, t=7 << 30,
+              scale=8 << 30, rank=9 << 30, ws=10 << 30, dA=11 << 30, dB=12 << 30, dX=13 << 30)
+SIZE = dict(T=40, K=64, M=32, L=2, R=8)  # fp32
+BYTES = dict(X=40 * 64 * 4, Y=40 * 32 * 4, base=40 * 32 * 4, A=2 * 8 * 64 * 4, B=2 * 8 * 32 * 4,
+             ids=40 * 4, t=40 * 8 * 4, scale=8, rank=8)
+
+
+def raw(which, **places):
+    """The status of a call with contiguous tensors at these addresses."""
+    p, z = {**PLACES, **places}, SIZE
+    bank = ctypes.byref(b.snack_lora(p["A"], p["B"], z["M"], z["K"], z["L"], z["R"], p["scale"],
+                                     p["rank"]))
+    end = (p["ws"], 1 << 30, None)
+    if which == "fwd":
+        return b.raw_status("snack_lora_fwd", bank, 0, p["ids"], z["T"], p["X"], z["K"], p["base"],
+                            z["M"], p["Y"], z["M"], p["t"], *end)
+    return b.raw_status("snack_lora_bwd", bank, 0, p["ids"], p["t"], z["T"], p["X"], z["K"], p["Y"],
+                        z["M"], p["base"], z["K"], p["dX"], z["K"], p["dA"], p["dB"], *end)
+
+
+@pytest.mark.parametrize("name", ["X", "base", "A", "B", "ids", "t", "scale", "rank"])
+def test_outputs_over_other_tensors_are_refused(name):
+    """The first or the last element of an output on another tensor's."""
+    at, n = PLACES[name], BYTES[name]
+    for start in (at + n - 4, at - BYTES["Y"] + 4, at + 4 if n > 8 else at):
+        assert raw("fwd", Y=start) == -2, (name, start - at)
+    if name != "t":
+        for start in (at + n - 4, at - BYTES["t"] + 4, at):
+            assert raw("fwd", t=start) == -2, (name, start - at)
+    n = BYTES["X"] if name == "base" else n  # the backward's base is like X
+    for out, size in (("dX", BYTES["X"]), ("dA", BYTES["A"]), ("dB", BYTES["B"])):
+        for start in (at + n - 4, at - size + 4):
+            assert raw("bwd", **{out: start}) == -2, (name, out, start - at)
+
+
+def test_outputs_over_outputs_are_refused():
+    assert raw("bwd", dA=PLACES["dB"] + BYTES["B"] - 4) == -2
+    assert raw("bwd", dA=PLACES["dX"]) == -2 and raw("bwd", dB=PLACES["dX"] + 4) == -2
+    assert raw("bwd", dX=PLACES["Y"] + 8) == -2            # over dY
+    assert raw("fwd", base=PLACES["Y"] + 32 * 4) == -2     # base a row further on
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("seed", range(4))
+def test_rows_beside_each_other_in_one_buffer(seed, dt):
+    """Rows of x and y anywhere in one buffer: a call is refused exactly where
+    an element belongs to both, and otherwise right."""
+    from test_lora import DT
+    rng = random.Random(seed)
+    T, K, M, L, R = 7, 12, 9, 2, 4
+    s = make(T, K, M, L, R, dt, seed=seed, ranks=False)
+    lora = b.snack_lora(s["A"], s["B"], M, K, L, R)
+    ws = torch.empty(b.snack_lora_workspace(lora, b._dtype(s["x"]), T), dtype=torch.uint8,
+                     device="cuda")
+    want = snk.lora_fwd(s["x"], s["ids"], s["A"], s["B"])
+    done = {True: 0, False: 0}
+    for _ in range(300):
+        ldx, ldy = rng.choice([(24, 24), (24, 24), (25, 25), (48, 24), (24, 31), (12, 9), (60, 60)])
+        ox, oy = rng.randrange(0, 300), rng.randrange(0, 300)
+        if rng.random() < 0.5:  # next to each other's rows
+            oy = ox + rng.choice([-1, 0, 1, 7, 8, 9, 10, 11, 12, 13, 14, 15, 16]) + ldx * rng.randrange(8)
+            oy = max(oy, 0)
+        over = bool({ox + i * ldx + k for i in range(T) for k in range(K)}
+                    & {oy + i * ldy + m for i in range(T) for m in range(M)})
+        buf = torch.zeros(1500, dtype=DT[dt], device="cuda")
+        x, y = buf[ox:].as_strided((T, K), (ldx, 1)), buf[oy:].as_strided((T, M), (ldy, 1))
+        x.copy_(s["x"])
+        kept = buf.clone()
+        try:
+            b.snack_lora_fwd(lora, s["ids"], T, x, ldx, None, M, y, ldy, ws=ws)
+        except snk.SnackError as e:
+            assert e.status == -2 and over, (ox, oy, ldx, ldy)
+            assert torch.equal(buf, kept)
+        else:
+            assert not over, (ox, oy, ldx, ldy)
+            assert torch.equal(y, want) and torch.equal(x, s["x"])
+        done[over] += 1
+    assert min(done.values()) > 50

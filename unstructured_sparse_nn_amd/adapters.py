@@ -19,8 +19,9 @@ def lora_fwd(x, ids, A, B, scale=None, ranks=None, base=None, out=None, t=None):
 
     x (T, K); base (T, M) or None; out (T, M), may be base; t (T, R) float32
     receives ``x @ A[a].T`` for :func:`lora_bwd`.  Rows of x, base and out may
-    be strided.  Autograd does not record this call (:class:`LoraAdapters` does);
-    out and t count as changed in place."""
+    be strided.  An out or t that shares memory with anything else is refused.
+    Autograd does not record this call (:class:`LoraAdapters` does); out and t
+    count as changed in place."""
     return calls().lora_fwd(x, ids, A, B, scale, ranks, base, out, t)
 
 
@@ -29,9 +30,10 @@ def lora_bwd(dy, x, ids, A, B, scale=None, ranks=None, t=None, base=None, out=No
     """Gradients (dx, dA, dB) of :func:`lora_fwd` from dy (T, M).
 
     t: what the forward stored (computed again without it).  base (T, K): the
-    shared projection's input gradient, added to dx.  out (T, K) receives dx
-    and may be base, and counts as changed in place.  want: which of the three to
-    compute (None for others).  Autograd does not record this call."""
+    shared projection's input gradient, added to dx.  out (T, K) receives dx, may
+    be base (an out that shares memory with anything else is refused) and counts
+    as changed in place.  want: which of the three to compute (None for others).
+    Autograd does not record this call."""
     return calls().lora_bwd(dy, x, ids, A, B, scale, ranks, t, base, out, *want)
 
 

@@ -1478,6 +1478,49 @@ snack_status check_lora(const snack_lora* p, snack_dtype dt, int32_t T) {
   return SNACK_OK;
 }
 
+// Memory of a call: n rows of `row` bytes, ld bytes apart (wide: sizes and
+// strides are the caller's).
+struct span_t {
+  __int128 p, row, ld, n;
+  span_t(const void* at, __int128 bytes, __int128 stride = 0, __int128 rows = 1)
+      : p((uintptr_t)at), row(bytes), ld(stride), n(at && bytes > 0 ? rows : 0) {
+    if (n > 1 && ld == row) row *= n, n = 1;
+  }
+  __int128 end() const { return p + (n - 1) * ld + row; }
+  // Whether a row meets the bytes from lo up to hi.
+  bool meets(__int128 lo, __int128 hi) const {
+    // the first row that ends past lo
+    const __int128 i = lo < p + row ? 0 : n == 1 ? 1 : (lo - row - p) / ld + 1;
+    return i < n && p + i * ld < hi;
+  }
+};
+
+// Whether a byte belongs to both.  Rows may lie between the other's rows.
+bool overlap(const span_t& a, const span_t& b) {
+  if (a.n == 0 || b.n == 0 || a.end() <= b.p || b.end() <= a.p) return false;
+  if (a.n > b.n) return overlap(b, a);
+  if (a.n > 1 && a.ld == b.ld) {  // row i of b begins `at` bytes after row i + q of a
+    const __int128 d = b.p - a.p, q = d >= 0 ? d / a.ld : -((a.ld - 1 - d) / a.ld), at = d - q * a.ld;
+    auto both = [&](__int128 k) { return std::max<__int128>(0, -k) < std::min(b.n, a.n - k); };
+    return (at < a.row && both(q)) || (at + b.row > a.ld && both(q + 1));
+  }
+  for (__int128 i = 0; i < a.n; ++i)
+    if (b.meets(a.p + i * a.ld, a.p + i * a.ld + a.row)) return true;
+  return false;
+}
+
+// Whether an output lies over an input or over another output.
+template <size_t O, size_t I>
+bool any_overlap(const span_t (&out)[O], const span_t (&in)[I]) {
+  for (size_t o = 0; o < O; ++o) {
+    for (const span_t& i : in)
+      if (overlap(out[o], i)) return true;
+    for (size_t q = 0; q < o; ++q)
+      if (overlap(out[o], out[q])) return true;
+  }
+  return false;
+}
+
 // Tokens up to which k_lora_few is taken.
 constexpr int32_t FEW_TOKENS = 64;
 
@@ -1745,6 +1788,12 @@ snack_status snack_lora_fwd(const snack_lora* lora, snack_dtype dtype, const int
   if (!lora->A || !lora->B || !ids || !X || !Y || !ws) return SNACK_E_NULL;
   if (Y == X || (Y == base && ldy != ldb)) return SNACK_E_SHAPE;
   if (ws_bytes < plan_of(lora, dtype, T, false).total) return SNACK_E_WORKSPACE;
+  const __int128 e = dtype == SNACK_BF16 ? 2 : 4, M = lora->M, K = lora->K, L = lora->L, R = lora->R;
+  const span_t out[] = {{Y, M * e, ldy * e, T}, {t, 4 * T * R}};
+  const span_t in[] = {{X, K * e, ldx * e, T}, {Y == base ? nullptr : base, M * e, ldb * e, T},
+                       {lora->A, L * R * K * e}, {lora->B, L * R * M * e},
+                       {lora->scale, 4 * L}, {lora->rank, 4 * L}, {ids, 4 * (__int128)T}};
+  if (any_overlap(out, in)) return SNACK_E_SHAPE;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const lora_dev d{lora->L, lora->R, lora->scale, lora->rank};
   if (dtype == SNACK_BF16)
@@ -1767,6 +1816,14 @@ snack_status snack_lora_bwd(const snack_lora* lora, snack_dtype dtype, const int
     if (dX && (dX == X || dX == dY || (dX == base && lddx != ldb))) return SNACK_E_SHAPE;
     if (ws_bytes < plan_of(lora, dtype, T, true).total) return SNACK_E_WORKSPACE;
   }
+  const __int128 e = dtype == SNACK_BF16 ? 2 : 4, M = lora->M, K = lora->K, L = lora->L, R = lora->R;
+  const span_t out[] = {{dX, K * e, lddx * e, T}, {dA, L * R * K * e}, {dB, L * R * M * e}};
+  const span_t in[] = {{X, K * e, ldx * e, T}, {dY, M * e, lddy * e, T},
+                       {dX == base ? nullptr : base, K * e, ldb * e, T},
+                       {lora->A, L * R * K * e}, {lora->B, L * R * M * e},
+                       {lora->scale, 4 * L}, {lora->rank, 4 * L}, {ids, 4 * (__int128)T},
+                       {t, 4 * T * R}};
+  if (any_overlap(out, in)) return SNACK_E_SHAPE;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const lora_dev d{lora->L, lora->R, lora->scale, lora->rank};
   if (dtype == SNACK_BF16)
