@@ -628,15 +628,16 @@ SNACK_API snack_status snack_lora_bwd(const snack_lora* lora, snack_dtype dtype,
  * `grads` is a host array of `count` entries, read before the call returns;
  * each tensor is n contiguous elements of its own dtype (any alignment, n may
  * be 0).  out NULL or equal to grad: in place; otherwise out must not overlap
- * any grad of the list.  Sums, norm and factor are held in 64 bits, so no
- * square overflows (a norm past the range of float is stored as infinity, and
- * the factor is still right).
+ * any grad of the list.  What is written must not overlap: no two outs, and no
+ * gradient twice where it is scaled in place.  Sums, norm and factor are held
+ * in 64 bits, so no square overflows (a norm past the range of float is stored
+ * as infinity, and the factor is still right).
  * NaN and infinities go by the formula: a NaN norm makes every output NaN, an
  * infinite one gives factor 0 (NaN where the gradient is infinite).
  * norm: device float (nullable in snack_grad_clip).  ws: device memory of
  * snack_grad_workspace(count) bytes.  Asynchronous; same bits for the same
  * inputs.  Errors: SNACK_E_NULL, SNACK_E_DTYPE, SNACK_E_SHAPE (n < 0,
- * max_norm < 0, eps < 0), SNACK_E_COUNT (count < 0), SNACK_E_OVERFLOW
+ * max_norm < 0, eps < 0, overlap), SNACK_E_COUNT (count < 0), SNACK_E_OVERFLOW
  * (n > 2^40), SNACK_E_NAN (max_norm or eps NaN), SNACK_E_WORKSPACE.
  */
 typedef struct snack_grad {

@@ -1,0 +1,75 @@
+"""Lists of gradients whose tensors share memory, and lists past 128 MB in every
+type and alignment.  Tolerances are those of clipping's other tests."""
+import random
+from array import array
+
+import pytest
+import torch
+
+import unstructured_sparse_nn_amd as snk
+from unstructured_sparse_nn_amd import binding as b
+from test_grad_clip import check, formula
+
+gpu = pytest.mark.gpu
+P = 1 << 30  # addresses that nothing reads: every call here is refused
+
+
+def raw(*rows):
+    tab = array("q", [v for r in rows for v in r])
+    return b.raw_status("snack_grad_clip", tab.buffer_info()[0], len(rows), 1.0, 0.0, 64, 64,
+                        1 << 30, None)
+
+
+@pytest.mark.parametrize("rows", [
+    [(P, P, 8, 0), (P, P, 8, 0)],                                # the same gradient twice
+    [(P, 0, 8, 0), (P, 0, 8, 0)],                                # the same with no outputs given
+    [(P + 28, P + 28, 4, 0), (P, P, 8, 0)],                      # one begins in another's last element
+    [(P, P + 4, 8, 0)],                                          # an output a step behind its gradient
+    [(P, 2 * P, 8, 0), (2 * P + 30, 3 * P, 8, 1)],               # over another entry's gradient
+    [(P, 3 * P, 8, 0), (2 * P, 3 * P + 28, 8, 0)],               # over another output
+    [(P, P, 8, 1), (2 * P, P + 14, 8, 1)],                       # over a gradient scaled in place
+    [(P + 64 * i, P + 64 * i, 16, 0) for i in range(300)] + [(P, P, 1, 1)],
+    [(P + 64 * i, 2 * P + 64 * i, 17, 0) for i in reversed(range(300))]], ids=range(9))
+def test_shared_memory_is_refused(rows):
+    assert raw(*rows) == -2
+    assert raw(*rows[::-1]) == -2
+
+
+@gpu
+def test_refused_where_tensors_share_memory_and_only_there():
+    """Gradients and outputs anywhere in one buffer, against the sets of their
+    elements."""
+    rng, done = random.Random(1), {True: 0, False: 0}
+    for _ in range(400):
+        buf = torch.randn(2000, generator=torch.Generator().manual_seed(5)).cuda()
+        n = [rng.choice([0, 1, 5, 40]) for _ in range(rng.randint(1, 6))]
+        at = [rng.randrange(900) for _ in n]
+        to = [a if rng.random() < 0.5 else rng.randrange(1900) for a in at]
+        grads = [buf[a:a + k] for a, k in zip(at, n)]
+        outs = [buf[a:a + k] for a, k in zip(to, n)]
+        over, written = False, set()
+        for a, k in zip(to, n):
+            span = set(range(a, a + k))
+            over, written = over or bool(span & written), written | span
+        for a, o, k in zip(at, to, n):
+            over = over or (a != o and bool(set(range(a, a + k)) & written))
+        kept = buf.clone()
+        want, ref = formula(grads, 0.5)
+        try:
+            norm = snk.clip_grads(grads, 0.5, out=outs)
+        except snk.SnackError as e:
+            assert e.status == -2 and over
+            assert torch.equal(buf, kept)
+        else:
+            assert not over
+            check(outs, norm, want, ref)
+        done[over] += 1
+    assert min(done.values()) > 50
+    g = torch.randn(50, device="cuda")  # read twice, written apart
+    outs = [torch.empty_like(g), torch.empty_like(g)]
+    check(outs, snk.clip_grads([g, g], 0.5, out=outs), *formula([g, g], 0.5))
+    w = torch.nn.Parameter(torch.zeros(50, device="cuda"))
+    w.grad = g.clone()
+    with pytest.raises(snk.SnackError):
+        snk.clip_grad_norm_([w, w], 0.5)
+    assert torch.equal(w.grad, g)

@@ -23,6 +23,8 @@ def grad_norm(grads):
 def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None):
     """Scale the tensors by min(1, max_norm / (norm + eps)), in place or into
     ``out`` (tensors of the same shapes); returns the norm before scaling.
+    Refused where an output shares memory with another output or with another
+    gradient (one gradient twice, in place, too).
     A NaN norm makes every output NaN; an infinite one zeroes the finite ones."""
     grads = list(grads)
     outs = None if out is None else list(out)
@@ -34,7 +36,8 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None):
 
 
 def clip_grad_norm_(parameters, max_norm: float, eps: float = 1e-6):
-    """:func:`clip_grads` on the ``.grad`` of the parameters that have one."""
+    """:func:`clip_grads` on the ``.grad`` of the parameters that have one; each
+    parameter once."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
     return clip_grads([p.grad for p in parameters if p.grad is not None], max_norm, eps)

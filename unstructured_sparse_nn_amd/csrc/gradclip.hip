@@ -14,6 +14,8 @@
 // 4.3 and 5.5 us, launch and three trips to memory each.
 #include <algorithm>
 #include <cmath>
+#include <memory>
+#include <new>
 
 #include "common.h"
 #include "internal.h"
@@ -204,6 +206,36 @@ snack_status check_grads(const snack_grad* g, int32_t count) {
   return SNACK_OK;
 }
 
+// Workgroups read and write the list in any order, so what one of them writes
+// must belong to no other entry: outputs must not share memory with each other,
+// nor with a gradient that is not scaled in place.
+snack_status check_shared(const snack_grad* g, int32_t count) {
+  struct span { uintptr_t at, end; };
+  if (count == 0) return SNACK_OK;
+  const std::unique_ptr<span[]> to(new (std::nothrow) span[count]);
+  if (!to) return SNACK_E_WORKSPACE;
+  auto span_of = [](const snack_grad& e, const void* p) {
+    return span{(uintptr_t)p, (uintptr_t)p + e.n * (e.dtype == SNACK_BF16 ? 2 : 4)};
+  };
+  auto before = [](const span& a, const span& b) { return a.at < b.at; };
+  int32_t n = 0;
+  for (int32_t i = 0; i < count; ++i)
+    if (g[i].n > 0) to[n++] = span_of(g[i], g[i].out ? g[i].out : g[i].grad);
+  span *const first = to.get(), *const last = first + n;
+  if (!std::is_sorted(first, last, before)) std::sort(first, last, before);
+  for (int32_t i = 1; i < n; ++i)
+    if (to[i].at < to[i - 1].end) return SNACK_E_SHAPE;
+  for (int32_t i = 0; i < count; ++i) {
+    if (g[i].n == 0 || !g[i].out || g[i].out == g[i].grad) continue;
+    const span r = span_of(g[i], g[i].grad);
+    if (r.at >= last[-1].end || r.end <= first->at) continue;
+    const span* next = std::lower_bound(first, last, r, before);  // the first that begins in r or after it
+    if ((next != last && next->at < r.end) || (next != first && next[-1].end > r.at))
+      return SNACK_E_SHAPE;
+  }
+  return SNACK_OK;
+}
+
 inline bool is_big(const snack_grad* g, int32_t count) {
   int64_t bytes = 0;
   for (int32_t i = 0; i < count && bytes <= BIG_BYTES; ++i)
@@ -309,6 +341,7 @@ snack_status snack_grad_clip(const snack_grad* grads, int32_t count, float max_n
   if (max_norm < 0 || eps < 0) return SNACK_E_SHAPE;
   if (!ws) return SNACK_E_NULL;
   if (ws_bytes < ws_of(count)) return SNACK_E_WORKSPACE;
+  if (snack_status st = check_shared(grads, count)) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const bool big = is_big(grads, count);
   const int32_t n_part = launch_squares(grads, count, big, (double*)ws, s);
