@@ -187,3 +187,45 @@ def test_rows_beside_each_other_in_one_buffer(seed, dt):
             assert torch.equal(y, want) and torch.equal(x, s["x"])
         done[over] += 1
     assert min(done.values()) > 50
+
+
+@pytest.mark.parametrize("move", [lambda m: m.to(torch.bfloat16), lambda m: m.bfloat16(),
+                                  lambda m: m.type(torch.bfloat16),
+                                  lambda m: torch.nn.Sequential(m).bfloat16()[0],
+                                  lambda m: m.bfloat16().float()], ids=range(5))
+def test_scales_and_ranks_keep_their_type(move):
+    m = snk.LoraAdapters(24, 16, 3, 8, alpha=5.0, ranks=[3, 7, 8], device="cpu")
+    moved = move(m)
+    assert moved.scale.dtype == torch.float32 and moved.ranks.dtype == torch.int32
+    assert torch.equal(moved.scale, torch.tensor([5 / 3, 5 / 7, 5 / 8]))
+    assert moved.ranks.tolist() == [3, 7, 8]
+    assert set(dict(moved.named_buffers())) == {"scale", "ranks"}
+    meta = moved.to("meta")
+    assert meta.scale.is_meta and meta.bfloat16().A.dtype == torch.bfloat16
+    assert snk.LoraAdapters(24, 16, 3, 8, device="cpu").bfloat16().ranks is None
+
+
+@gpu
+@pytest.mark.parametrize("default", [torch.float32])
+def test_moved_module_and_other_default_types(default):
+    """The module cast to bf16 and moved to the GPU, and made under another
+    default type, computes what its parameters say."""
+    s = make(70, 24, 16, 3, 8, "bf16", seed=6, ranks=False)
+    s["ranks"] = torch.tensor([3, 7, 8], dtype=torch.int32, device="cuda")
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(default)
+    try:
+        m = torch.nn.Sequential(snk.LoraAdapters(24, 16, 3, 8, alpha=5.0, ranks=[3, 7, 8],
+                                                 device="cpu")).bfloat16().cuda()[0]
+        with torch.no_grad():
+            m.A.copy_(s["A"])
+            m.B.copy_(s["B"])
+        x = s["x"].clone().requires_grad_()
+        y = m(x, s["ids"], s["base"])
+        y.backward(s["dy"])
+    finally:
+        torch.set_default_dtype(before)
+    s["scale"], s["gbase"] = torch.tensor([5 / 3, 5 / 7, 5 / 8]), torch.zeros(70, 24)
+    ref, tol = reference(s, "bf16", grads=True)
+    for k, v in (("y", y.detach()), ("dx", x.grad), ("dA", m.A.grad), ("dB", m.B.grad)):
+        close(v, ref[k], tol[k], k)

@@ -84,6 +84,16 @@ class LoraAdapters(torch.nn.Module):
         self.register_buffer("ranks", None if ranks is None else torch.tensor(
             ranks, dtype=torch.int32, device=device))
 
+    def _apply(self, fn, recurse=True):
+        # the kernels read scale as float32 and ranks as int32, whatever type the
+        # module is cast to: casts move the buffers to another device only
+        kept = {k: v for k, v in self._buffers.items() if v is not None}
+        super()._apply(fn, recurse)
+        for k, v in kept.items():
+            if self._buffers[k].dtype != v.dtype:
+                self._buffers[k] = v.to(self._buffers[k].device)
+        return self
+
     def forward(self, x, ids, base=None):
         """base + each row's adapter applied to x (rows of x: tokens)."""
         if torch.is_grad_enabled():
