@@ -206,7 +206,7 @@ def test_scales_and_ranks_keep_their_type(move):
 
 
 @gpu
-@pytest.mark.parametrize("default", [torch.float32])
+@pytest.mark.parametrize("default", [torch.float32, torch.bfloat16, torch.float64])
 def test_moved_module_and_other_default_types(default):
     """The module cast to bf16 and moved to the GPU, and made under another
     default type, computes what its parameters say."""

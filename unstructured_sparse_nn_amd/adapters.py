@@ -40,7 +40,7 @@ def lora_bwd(dy, x, ids, A, B, scale=None, ranks=None, t=None, base=None, out=No
 class _LoraFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, A, B, base, ids, scale, ranks):
-        t = torch.empty(x.shape[0], A.shape[1], device=x.device)
+        t = torch.empty(x.shape[0], A.shape[1], dtype=torch.float32, device=x.device)
         y = lora_fwd(x, ids, A, B, scale, ranks, base, t=t)
         ctx.save_for_backward(x, A, B, ids, scale, ranks, t)
         return y
