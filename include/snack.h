@@ -598,7 +598,7 @@ SNACK_API snack_status snack_conv1x1(const snack_plan* plan, const void* vals, s
  * Both calls are asynchronous, allocate nothing, add no floats by atomics and
  * give the same bits for the same inputs.  Errors: SNACK_E_NULL, SNACK_E_DTYPE,
  * SNACK_E_SHAPE (sizes, strides, overlap), SNACK_E_OVERFLOW (M or K > 2^23,
- * T within 2^20 of 2^31), SNACK_E_WORKSPACE.
+ * T > 2^28 - 2^20, in the backward T > 2^27 - 2^19), SNACK_E_WORKSPACE.
  */
 typedef struct snack_lora {
   int32_t M, K, L, R;

@@ -229,3 +229,57 @@ def test_moved_module_and_other_default_types(default):
     ref, tol = reference(s, "bf16", grads=True)
     for k, v in (("y", y.detach()), ("dx", x.grad), ("dA", m.A.grad), ("dB", m.B.grad)):
         close(v, ref[k], tol[k], k)
+
+
+MOST = {False: 2 ** 28 - 2 ** 20, True: 2 ** 27 - 2 ** 19}  # tokens of a forward and of a backward
+
+
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("L,R", [(1, 1), (8192, 256)])
+def test_more_tokens_than_a_launch_holds_are_refused(L, R, backward):
+    bank = b.snack_lora(PLACES["A"], PLACES["B"], 8, 8, L, R)
+    most = MOST[backward]
+    assert b.snack_lora_workspace(bank, b.F32, most, backward) > 0
+    for T in (most + 1, 2 ** 30):
+        with pytest.raises(snk.SnackError) as e:
+            b.snack_lora_workspace(bank, b.F32, T, backward)
+        assert e.value.status == -10
+        args = (PLACES["ws"], 1 << 50, None)
+        if backward:
+            st = b.raw_status("snack_lora_bwd", ctypes.byref(bank), 0, 1 << 20, None, T, 1 << 40, 8,
+                              1 << 42, 8, None, 8, 1 << 44, 8, None, None, *args)
+        else:
+            st = b.raw_status("snack_lora_fwd", ctypes.byref(bank), 0, 1 << 20, T, 1 << 40, 8, None,
+                              8, 1 << 44, 8, None, *args)
+        assert st == -10
+
+
+@gpu
+@pytest.mark.parametrize("backward", [False, True])
+def test_the_most_tokens(backward):
+    """All tokens a launch holds, some rows nonzero: 8 features, rank 2."""
+    T, K, M, R = MOST[backward], 8, 8, 2
+    rows = torch.tensor([0, 77, T // 2 + 31, T - 2 ** 20, T - 33, T - 1], device="cuda")
+    s = make(rows.numel(), K, M, 1, R, "bf16", seed=2, ids="0", ranks=False)
+    s["base"], s["gbase"] = torch.zeros_like(s["base"]), torch.zeros_like(s["gbase"])
+    ref, tol = reference(s, "bf16", grads=True)
+
+    def spread(v):
+        w = torch.zeros(T, v.shape[1], dtype=v.dtype, device="cuda")
+        w[rows] = v
+        return w
+
+    ids = torch.zeros(T, dtype=torch.int32, device="cuda")
+    args = (ids, s["A"], s["B"], s["scale"])
+    x = spread(s["x"])
+    if backward:
+        dx, dA, dB = snk.lora_bwd(spread(s["dy"]), x, *args)
+        close(dx[rows], ref["dx"], tol["dx"], "dx")
+        close(dA, ref["dA"], tol["dA"], "dA")
+        close(dB, ref["dB"], tol["dB"], "dB")
+        out = dx
+    else:
+        out = snk.lora_fwd(x, *args)
+        close(out[rows], ref["y"], tol["y"], "y")
+    out[rows] = 0
+    assert int(out.view(-1, 2 ** 20).any(1).sum()) == 0  # all others

@@ -33,7 +33,13 @@ typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 constexpr int32_t TILE = 32;  // tokens of a tile at most
 constexpr int32_t MAX_RANK = 256;
 constexpr int32_t MAX_ADAPTERS = 8192;
-constexpr int32_t MAX_FEATURES = 1 << 23;  // column blocks are a grid's y
+constexpr int32_t MAX_FEATURES = 1 << 23;  // columns stay far inside 32 bits
+// A launch holds fewer than 2^32 threads along x: 2^23 workgroups of 512.
+// k_lora_apply has one for each tile of 32 tokens, two in a backward, and up to
+// one tile more for each adapter.
+constexpr int32_t max_tokens(bool backward) {
+  return backward ? (1 << 27) - (1 << 19) : (1 << 28) - (1 << 20);
+}
 
 struct lora_dev {  // what every kernel needs of the adapters
   int32_t L, R;
@@ -1468,13 +1474,13 @@ __global__ __launch_bounds__(256) void k_lora_join(lora_dev d, route_t p, int32_
 }
 
 // --------------------------------------------------------------------- host
-snack_status check_lora(const snack_lora* p, snack_dtype dt, int32_t T) {
+snack_status check_lora(const snack_lora* p, snack_dtype dt, int32_t T, bool backward) {
   if (!p) return SNACK_E_NULL;
   if (dt != SNACK_F32 && dt != SNACK_BF16) return SNACK_E_DTYPE;
   if (p->M < 1 || p->K < 1 || p->L < 1 || p->L > MAX_ADAPTERS || p->R < 1 || p->R > MAX_RANK ||
       T < 0)
     return SNACK_E_SHAPE;
-  if (T > INT32_MAX - (1 << 20) || p->M > MAX_FEATURES || p->K > MAX_FEATURES) return SNACK_E_OVERFLOW;
+  if (T > max_tokens(backward) || p->M > MAX_FEATURES || p->K > MAX_FEATURES) return SNACK_E_OVERFLOW;
   return SNACK_OK;
 }
 
@@ -1773,7 +1779,7 @@ extern "C" {
 snack_status snack_lora_workspace(const snack_lora* lora, snack_dtype dtype, int32_t T,
                                   int32_t backward, size_t* bytes) {
   if (!bytes) return SNACK_E_NULL;
-  if (snack_status st = check_lora(lora, dtype, T)) return st;
+  if (snack_status st = check_lora(lora, dtype, T, backward != 0)) return st;
   *bytes = plan_of(lora, dtype, T, backward != 0).total;
   return SNACK_OK;
 }
@@ -1782,7 +1788,7 @@ snack_status snack_lora_fwd(const snack_lora* lora, snack_dtype dtype, const int
                             int32_t T, const void* X, int64_t ldx, const void* base, int64_t ldb,
                             void* Y, int64_t ldy, float* t, void* ws, size_t ws_bytes,
                             void* stream) {
-  if (snack_status st = check_lora(lora, dtype, T)) return st;
+  if (snack_status st = check_lora(lora, dtype, T, false)) return st;
   if (ldx < lora->K || ldy < lora->M || (base && ldb < lora->M)) return SNACK_E_SHAPE;
   if (T == 0) return SNACK_OK;
   if (!lora->A || !lora->B || !ids || !X || !Y || !ws) return SNACK_E_NULL;
@@ -1808,7 +1814,7 @@ snack_status snack_lora_bwd(const snack_lora* lora, snack_dtype dtype, const int
                             const float* t, int32_t T, const void* X, int64_t ldx, const void* dY,
                             int64_t lddy, const void* base, int64_t ldb, void* dX, int64_t lddx,
                             void* dA, void* dB, void* ws, size_t ws_bytes, void* stream) {
-  if (snack_status st = check_lora(lora, dtype, T)) return st;
+  if (snack_status st = check_lora(lora, dtype, T, true)) return st;
   if (ldx < lora->K || lddy < lora->M || (dX && lddx < lora->K) || (base && ldb < lora->K))
     return SNACK_E_SHAPE;
   if (T > 0) {
