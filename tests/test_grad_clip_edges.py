@@ -73,3 +73,45 @@ def test_refused_where_tensors_share_memory_and_only_there():
     with pytest.raises(snk.SnackError):
         snk.clip_grad_norm_([w, w], 0.5)
     assert torch.equal(w.grad, g)
+
+
+def test_table_refuses_what_does_not_fit():
+    g = [torch.ones(4, 6), torch.ones(3)]
+    for bad in ([g[0].half(), g[1]], g):  # type, then device: tensors of the GPU only
+        with pytest.raises(TypeError):
+            b.snack_grad_table(bad)
+    for grads in ([g[0][:, ::2]], [torch.ones(1).expand(4)], [torch.ones(5).as_strided((3, 3), (1, 1))]):
+        with pytest.raises(ValueError, match="gaps or overlaps"):
+            b.snack_grad_table(grads)
+    for outs in (g[:1], g + g, [g[0], torch.ones(4)], [g[0].t(), g[1]], [g[0].mT.contiguous().mT, g[1]]):
+        with pytest.raises(ValueError, match="output"):
+            b.snack_grad_table(g, outs)
+    with pytest.raises(TypeError):
+        b.snack_grad_table(g, [g[0].bfloat16(), g[1]])
+    tab = array("q", [0] * 8)  # two empty tensors
+    for count in (3, -1):
+        with pytest.raises((ValueError, snk.SnackError)):
+            b.snack_grad_norm(tab, count, 64, 64, stream=0, ws_bytes=1 << 30)
+        with pytest.raises((ValueError, snk.SnackError)):
+            b.snack_grad_clip(tab, count, 1.0, 0.0, 64, 64, stream=0, ws_bytes=1 << 30)
+
+
+@gpu
+def test_binding_and_torch_calls_agree():
+    """The binding's own calls, bit for bit."""
+    g = [torch.randn(50, 7, device="cuda"), torch.randn(8, 3, device="cuda").t().bfloat16(),
+         torch.empty(0, device="cuda"), torch.randn(40000, device="cuda")]
+    outs = [torch.empty_like(x) for x in g]
+    ws = torch.empty(b.snack_grad_workspace(4), dtype=torch.uint8, device="cuda")
+    norm = torch.empty((), device="cuda")
+    tab = b.snack_grad_table(g, outs)
+    b.snack_grad_clip(tab, 4, 0.5, 1e-6, norm, ws)
+    want = [torch.empty_like(x) for x in g]
+    assert torch.equal(norm, snk.clip_grads(g, 0.5, out=want))
+    assert all(torch.equal(p, q) for p, q in zip(outs, want))
+    b.snack_grad_norm(b.snack_grad_table(g[:2]), 2, norm, ws)
+    assert torch.equal(norm, snk.grad_norm(g[:2]))
+    b.snack_grad_norm(tab, 1, norm, ws)  # fewer than the table has
+    assert torch.equal(norm, snk.grad_norm(g[:1]))
+    b.snack_grad_clip(b.snack_grad_table(g), 4, 0.5, 1e-6, None, ws)  # in place
+    assert all(torch.equal(p, q) for p, q in zip(g, want))

@@ -283,3 +283,31 @@ def test_the_most_tokens(backward):
         close(out[rows], ref["y"], tol["y"], "y")
     out[rows] = 0
     assert int(out.view(-1, 2 ** 20).any(1).sum()) == 0  # all others
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_binding_and_torch_calls_agree(dt):
+    """The binding's own calls, bit for bit, with all arguments and with few."""
+    T, K, M, L, R = 90, 24, 40, 3, 8
+    s = make(T, K, M, L, R, dt, seed=1)
+    args = (s["x"], s["ids"], s["A"], s["B"], s["scale"], s["ranks"])
+    lora = b.snack_lora(s["A"], s["B"], M, K, L, R, s["scale"], s["ranks"])
+    code = b._dtype(s["x"])
+
+    def ws(backward):
+        return torch.empty(b.snack_lora_workspace(lora, code, T, backward), dtype=torch.uint8,
+                           device="cuda")
+
+    y, t = torch.empty_like(s["base"]), torch.empty(T, R, device="cuda")
+    b.snack_lora_fwd(lora, s["ids"], T, s["x"], K, s["base"], M, y, M, t=t, ws=ws(False))
+    want_t = torch.empty_like(t)
+    assert torch.equal(y, snk.lora_fwd(*args, s["base"], t=want_t)) and torch.equal(t, want_t)
+    dx, dA, dB = torch.empty_like(s["x"]), torch.empty_like(s["A"]), torch.empty_like(s["B"])
+    b.snack_lora_bwd(lora, s["ids"], t, T, s["x"], K, s["dy"], M, s["gbase"], K, dx, K, dA, dB,
+                     ws=ws(True))
+    want = snk.lora_bwd(s["dy"], *args, t=t, base=s["gbase"])
+    assert all(torch.equal(p, q) for p, q in zip((dx, dA, dB), want))
+    b.snack_lora_bwd(lora, s["ids"], None, T, s["x"], K, s["dy"], M, None, K, None, K, dB=dB,
+                     ws=ws(True))
+    assert torch.equal(dB, snk.lora_bwd(s["dy"], *args, want=(False, False, True))[2])

@@ -460,19 +460,42 @@ def snack_lora_bwd(lora: SnackLora, ids, t, T: int, X, ldx: int, dY, lddy: int, 
            "snack_lora_bwd")
 
 
+def _dense(x) -> bool:
+    """Whether x fills its memory without gaps or overlaps."""
+    return x.is_contiguous() or x.permute(
+        sorted(range(x.dim()), key=lambda d: (-x.stride(d), -x.size(d)))).is_contiguous()
+
+
 def snack_grad_table(grads, outs=None):
     """The host array of ``struct snack_grad`` for tensors (outs: where the
     scaled ones go, default in place), as an ``array('q')``."""
     import torch
     from array import array
     codes = {torch.float32: F32, torch.bfloat16: BF16}
+    grads = list(grads)
+    outs = grads if outs is None else list(outs)
+    if len(outs) != len(grads):
+        raise ValueError(f"{len(grads)} gradients but {len(outs)} outputs")
     rows = array("q")
-    try:
-        for g, o in zip(grads, grads if outs is None else outs):
-            rows.extend((g.data_ptr(), o.data_ptr(), g.numel(), codes[g.dtype]))
-    except KeyError as e:
-        raise TypeError(f"unsupported dtype {e.args[0]}") from None
+    for g, o in zip(grads, outs):
+        if g.dtype not in codes:
+            raise TypeError(f"unsupported dtype {g.dtype}")
+        if not _dense(g):
+            raise ValueError("a gradient must fill its memory without gaps or overlaps")
+        if o.dtype != g.dtype or o.device != g.device:
+            raise TypeError("an output must have its gradient's dtype and device")
+        if o.shape != g.shape or o.stride() != g.stride():
+            raise ValueError("an output must have its gradient's shape and strides")
+        rows.extend((g.data_ptr(), o.data_ptr(), g.numel(), codes[g.dtype]))
+    if any(not g.is_cuda or g.device != grads[0].device for g in grads):
+        raise TypeError("gradients must be on one GPU")
     return rows
+
+
+def _grad_table(table, count: int):
+    if 4 * count > len(table):
+        raise ValueError(f"{count} gradients, but the table holds {len(table) // 4}")
+    return table.buffer_info()[0]
 
 
 def snack_grad_workspace(count: int) -> int:
@@ -482,13 +505,13 @@ def snack_grad_workspace(count: int) -> int:
 
 
 def snack_grad_norm(table, count: int, norm, ws, stream=None, ws_bytes=None):
-    _check(_lib.snack_grad_norm(table.buffer_info()[0], count, _ptr(norm), _ptr(ws),
+    _check(_lib.snack_grad_norm(_grad_table(table, count), count, _ptr(norm), _ptr(ws),
                                 _nbytes(ws, ws_bytes), _stream(stream)), "snack_grad_norm")
 
 
 def snack_grad_clip(table, count: int, max_norm: float, eps: float, norm, ws, stream=None,
                     ws_bytes=None):
-    _check(_lib.snack_grad_clip(table.buffer_info()[0], count, max_norm, eps, _ptr(norm),
+    _check(_lib.snack_grad_clip(_grad_table(table, count), count, max_norm, eps, _ptr(norm),
                                 _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream)),
            "snack_grad_clip")
 
