@@ -311,3 +311,37 @@ def test_binding_and_torch_calls_agree(dt):
     b.snack_lora_bwd(lora, s["ids"], None, T, s["x"], K, s["dy"], M, None, K, None, K, dB=dB,
                      ws=ws(True))
     assert torch.equal(dB, snk.lora_bwd(s["dy"], *args, want=(False, False, True))[2])
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,R", [(5, 16), (100, 16), (100, 40), (3000, 16)])
+def test_sums_next_to_the_largest_float(T, R, dt):
+    """t and u of 2^128 - 2^118, which rounds to infinity in bf16: beside small
+    factors the results are finite."""
+    K = M = 136
+    s = make(T, K, M, 1, R, dt, seed=T + R, ids="0", ranks=False)
+    s["scale"] = torch.ones(1, device="cuda")
+    s["base"], s["gbase"] = torch.zeros_like(s["base"]), torch.zeros_like(s["gbase"])
+    steps = torch.zeros(K, device="cuda")
+    steps[:10] = 2.0 ** (63 - torch.arange(10, device="cuda", dtype=torch.float32))
+    for a, f in (("x", "A"), ("dy", "B")):  # sum over the features: 2^127 + ... + 2^118
+        v = dict(s)
+        v[a] = torch.full_like(s[a], 2.0 ** 64)
+        v[f] = torch.zeros_like(s[f])
+        v[f][0, 3], v[f][0, R - 1] = steps, -steps
+        other, small = ("B", "dy") if a == "x" else ("A", "x")
+        v[other], v[small] = (s[other] * 2.0 ** -100).to(s[a].dtype), (s[small] * 2.0 ** -120).to(s[a].dtype)
+        ref, tol = reference(v, dt, grads=True)
+        args = (v["ids"], v["A"], v["B"])
+        if a == "x":
+            t = torch.empty(T, R, device="cuda")
+            close(snk.lora_fwd(v["x"], *args, t=t), ref["y"], tol["y"], "y")
+            assert float(t.abs().max()) == 2.0 ** 128 - 2.0 ** 118
+            for kept in (t, None):
+                dB = snk.lora_bwd(v["dy"], v["x"], *args, t=kept, want=(False, False, True))[2]
+                close(dB, ref["dB"], tol["dB"], "dB")
+        else:
+            dx, dA, _ = snk.lora_bwd(v["dy"], v["x"], *args, want=(True, True, False))
+            close(dx, ref["dx"], tol["dx"], "dx")
+            close(dA, ref["dA"], tol["dA"], "dA")

@@ -216,11 +216,18 @@ __device__ __forceinline__ void round_to(const float (&v)[E], piece<float, E>& o
   for (int e = 0; e < E; ++e) o.w[e] = __float_as_uint(v[e]);
 }
 
-// v as two bf16 parts, hi + lo: off by at most 2^-16 of v.  Infinities and NaN
-// are hi alone.
+// v as two bf16 parts, hi + lo: off by at most 2^-16 of v, a 256th of the
+// rounding of what comes of it (bf16's half step, 2^-8), for two products of
+// the matrix cores where fp32's 24 bits would take three.  hi is at most the
+// largest bf16, which larger floats would round past.  Infinities and NaN are
+// hi alone.
 __device__ __forceinline__ void split_frag(const float (&v)[8], frag<bf16>& hi, frag<bf16>& lo) {
-  hi = to_frag(v);
-  float rest[8];
+  const float most = __uint_as_float(0x7F7F0000u);
+  float top[8], rest[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    top[e] = fabsf(v[e]) < __builtin_inff() ? __builtin_amdgcn_fmed3f(v[e], -most, most) : v[e];
+  hi = to_frag(top);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float h = at(hi, e);
