@@ -115,3 +115,31 @@ def test_binding_and_torch_calls_agree():
     assert torch.equal(norm, snk.grad_norm(g[:1]))
     b.snack_grad_clip(b.snack_grad_table(g), 4, 0.5, 1e-6, None, ws)  # in place
     assert all(torch.equal(p, q) for p, q in zip(g, want))
+
+
+@gpu
+@pytest.mark.parametrize("types", [["f32"], ["bf16"], ["bf16", "f32"]], ids=str)
+def test_lists_past_128_megabytes(types):
+    """Large and small tensors at odd alignments, out of place and in place."""
+    dt = [{"f32": torch.float32, "bf16": torch.bfloat16}[t] for t in types]
+    g = torch.Generator(device="cuda").manual_seed(7)
+    sizes = [16384 * 700 + 5, 3, 16384, 30000001, 16383, 16385 * 9, 0, 40000000]
+    grads, outs, kept = [], [], []
+    for i, n in enumerate(sizes):
+        d = dt[i % len(dt)]
+        wide = torch.randn(n + 16, generator=g, device="cuda").to(d)
+        to = torch.full((n + 16,), 7.0, dtype=d, device="cuda")
+        grads.append(wide[i:i + n])
+        outs.append(to[8 - i:8 - i + n])
+        kept.append((to, 8 - i, n))
+    assert sum(x.numel() * x.element_size() for x in grads) > 128 << 20
+    want, ref = formula(grads, 3.0)
+    assert abs(float(snk.grad_norm(grads)) - want) <= 1.01 * 2.0 ** -24 * want
+    check(outs, snk.clip_grads(grads, 3.0, out=outs), want, ref)
+    assert all((to[:a] == 7).all() and (to[a + n:] == 7).all() for to, a, n in kept)
+    norm = snk.clip_grads(grads, 3.0)
+    check(grads, norm, want, ref)
+    assert all(torch.equal(p, q) for p, q in zip(grads, outs))
+    again = [x.clone() for x in grads]
+    assert abs(float(snk.clip_grads(grads, 1e9)) - 3.0) < 3.0 * 2.0 ** -8 + 1e-5
+    assert all(torch.equal(p, q) for p, q in zip(grads, again))

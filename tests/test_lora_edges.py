@@ -345,3 +345,46 @@ def test_sums_next_to_the_largest_float(T, R, dt):
             dx, dA, _ = snk.lora_bwd(v["dy"], v["x"], *args, want=(True, True, False))
             close(dx, ref["dx"], tol["dx"], "dx")
             close(dA, ref["dA"], tol["dA"], "dA")
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("width", [136, 200, 648])
+@pytest.mark.parametrize("case", [(20, 1, 16, [16]), (90, 1, 16, [9]), (300, 3, 16, [16, 5, 11]),
+                                  (3000, 2, 16, [13, 16]), (200, 2, 40, [33, 40])], ids=str)
+def test_infinities_in_the_factors(case, width, dt):
+    """Infinities of both signs and a NaN in factors that tokens use: the
+    columns that they lie in are the formula's, all others finite."""
+    T, L, R, ranks = case
+    s = make(T, width, width, L, R, dt, seed=T + width, ids="runs", ranks=False)
+    s["ids"][2] = -1
+    s["ranks"] = torch.tensor(ranks, dtype=torch.int32, device="cuda")
+    inf, nan = float("inf"), float("nan")
+    for f in ("A", "B"):  # the last rank of the first adapter, the first ranks of the last one
+        s[f][0, ranks[0] - 1, 7], s[f][0, 1, width - 1] = inf, -inf
+        s[f][L - 1, 0, 9], s[f][L - 1, 2, 64], s[f][L - 1, 1, 66] = -inf, inf, nan
+        s[f][L - 1, 0, 70], s[f][L - 1, 1, 70] = inf, -inf
+    cols = [7, 9, 64, 66, 70, width - 1]
+
+    def formula(v, F, base):
+        want = base.double().cpu().clone()
+        F, scale, ids = F.double().cpu(), s["scale"].double().cpu(), s["ids"].cpu()
+        for l, r in enumerate(ranks):
+            rows = ids == l
+            want[rows] += scale[l] * (v[rows, :r, None] * F[l, :r]).sum(1)
+        return want
+
+    # t of x by the factor without infinities, and so u of dy
+    clean = {f: torch.where(torch.isfinite(s[f]), s[f], torch.zeros_like(s[f])) for f in ("A", "B")}
+    for name, got, want, v in (
+            ("y", snk.lora_fwd(s["x"], s["ids"], clean["A"], s["B"], s["scale"], s["ranks"],
+                               s["base"]), "B", "x"),
+            ("dx", snk.lora_bwd(s["dy"], s["x"], s["ids"], s["A"], clean["B"], s["scale"],
+                                s["ranks"], base=s["gbase"], want=(True, False, False))[0], "A", "dy")):
+        c = dict(s, **clean)
+        if name == "dx":
+            c = dict(c, x=s["dy"], A=clean["B"], B=clean["A"], base=s["gbase"])
+        ref, tol = reference(c, dt)
+        full = formula(ref["t"], s[want], c["base"])
+        same_pattern(got, full, ref["y"], tol["y"], name)
+        assert torch.isfinite(got[:, [k for k in range(width) if k not in cols]]).all()
