@@ -222,12 +222,19 @@ __device__ __forceinline__ void round_to(const float (&v)[E], piece<float, E>& o
 // largest bf16, which larger floats would round past.  Infinities and NaN are
 // hi alone.
 __device__ __forceinline__ void split_frag(const float (&v)[8], frag<bf16>& hi, frag<bf16>& lo) {
-  const float most = __uint_as_float(0x7F7F0000u);
-  float top[8], rest[8];
+  hi = to_frag(v);
+  float peak = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    top[e] = fabsf(v[e]) < __builtin_inff() ? __builtin_amdgcn_fmed3f(v[e], -most, most) : v[e];
-  hi = to_frag(top);
+  for (int e = 0; e < 8; ++e) peak = fmaxf(peak, fabsf(v[e]));
+  if (peak >= __uint_as_float(0x7F7F8000u)) {  // rounds past the largest bf16, or infinite
+    const float most = __uint_as_float(0x7F7F0000u);
+    float top[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      top[e] = fabsf(v[e]) < __builtin_inff() ? fminf(fmaxf(v[e], -most), most) : v[e];
+    hi = to_frag(top);
+  }
+  float rest[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float h = at(hi, e);
