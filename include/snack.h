@@ -576,9 +576,11 @@ SNACK_API snack_status snack_conv1x1(const snack_plan* plan, const void* vals, s
  * snack_lora_fwd: with a = ids[i],
  *     t[i, j] = sum_k A[a, j, k] X[i, k]                 (fp32; 0 for j >= r)
  *     Y[i, m] = base[i, m] + s_a sum_j t[i, j] B[a, j, m]
- * one rounding to the output type.  base (nullable: zeros) is the shared
- * projection's output and may be Y itself (same stride).  t (nullable,
- * T x R floats, contiguous) receives t for snack_lora_bwd.
+ * one rounding to the output type (bf16: in the matrix cores' products t, and u
+ * below, count as two bf16 parts, off by at most 2^-16 of them).  base
+ * (nullable: zeros) is the shared projection's output and may be Y itself (same
+ * stride).  t (nullable, T x R floats, contiguous) receives t for
+ * snack_lora_bwd.
  *
  * snack_lora_bwd: with u[i, j] = sum_m B[a, j, m] dY[i, m],
  *     dX[i, k] = base[i, k] + s_a sum_j u[i, j] A[a, j, k]

@@ -29,9 +29,11 @@ constexpr int32_t MAX_BLOCKS = 4096;
 // Lists of more than BIG_BYTES leave no room for their outputs in the 256 MB
 // cache before memory: those are stored past the caches, since the lines that
 // plain stores leave there have to be written back while the next call reads,
-// and workgroups take larger units.  48 bf16 gradients, 274 MB in all: 140 us
-// against 171 us with plain stores; 48 fp32 gradients, 1 MB: 9.8 us with small
-// units, 11.5 us with large ones.
+// and workgroups take larger units.  Lists of bf16 gradients out of place, small
+// units with plain stores against this: 160 MB in 48 tensors 111 and 96 us, 274 MB
+// 181 and 147 us, 800 MB 501 and 431 us, in 400 tensors 569 and 581 us; 1 MB of fp32
+// in 48: 9.8 and 11.5 us.  Not taken: out of place it pays from 37 MB on (33.5 and
+// 28.9 us; 96 MB 68 and 56 us).
 constexpr int64_t BIG_BYTES = 128ll << 20;
 constexpr int32_t unit_of(bool big) { return big ? 16384 : 4096; }  // elements
 

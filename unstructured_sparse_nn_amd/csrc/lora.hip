@@ -12,11 +12,11 @@
 // A few tokens take k_lora_few, a workgroup's worth of dot products each.
 // More tokens are cut into tiles of up to 32 of one adapter, which feed the
 // matrix cores: reduce and expand of a tile in one kernel (k_lora_apply), the
-// gradients in a second one (k_lora_grad) that reads x and dy once more, for
-// the sums over the tokens need all of u first.  Up to 8,192 tokens the
-// workgroups find their tiles' tokens themselves; beyond, k_lora_route sorts
-// them first.  The ranks are few, so all of it is bound by memory: x, base and
-// y once each, beside factors that stay in the caches.
+// gradients in a second one (k_lora_grad), for dA needs all of u first.  That
+// one reads x and dy: dy for the second time, x too where t was not kept.  Up
+// to 8,192 tokens the workgroups find their tiles' tokens themselves; beyond,
+// k_lora_route sorts them first.  The ranks are few, so all of it is bound by
+// memory: x, base and y once each, beside factors that stay in the caches.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -660,9 +660,11 @@ __device__ __forceinline__ bool place_of(int32_t tiles, int32_t roles, int32_t& 
 // Up to SELF_TOKENS tokens and SELF_GROUPS - 1 adapters, every workgroup finds
 // the tokens of its tile itself: it counts the groups in LDS (whole numbers:
 // the order of the additions does not matter), finds its tile's group and
-// collects that group's tokens.  4,099 tokens of 12 adapters: 63.7 us in all,
-// 74.4 us with k_lora_route before; 6,001 tokens of 24: 192 us, 197 us with it.
-// SELF_BYTES: LDS that it takes.
+// collects that group's tokens.  Against k_lora_route before (rank 16, bf16, 4096
+// to 4096; 2 to 500 adapters measured at 300 to 8,192 tokens), of 12 adapters: a
+// forward of 1,024 tokens 19.1 us and 23.3 us, of 4,099 37.6 and 43.0, of 8,192
+// 71.5 and 76.7; a backward of 4,099 76.9 and 79.4 us, of 6,001 81.1 and 80.3, of
+// 8,192 125.6 and 129.2.  SELF_BYTES: LDS that it takes.
 constexpr int32_t SELF_TOKENS = 8192, SELF_GROUPS = 1024;
 constexpr size_t SELF_BYTES = 4 * (SELF_GROUPS + WAVES + 4 + WAVES);
 
@@ -1120,8 +1122,8 @@ __device__ __forceinline__ void expand_any(const expand_arg<T>& q, const T* __re
 // and write a share of the sum over k each.  self: no tables are there yet, see
 // self_route.  REDUCE and EXPAND do one half each, for more than 16 ranks: 64
 // ranks at a time want 243 registers in the sums, the expansion 121 and twice
-// the waves (6,001 tokens of ranks 16 to 64, backward: 60 and 40 us; 120 us as
-// one kernel).
+// the waves (6,001 tokens of ranks 16 to 64, backward: 59 and 40 us; 120 us as
+// one kernel).  BOTH in fp32 keeps 4 of its 132 registers in scratch memory.
 enum { BOTH, REDUCE, EXPAND };
 
 template <typename T, int NR, int MODE>
@@ -1241,8 +1243,9 @@ struct grad_arg {
 // LDS.  tw = 1: each wave has its own columns.  grid: column blocks (of X, then
 // of dY) x slots x rank blocks of 16 * NR.  Bound by the reading of X and dY,
 // 256 bytes of a row at a time: 31 us for the 134 MB of 8,192 tokens at
-// 4096x4096 (4.3 TB/s), 49 us for the 181 MB of 6,001 tokens of 24 adapters.
-// NR is 2 at most: 64 ranks at a time spill registers.
+// 4096x4096 (4.3 TB/s), 50 us for the 181 MB of 6,001 tokens of 24 adapters.
+// NR is 2 at most: 64 ranks at a time spill registers.  NR = 1 in bf16 keeps 5
+// of its 133 in scratch memory, for four waves a SIMD.
 constexpr int grad_waves(int NR) { return NR == 1 ? 8 : 4; }
 
 template <typename T, int NR, bool FULL>
@@ -1580,7 +1583,10 @@ plan_t plan_of(const snack_lora* p, snack_dtype dt, int32_t T, bool backward) {
   // together, for tokens may all have one adapter (164 fp32 tokens that do, of 7,
   // 2344 to 2525: 63 us with one wave a slot, 28 us shared), and where adapters
   // have tiles enough for all waves.  Elsewhere one wave sums it alone (300
-  // tokens of 16 adapters of rank 64, 4096 to 4096: 8 us, 35 us shared).
+  // tokens of 16 adapters of rank 64, 4096 to 4096: 8 us, 35 us shared).  Not
+  // looked at here: fewer tiles than adapters leave most waves of a shared slot
+  // idle (a backward of 100 bf16 tokens of 64 adapters of rank 16, 4096 to 4096:
+  // 79 us, 24 us with one wave a slot).
   const int32_t gw = grad_waves(w.NT), users = std::max(1, std::min(p->L, w.whole));
   const int64_t blocks = w.blocksA + w.blocksB, alone = blocks * users * cdiv(w.NT, 2);
   const int32_t per = w.whole / users;  // tiles of an adapter
