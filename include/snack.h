@@ -658,6 +658,152 @@ SNACK_API snack_status snack_grad_clip(const snack_grad* grads, int32_t count, f
                                        void* stream);
 
 /*
+ * snack_dropout -- dropout without a stored mask, forward and backward.
+ * With n = round_half_up(p 2^16) and element i = r * cols + c of a matrix:
+ *     Y[r, c] = residual[r, c] + (u_i < n ? 0 : X[r, c] * 2^16 / (2^16 - n))
+ * u_i is field i mod 4 (16 bits, lowest first) of output number i / 4 of a
+ * SplitMix64 generator whose seed is output number `step` of one seeded with
+ * `seed` (the restructure's stream: its candidate i is output number i of the
+ * same generator).  step_dev (nullable, device) is added to `step` when the
+ * kernel runs, so that a captured graph draws anew at each replay.  The
+ * backward is the same call on dY with no residual.  A dropped element is
+ * exactly 0 (the residual), whatever X holds there; p = 1 drops all.
+ * Rows are ld elements apart, at any alignment; Y may be X or residual itself
+ * (same stride) and must share no memory otherwise.  Asynchronous.  Errors:
+ * SNACK_E_NULL, SNACK_E_DTYPE, SNACK_E_SHAPE (sizes, strides, p outside [0, 1],
+ * overlap), SNACK_E_NAN (p), SNACK_E_OVERFLOW (rows * cols > 2^36, or with
+ * strides cols >= 2^31 or 2^32 - 2^20 pieces of 16 bytes).
+ */
+SNACK_API snack_status snack_dropout(snack_dtype dtype, const void* X, int64_t ldx,
+                                     const void* residual, int64_t ldr, void* Y, int64_t ldy,
+                                     int64_t rows, int64_t cols, double p, uint64_t seed,
+                                     uint64_t step, const uint64_t* step_dev, void* stream);
+
+/*
+ * Rows of a table W (V x D) looked up by token, and the table's gradient.
+ * ids: T token numbers on the device, id_bytes wide (4: int32, 8: int64).
+ *     Y[i, :]  = scale * W[ids[i], :]
+ *     dW[v, :] = base[v, :] + scale * sum_{i : ids[i] = v} dY[i, :]
+ * A negative number means no token: its row of Y is 0.  One >= V reads nothing:
+ * its row of Y is NaN.  Neither takes part in dW.  dW is overwritten in full;
+ * base (nullable: zeros) may be dW itself (same stride), whose rows without a
+ * token are then left alone.  Sums are fp32 in a fixed order, one rounding.
+ * Row strides in elements, any alignment.  Y and dW must share no memory with
+ * an input (other than dW with base, if it is base).
+ * snack_embed_workspace: bytes of ws for the gradient.  Asynchronous; same bits
+ * for the same inputs.  Errors: SNACK_E_NULL, SNACK_E_DTYPE (dtype, id_bytes),
+ * SNACK_E_SHAPE (sizes, strides, overlap), SNACK_E_OVERFLOW (T > 2^28, V > 2^30,
+ * D > 2^23, or 2^32 - 2^20 pieces of 16 bytes in the T or V rows),
+ * SNACK_E_WORKSPACE.
+ */
+SNACK_API snack_status snack_embed_fwd(snack_dtype dtype, const void* ids, int32_t id_bytes,
+                                       int64_t T, const void* W, int64_t ldw, int32_t V,
+                                       int32_t D, float scale, void* Y, int64_t ldy,
+                                       void* stream);
+SNACK_API snack_status snack_embed_workspace(snack_dtype dtype, int64_t T, int32_t V, int32_t D,
+                                             size_t* bytes);
+SNACK_API snack_status snack_embed_bwd(snack_dtype dtype, const void* ids, int32_t id_bytes,
+                                       int64_t T, const void* dY, int64_t lddy, int32_t V,
+                                       int32_t D, float scale, const void* base, int64_t ldb,
+                                       void* dW, int64_t lddw, void* ws, size_t ws_bytes,
+                                       void* stream);
+
+/*
+ * Log-probabilities of target tokens from logits X (T x V), and the logits'
+ * gradient.  With m_i = max_v X[i, v] and l_i = log sum_v exp(X[i, v] - m_i):
+ *     logp[i]    = (X[i, t_i] - m_i) - l_i           (fp32)
+ *     norm[2i]   = m_i, norm[2i + 1] = l_i           (fp32, for the gradient)
+ *     dX[i, v]   = dlogp[i] * ([v = t_i] - exp((X[i, v] - m_i) - l_i))
+ * targets: as the ids above.  A negative target means none: logp 0, a row of
+ * zeros in dX.  One >= V: logp NaN, a row of NaN.  Rows whose dlogp is 0, or
+ * without a target, are zeros in dX and their logits are not read.  Logits of
+ * -infinity have probability 0; a row of nothing else has m the lowest float, l
+ * -infinity, logp -infinity and a zero gradient.  A NaN or +infinity makes its
+ * row NaN.  dX may be X itself (same stride).  Outputs share no other memory.
+ * snack_logp_workspace: bytes of ws for snack_logp_fwd (may be 0).
+ * Asynchronous; same bits for the same inputs.  Errors: SNACK_E_NULL,
+ * SNACK_E_DTYPE (dtype, id_bytes), SNACK_E_SHAPE (V < 1, sizes, strides,
+ * overlap), SNACK_E_OVERFLOW (V > 2^30, T * ceil(V / n) >= 2^24 with n = 4,096
+ * fp32 or 8,192 bf16 logits), SNACK_E_WORKSPACE.
+ */
+SNACK_API snack_status snack_logp_workspace(snack_dtype dtype, int64_t T, int32_t V,
+                                            size_t* bytes);
+SNACK_API snack_status snack_logp_fwd(snack_dtype dtype, const void* X, int64_t ldx, int64_t T,
+                                      int32_t V, const void* targets, int32_t id_bytes,
+                                      float* logp, float* norm, void* ws, size_t ws_bytes,
+                                      void* stream);
+SNACK_API snack_status snack_logp_bwd(snack_dtype dtype, const float* dlogp, const void* X,
+                                      int64_t ldx, int64_t T, int32_t V, const void* targets,
+                                      int32_t id_bytes, const float* norm, void* dX, int64_t lddx,
+                                      void* stream);
+
+/*
+ * Losses of answers by the log-probabilities of their tokens, with the
+ * gradient.  A batch is S sequences among T tokens: sequence j has the tokens
+ * from starts[j] up to starts[j + 1] (device, S + 1 int32, not decreasing, in
+ * [0, T]; NULL: T / S tokens each).  mask (nullable, T bytes): tokens whose
+ * byte is 0 do not count, are not read, and have gradient 0, as tokens of no
+ * sequence have.  Per token arrays are fp32 and contiguous.
+ *
+ * snack_preference: sequence 2p is preferred to 2p + 1.  With
+ *     d_j = sum over j's counted tokens of (logps - ref)  (average: divided by
+ *           their number, or by 1 where there is none), h = d_2p - d_2p+1:
+ *     loss = 2 / S sum_p f(h)
+ *     SNACK_PREF_SIGMOID  f = -(1 - smoothing) log sigmoid(beta h)
+ *                             - smoothing log sigmoid(-beta h)
+ *     SNACK_PREF_HINGE    f = max(0, 1 - beta h)
+ *     SNACK_PREF_SQUARED  f = (h - 1 / (2 beta))^2
+ * ref (nullable: zeros).  rewards (S floats): beta d_j.
+ *
+ * snack_policy_loss: with A the advantage of the token (by_token) or of its
+ * sequence, r = exp(logps - old), k = ref - logps, at each counted token
+ *     f = -min(r A, clamp(r, 1 - low, 1 + high) A) + kl (exp(k) - k - 1)
+ * and loss = sum f / N over all N counted tokens, or (sequence_mean)
+ * 1 / S sum_j (sum f / n_j), empty ones as 0.  The clamp has no gradient where it
+ * decides; whether it does goes by logps - old against log(1 - low) and
+ * log(1 + high) in 64 bits.  old (nullable): logps itself, r = 1.  ref
+ * (nullable): no KL term.  stats (2 floats): the means over the N tokens of
+ * exp(k) - k - 1 and of whether the clamp decided.
+ *
+ * Both: dloss (nullable, device float: 1) is the loss's gradient; loss, rewards
+ * or stats, and dlogps (T floats, overwritten) are written if not NULL.  Sums
+ * are 64-bit.  No output shares memory with anything.  snack_seqs_workspace:
+ * bytes of ws for either (may be 0).  Asynchronous; same bits for the same
+ * inputs.  Errors: SNACK_E_NULL, SNACK_E_SHAPE (sizes, S odd for pairs, T not
+ * divisible by S without starts, beta <= 0 or infinite, smoothing outside [0, 1]
+ * or with another form than sigmoid, low outside [0, 1], high < 0, kl < 0,
+ * overlap), SNACK_E_NAN, SNACK_E_OVERFLOW (S > 2^24, T > 2^30),
+ * SNACK_E_WORKSPACE.
+ */
+#define SNACK_PREF_SIGMOID 0
+#define SNACK_PREF_HINGE 1
+#define SNACK_PREF_SQUARED 2
+typedef struct snack_seqs {
+  int32_t S, T;
+  const int32_t* starts;
+  const uint8_t* mask;
+} snack_seqs;
+typedef struct snack_pref {
+  double beta, smoothing;
+  int32_t form, average;
+} snack_pref;
+typedef struct snack_policy {
+  double low, high, kl;
+  int32_t by_token, sequence_mean;
+} snack_policy;
+
+SNACK_API snack_status snack_seqs_workspace(int32_t S, int32_t T, size_t* bytes);
+SNACK_API snack_status snack_preference(const snack_seqs* batch, const snack_pref* pref,
+                                        const float* logps, const float* ref, const float* dloss,
+                                        float* loss, float* rewards, float* dlogps, void* ws,
+                                        size_t ws_bytes, void* stream);
+SNACK_API snack_status snack_policy_loss(const snack_seqs* batch, const snack_policy* policy,
+                                         const float* logps, const float* old, const float* ref,
+                                         const float* advantages, const float* dloss, float* loss,
+                                         float* stats, float* dlogps, void* ws, size_t ws_bytes,
+                                         void* stream);
+
+/*
  * GELU with the exact error function, h = z * Phi(z), and its backward
  * dz = dh * (Phi(z) + z * phi(z)), elementwise over n fp32 values (the
  * nonlinearity between the two sparse layers of a GPT-2-shaped MLP block).

@@ -19,7 +19,15 @@ from .binding import (ACT_GELU, ACT_NONE, ACT_RELU, BATCH_MAJOR, BF16, CONV_NCHW
                       snack_spmm_fwd_act, snack_version, snack_calibrate,
                       snack_lora, snack_lora_workspace, snack_lora_fwd, snack_lora_bwd,
                       snack_grad_table, snack_grad_workspace, snack_grad_norm, snack_grad_clip,
+                      snack_dropout, snack_embed_workspace, snack_embed_fwd, snack_embed_bwd,
+                      snack_logp_workspace, snack_logp_fwd, snack_logp_bwd, snack_seqs,
+                      snack_seqs_workspace, snack_preference, snack_policy_loss,
                       status_str)
 from .adapters import LoraAdapters, lora_bwd, lora_fwd  # noqa: F401
 from .clip import clip_grad_norm_, clip_grads, grad_norm  # noqa: F401
+from .dropout import Dropout, dropout_bwd, dropout_fwd  # noqa: F401
 from .layer import SparseLinear, Topology  # noqa: F401
+from .losses import (policy_grads, policy_loss, preference_grads,  # noqa: F401
+                     preference_loss)
+from .tokens import (TokenEmbedding, embed_bwd, embed_fwd, logp_bwd, logp_fwd,  # noqa: F401
+                     token_logps)

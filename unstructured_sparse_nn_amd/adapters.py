@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import torch
 
+from .dropout import dropout_bwd, dropout_fwd, random_seed
 from .native import calls
 
 
@@ -56,6 +57,35 @@ class _LoraFn(torch.autograd.Function):
         return dx, dA, dB, gy if ctx.needs_input_grad[3] else None, None, None, None
 
 
+class _DroppedLoraFn(torch.autograd.Function):
+    """The same on dropout(x), which the backward makes again from x."""
+
+    @staticmethod
+    def forward(ctx, x, A, B, base, ids, scale, ranks, p, seed, step):
+        on_gpu = isinstance(step, torch.Tensor)
+        t = torch.empty(x.shape[0], A.shape[1], dtype=torch.float32, device=x.device)
+        y = lora_fwd(dropout_fwd(x, p, seed, step), ids, A, B, scale, ranks, base, t=t)
+        ctx.save_for_backward(x, A, B, ids, scale, ranks, t, step if on_gpu else None)
+        ctx.args = p, seed, None if on_gpu else step
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gy):
+        x, A, B, ids, scale, ranks, t, step = ctx.saved_tensors
+        p, seed, number = ctx.args
+        step = number if step is None else step
+        want = ctx.needs_input_grad[:3]
+        dx = dA = dB = None
+        if any(want):
+            if want[1]:
+                x = dropout_fwd(x, p, seed, step)
+            dx, dA, dB = lora_bwd(gy, x, ids, A, B, scale, ranks, t, want=want)
+            if want[0]:
+                dx = dropout_bwd(dx, p, seed, step, out=dx)
+        return (dx, dA, dB, gy if ctx.needs_input_grad[3] else None, *[None] * 6)
+
+
 class LoraAdapters(torch.nn.Module):
     """L trainable low-rank adapters of one projection.
 
@@ -63,14 +93,23 @@ class LoraAdapters(torch.nn.Module):
     an untrained adapter changes nothing.  ``ranks`` (a list) may give each
     adapter its own rank up to ``rank``; ``alpha / rank`` is the scale.
 
+    ``dropout``: in training, the adapters see x with that share of its elements
+    dropped (base does not).  Its mask comes from ``seed`` (drawn from torch's
+    generator if None) and ``step``, which counts the calls in training and is no
+    part of the state dict; a call may name its own, a number or one int64 on the
+    GPU (:mod:`.dropout`).
+
     Forward and backward can be captured into a graph.  As with any torch
     module, no output of an eager step may still hold these parameters' autograd
     graph while the backward is captured: torch would join the eager stream to
     the capture and end the process."""
 
     def __init__(self, in_features: int, out_features: int, adapters: int, rank: int,
-                 alpha: float = 16.0, ranks=None, dtype=torch.float32, device="cuda"):
+                 alpha: float = 16.0, ranks=None, dtype=torch.float32, device="cuda",
+                 dropout: float = 0.0, seed: int | None = None):
         super().__init__()
+        if not 0 <= dropout <= 1:
+            raise ValueError("dropout: from 0 to 1")
         if ranks is not None and (len(ranks) != adapters
                                   or not all(0 < r <= rank for r in ranks)):
             raise ValueError("ranks: one per adapter, from 1 to rank")
@@ -83,6 +122,9 @@ class LoraAdapters(torch.nn.Module):
                                                    device=device))
         self.register_buffer("ranks", None if ranks is None else torch.tensor(
             ranks, dtype=torch.int32, device=device))
+        self.dropout, self.seed, self.step = dropout, seed, 0
+        if dropout > 0 and seed is None:
+            self.seed = random_seed()
 
     def _apply(self, fn, recurse=True):
         # the kernels read scale as float32 and ranks as int32, whatever type the
@@ -94,8 +136,13 @@ class LoraAdapters(torch.nn.Module):
                 self._buffers[k] = v.to(self._buffers[k].device)
         return self
 
-    def forward(self, x, ids, base=None):
+    def forward(self, x, ids, base=None, step=None):
         """base + each row's adapter applied to x (rows of x: tokens)."""
+        if self.training and self.dropout > 0:
+            if step is None:
+                step, self.step = self.step, self.step + 1
+            return _DroppedLoraFn.apply(x, self.A, self.B, base, ids, self.scale, self.ranks,
+                                        self.dropout, self.seed, step)
         if torch.is_grad_enabled():
             return _LoraFn.apply(x, self.A, self.B, base, ids, self.scale, self.ranks)
         return lora_fwd(x, ids, self.A, self.B, self.scale, self.ranks, base)

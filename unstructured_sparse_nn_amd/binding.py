@@ -27,6 +27,7 @@ PLAN_NODE_MAJOR_ONLY = 1
 PRUNE_SORT_PLAN = 1
 HOST_WORDS_BYTES = 64
 STATIC_WS_MAX = 32 << 20
+PREF_SIGMOID, PREF_HINGE, PREF_SQUARED = 0, 1, 2
 BATCH_MAJOR, NODE_MAJOR = 0, 1
 PLAN_SLOTS = 16
 
@@ -68,6 +69,24 @@ class SnackLora(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int32), ("K", ctypes.c_int32), ("L", ctypes.c_int32),
                 ("R", ctypes.c_int32), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
                 ("scale", ctypes.c_void_p), ("rank", ctypes.c_void_p)]
+
+
+class SnackSeqs(ctypes.Structure):
+    """Mirror of ``struct snack_seqs``."""
+    _fields_ = [("S", ctypes.c_int32), ("T", ctypes.c_int32), ("starts", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p)]
+
+
+class SnackPref(ctypes.Structure):
+    """Mirror of ``struct snack_pref``."""
+    _fields_ = [("beta", ctypes.c_double), ("smoothing", ctypes.c_double),
+                ("form", ctypes.c_int32), ("average", ctypes.c_int32)]
+
+
+class SnackPolicy(ctypes.Structure):
+    """Mirror of ``struct snack_policy``."""
+    _fields_ = [("low", ctypes.c_double), ("high", ctypes.c_double), ("kl", ctypes.c_double),
+                ("by_token", ctypes.c_int32), ("sequence_mean", ctypes.c_int32)]
 
 
 class SnackPlan(ctypes.Structure):
@@ -137,6 +156,18 @@ def _load():
         "snack_grad_workspace": ([i32, ctypes.POINTER(sz)], i32),
         "snack_grad_norm": ([P, i32, P, P, sz, P], i32),
         "snack_grad_clip": ([P, i32, ctypes.c_float, ctypes.c_float, P, P, sz, P], i32),
+        "snack_dropout": ([i32, P, i64, P, i64, P, i64, i64, i64, ctypes.c_double, u64, u64, P, P],
+                          i32),
+        "snack_embed_fwd": ([i32, P, i32, i64, P, i64, i32, i32, ctypes.c_float, P, i64, P], i32),
+        "snack_embed_workspace": ([i32, i64, i32, i32, ctypes.POINTER(sz)], i32),
+        "snack_embed_bwd": ([i32, P, i32, i64, P, i64, i32, i32, ctypes.c_float, P, i64, P, i64, P,
+                             sz, P], i32),
+        "snack_logp_workspace": ([i32, i64, i32, ctypes.POINTER(sz)], i32),
+        "snack_logp_fwd": ([i32, P, i64, i64, i32, P, i32, P, P, P, sz, P], i32),
+        "snack_logp_bwd": ([i32, P, P, i64, i64, i32, P, i32, P, P, i64, P], i32),
+        "snack_seqs_workspace": ([i32, i32, ctypes.POINTER(sz)], i32),
+        "snack_preference": ([P, P, P, P, P, P, P, P, P, sz, P], i32),
+        "snack_policy_loss": ([P, P, P, P, P, P, P, P, P, P, P, sz, P], i32),
         "snack_gelu_fwd": ([P, P, i64, P], i32),
         "snack_gelu_bwd": ([P, P, P, i64, P], i32),
         "snack_dense_fwd": ([P, P, i32, i32, i32, P, i32, P, P], i32),
@@ -514,6 +545,84 @@ def snack_grad_clip(table, count: int, max_norm: float, eps: float, norm, ws, st
     _check(_lib.snack_grad_clip(_grad_table(table, count), count, max_norm, eps, _ptr(norm),
                                 _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream)),
            "snack_grad_clip")
+
+
+def snack_dropout(X, ldx: int, residual, ldr: int, Y, ldy: int, rows: int, cols: int, p: float,
+                  seed: int, step: int = 0, step_dev=None, stream=None, dtype=None):
+    """Y = residual + dropout(X); see the header for the generator."""
+    dt = _dtype(X, Y, dtype=dtype)
+    _check(_lib.snack_dropout(dt, _ptr(X), ldx, _ptr(residual), ldr, _ptr(Y), ldy, rows, cols, p,
+                              seed, step, _ptr(step_dev), _stream(stream)), "snack_dropout")
+
+
+def snack_embed_fwd(ids, id_bytes: int, T: int, W, ldw: int, V: int, D: int, scale: float, Y,
+                    ldy: int, stream=None, dtype=None):
+    dt = _dtype(W, Y, dtype=dtype)
+    _check(_lib.snack_embed_fwd(dt, _ptr(ids), id_bytes, T, _ptr(W), ldw, V, D, scale, _ptr(Y),
+                                ldy, _stream(stream)), "snack_embed_fwd")
+
+
+def snack_embed_workspace(dtype: int, T: int, V: int, D: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.snack_embed_workspace(dtype, T, V, D, ctypes.byref(out)), "snack_embed_workspace")
+    return out.value
+
+
+def snack_embed_bwd(ids, id_bytes: int, T: int, dY, lddy: int, V: int, D: int, scale: float, base,
+                    ldb: int, dW, lddw: int, ws, stream=None, ws_bytes=None, dtype=None):
+    """dW = base + scale * (sums of dY's rows by token)."""
+    dt = _dtype(dY, dW, dtype=dtype)
+    _check(_lib.snack_embed_bwd(dt, _ptr(ids), id_bytes, T, _ptr(dY), lddy, V, D, scale, _ptr(base),
+                                ldb, _ptr(dW), lddw, _ptr(ws), _nbytes(ws, ws_bytes),
+                                _stream(stream)), "snack_embed_bwd")
+
+
+def snack_logp_workspace(dtype: int, T: int, V: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.snack_logp_workspace(dtype, T, V, ctypes.byref(out)), "snack_logp_workspace")
+    return out.value
+
+
+def snack_logp_fwd(X, ldx: int, T: int, V: int, targets, id_bytes: int, logp, norm, ws=None,
+                   stream=None, ws_bytes=None, dtype=None):
+    dt = _dtype(X, dtype=dtype)
+    _check(_lib.snack_logp_fwd(dt, _ptr(X), ldx, T, V, _ptr(targets), id_bytes, _ptr(logp),
+                               _ptr(norm), _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream)),
+           "snack_logp_fwd")
+
+
+def snack_logp_bwd(dlogp, X, ldx: int, T: int, V: int, targets, id_bytes: int, norm, dX, lddx: int,
+                   stream=None, dtype=None):
+    dt = _dtype(X, dX, dtype=dtype)
+    _check(_lib.snack_logp_bwd(dt, _ptr(dlogp), _ptr(X), ldx, T, V, _ptr(targets), id_bytes,
+                               _ptr(norm), _ptr(dX), lddx, _stream(stream)), "snack_logp_bwd")
+
+
+def snack_seqs(S: int, T: int, starts=None, mask=None) -> SnackSeqs:
+    """The batch's struct: starts (S + 1 int32) and mask (T bytes) are device
+    arrays, both optional."""
+    return SnackSeqs(S, T, _ptr(starts), _ptr(mask))
+
+
+def snack_seqs_workspace(S: int, T: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.snack_seqs_workspace(S, T, ctypes.byref(out)), "snack_seqs_workspace")
+    return out.value
+
+
+def snack_preference(batch: SnackSeqs, pref: SnackPref, logps, ref, dloss, loss, rewards, dlogps,
+                     ws=None, stream=None, ws_bytes=None):
+    _check(_lib.snack_preference(ctypes.byref(batch), ctypes.byref(pref), _ptr(logps), _ptr(ref),
+                                 _ptr(dloss), _ptr(loss), _ptr(rewards), _ptr(dlogps), _ptr(ws),
+                                 _nbytes(ws, ws_bytes), _stream(stream)), "snack_preference")
+
+
+def snack_policy_loss(batch: SnackSeqs, policy: SnackPolicy, logps, old, ref, advantages, dloss,
+                      loss, stats, dlogps, ws=None, stream=None, ws_bytes=None):
+    _check(_lib.snack_policy_loss(ctypes.byref(batch), ctypes.byref(policy), _ptr(logps),
+                                  _ptr(old), _ptr(ref), _ptr(advantages), _ptr(dloss), _ptr(loss),
+                                  _ptr(stats), _ptr(dlogps), _ptr(ws), _nbytes(ws, ws_bytes),
+                                  _stream(stream)), "snack_policy_loss")
 
 
 def snack_gelu_fwd(z, h, n=None, stream=None):

@@ -23,6 +23,8 @@
 
 #include "common.h"
 #include "internal.h"
+#include "pieces.h"
+#include "spans.h"
 
 namespace snk {
 namespace {
@@ -59,23 +61,8 @@ __device__ __forceinline__ int wave_id() {
   return __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
 }
 
-// ------------------------------------------------------------- 16-byte pieces
-// Rows start at any element, so pieces are loaded and stored without an
-// alignment claim; the hardware takes a 16-byte access at any address.
-template <typename T> constexpr int EL = 16 / sizeof(T);
-template <typename T> struct __attribute__((aligned(16))) frag { uint32_t w[4]; };
+using snk::load_frag;  // beside the forms below
 
-__device__ __forceinline__ float at(const frag<bf16>& f, int e) {
-  return __uint_as_float(e & 1 ? f.w[e / 2] & 0xFFFF0000u : f.w[e / 2] << 16);
-}
-__device__ __forceinline__ float at(const frag<float>& f, int e) { return __uint_as_float(f.w[e]); }
-
-template <typename T>
-__device__ __forceinline__ frag<T> load_frag(const T* p) {
-  frag<T> f;
-  __builtin_memcpy(&f, p, 16);
-  return f;
-}
 __device__ __forceinline__ uint32_t pick(bool first, uint32_t a, uint32_t b) { return first ? a : b; }
 
 // f moved down by sh elements, zeros behind.
@@ -119,19 +106,6 @@ __device__ __forceinline__ frag<T> load_frag(const T* p, int32_t n, int64_t row)
       if (e * (int)sizeof(T) / 4 == q) f.w[q] |= v << (8 * (e * sizeof(T) % 4));
   }
   return f;
-}
-template <typename T>
-__device__ __forceinline__ void store_frag(T* p, const frag<T>& f, int32_t n) {
-  if (n >= EL<T>) {
-    __builtin_memcpy(p, &f, 16);
-  } else {
-#pragma unroll
-    for (int e = 0; e < EL<T> - 1; ++e)
-      if (e < n) {
-        const uint32_t v = f.w[e * sizeof(T) / 4] >> (8 * (e * sizeof(T) % 4));
-        __builtin_memcpy(p + e, &v, sizeof(T));
-      }
-  }
 }
 // Pieces of E elements, loaded and stored likewise.
 template <typename T, int E> struct piece { uint32_t w[E * sizeof(T) / 4]; };
@@ -188,21 +162,6 @@ __device__ __forceinline__ f4 mma(const frag<float>& a, const frag<float>& b, f4
 #pragma unroll
   for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(at(a, e), at(b, e), c, 0, 0, 0);
   return c;
-}
-
-// Two floats as bf16, rounded to nearest even, in one dword.
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  typedef float f2 __attribute__((ext_vector_type(2)));
-  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{a, b}), b2));
-}
-__device__ __forceinline__ frag<bf16> to_frag(const float (&v)[8]) {
-  return frag<bf16>{{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
-                     bf16_pair(v[6], v[7])}};
-}
-__device__ __forceinline__ frag<float> to_frag(const float (&v)[4]) {
-  return frag<float>{{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                      __float_as_uint(v[3])}};
 }
 
 template <int E>
@@ -1499,49 +1458,6 @@ snack_status check_lora(const snack_lora* p, snack_dtype dt, int32_t T, bool bac
     return SNACK_E_SHAPE;
   if (T > max_tokens(backward) || p->M > MAX_FEATURES || p->K > MAX_FEATURES) return SNACK_E_OVERFLOW;
   return SNACK_OK;
-}
-
-// Memory of a call: n rows of `row` bytes, ld bytes apart (wide: sizes and
-// strides are the caller's).
-struct span_t {
-  __int128 p, row, ld, n;
-  span_t(const void* at, __int128 bytes, __int128 stride = 0, __int128 rows = 1)
-      : p((uintptr_t)at), row(bytes), ld(stride), n(at && bytes > 0 ? rows : 0) {
-    if (n > 1 && ld == row) row *= n, n = 1;
-  }
-  __int128 end() const { return p + (n - 1) * ld + row; }
-  // Whether a row meets the bytes from lo up to hi.
-  bool meets(__int128 lo, __int128 hi) const {
-    // the first row that ends past lo
-    const __int128 i = lo < p + row ? 0 : n == 1 ? 1 : (lo - row - p) / ld + 1;
-    return i < n && p + i * ld < hi;
-  }
-};
-
-// Whether a byte belongs to both.  Rows may lie between the other's rows.
-bool overlap(const span_t& a, const span_t& b) {
-  if (a.n == 0 || b.n == 0 || a.end() <= b.p || b.end() <= a.p) return false;
-  if (a.n > b.n) return overlap(b, a);
-  if (a.n > 1 && a.ld == b.ld) {  // row i of b begins `at` bytes after row i + q of a
-    const __int128 d = b.p - a.p, q = d >= 0 ? d / a.ld : -((a.ld - 1 - d) / a.ld), at = d - q * a.ld;
-    auto both = [&](__int128 k) { return std::max<__int128>(0, -k) < std::min(b.n, a.n - k); };
-    return (at < a.row && both(q)) || (at + b.row > a.ld && both(q + 1));
-  }
-  for (__int128 i = 0; i < a.n; ++i)
-    if (b.meets(a.p + i * a.ld, a.p + i * a.ld + a.row)) return true;
-  return false;
-}
-
-// Whether an output lies over an input or over another output.
-template <size_t O, size_t I>
-bool any_overlap(const span_t (&out)[O], const span_t (&in)[I]) {
-  for (size_t o = 0; o < O; ++o) {
-    for (const span_t& i : in)
-      if (overlap(out[o], i)) return true;
-    for (size_t q = 0; q < o; ++q)
-      if (overlap(out[o], out[q])) return true;
-  }
-  return false;
 }
 
 // Tokens up to which k_lora_few is taken.

@@ -1,5 +1,6 @@
-// torch_calls.cpp -- the torch-facing calls of the low-rank adapters and of
-// gradient clipping: checks of the tensors, outputs, workspace and the call
+// torch_calls.cpp -- the torch-facing calls of the low-rank adapters, of
+// gradient clipping, and of dropout, embedding, token log-probabilities and the
+// losses: checks of the tensors, outputs, workspace and the call
 // into the HIP library, with no Python between them.  One token through an
 // adapter costs the GPU 6 us and 48 gradients of a small model 10 us; the same
 // checks written in Python took 13 us and 58 us, 590 us for 600 gradients.
@@ -17,6 +18,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstddef>
+#include <cstring>
 #include <vector>
 
 #include "snack.h"
@@ -32,6 +35,16 @@ struct library_t {
   decltype(&snack_grad_workspace) grad_workspace;
   decltype(&snack_grad_norm) grad_norm;
   decltype(&snack_grad_clip) grad_clip;
+  decltype(&snack_dropout) dropout;
+  decltype(&snack_embed_fwd) embed_fwd;
+  decltype(&snack_embed_workspace) embed_workspace;
+  decltype(&snack_embed_bwd) embed_bwd;
+  decltype(&snack_logp_workspace) logp_workspace;
+  decltype(&snack_logp_fwd) logp_fwd;
+  decltype(&snack_logp_bwd) logp_bwd;
+  decltype(&snack_seqs_workspace) seqs_workspace;
+  decltype(&snack_preference) preference;
+  decltype(&snack_policy_loss) policy_loss;
   PyObject* check;  // check(status, what) raises
 } lib;
 
@@ -325,18 +338,390 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------- dropout, tokens and losses
+struct matrix_t { Tensor t; int64_t rows, cols, ld; };
+
+// x of any shape as rows of its last axis, `ld` elements apart.  must: x itself
+// (an output); otherwise what does not lie so is copied.
+matrix_t matrix(const Tensor& x, const char* name, bool must) {
+  const int64_t n = x.dim(), cols = n ? x.size(n - 1) : 1;
+  if (x.is_contiguous()) return {x, cols ? x.numel() / cols : 0, cols, cols};
+  bool fits = x.numel() == 0 || cols == 1 || x.stride(n - 1) == 1;
+  int64_t rows = 1, ld = cols, next = 0;  // next: the stride that one more axis has to have
+  for (int64_t d = n - 2; d >= 0; --d) {
+    if (x.size(d) == 1) continue;
+    if (rows == 1) ld = x.stride(d);
+    else if (x.stride(d) != next) fits = false;
+    rows *= x.size(d);
+    next = x.stride(d) * x.size(d);
+  }
+  if (fits && (ld >= cols || rows <= 1)) return {x, rows, cols, rows > 1 ? ld : cols};
+  if (must) refuse(PyExc_ValueError, "%s: rows must be contiguous, evenly apart and must not overlap", name);
+  return {x.contiguous(), cols ? x.numel() / cols : 0, cols, cols};
+}
+
+snack_dtype dtype_of(const Tensor& x, const char* name) {
+  const at::ScalarType type = x.scalar_type();
+  if (type != at::kFloat && type != at::kBFloat16)
+    refuse(PyExc_TypeError, "%s: unsupported dtype %s", name, c10::toString(type));
+  if (!x.is_cuda()) refuse(PyExc_TypeError, "%s: expected a tensor on the GPU", name);
+  return type == at::kBFloat16 ? SNACK_BF16 : SNACK_F32;
+}
+
+void same(const Tensor& t, const char* name, const Tensor& like, at::IntArrayRef sizes) {
+  if (t.scalar_type() != like.scalar_type() || t.device() != like.device())
+    refuse(PyExc_TypeError, "%s: expected dtype %s on the other tensors' device", name,
+           c10::toString(like.scalar_type()));
+  if (t.sizes() != sizes) refuse(PyExc_ValueError, "%s: unexpected shape", name);
+}
+
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw refused();
+  return v;
+}
+int truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw refused();
+  return v;
+}
+
+// Token numbers: int32 or int64, any shape.
+struct tokens_t { Tensor t; int32_t bytes; };
+tokens_t tokens(const Tensor& ids, const char* name, const Tensor& like) {
+  if (ids.scalar_type() != at::kInt && ids.scalar_type() != at::kLong)
+    refuse(PyExc_TypeError, "%s: expected int32 or int64", name);
+  if (ids.device() != like.device())
+    refuse(PyExc_TypeError, "%s: expected on the other tensors' device", name);
+  return {ids.contiguous(), ids.scalar_type() == at::kLong ? 8 : 4};
+}
+
+std::vector<int64_t> with_axis(at::IntArrayRef sizes, int64_t n) {
+  std::vector<int64_t> v(sizes.begin(), sizes.end());
+  v.push_back(n);
+  return v;
+}
+
+PyObject* tuple(std::initializer_list<Tensor> items) {
+  PyObject* r = PyTuple_New((Py_ssize_t)items.size());
+  if (!r) throw refused();
+  Py_ssize_t i = 0;
+  for (const Tensor& t : items) PyTuple_SET_ITEM(r, i++, wrap(t));
+  return r;
+}
+
+Tensor scratch(const Tensor& like, size_t n) { return n ? bytes_on(like, n) : Tensor(); }
+
+// dropout(x, p, seed, step, step tensor or None, residual, out) -> out
+PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 7) refuse(PyExc_TypeError, "7 arguments expected");
+    const Tensor& x0 = tensor(a[0], "x");
+    const double p = number(a[1]);
+    const uint64_t seed = PyLong_AsUnsignedLongLongMask(a[2]);
+    const uint64_t step = PyLong_AsUnsignedLongLongMask(a[3]);
+    if (PyErr_Occurred()) throw refused();
+    const Tensor more = maybe(a[4], "step"), res0 = maybe(a[5], "residual");
+    Tensor out = maybe(a[6], "out");
+    const snack_dtype dt = dtype_of(x0, "x");
+    if (more.defined() && (more.scalar_type() != at::kLong || more.numel() != 1 ||
+                           more.device() != x0.device()))
+      refuse(PyExc_TypeError, "step: expected a number or one int64 on x's device");
+    if (res0.defined()) same(res0, "residual", x0, x0.sizes());
+    if (out.defined()) same(out, "out", x0, x0.sizes());
+    const c10::DeviceGuard guard(x0.device());
+    if (!out.defined()) out = at::empty(x0.sizes(), x0.options());
+    matrix_t x = matrix(x0, "x", false), y = matrix(out, "out", true), r = x;
+    if (res0.defined()) r = matrix(res0, "residual", false);
+    // one contiguous tensor has no rows: the others' count then
+    const int64_t rows = x.rows, cols = x.cols;
+    void* s = stream();
+    check(unlocked([&] {
+            return lib.dropout(dt, ptr(x.t), x.ld, res0.defined() ? ptr(r.t) : nullptr, r.ld,
+                               ptr(out), y.ld, rows, cols, p, seed, step,
+                               (const uint64_t*)ptr(more), s);
+          }),
+          "snack_dropout");
+    if (a[6] != Py_None) written(out);
+    return wrap(out);
+  });
+}
+
+// embed_fwd(ids, weight, scale, out) -> out
+PyObject* embed_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 4) refuse(PyExc_TypeError, "4 arguments expected");
+    const Tensor &ids0 = tensor(a[0], "ids"), &w0 = tensor(a[1], "weight");
+    const double scale = number(a[2]);
+    Tensor out = maybe(a[3], "out");
+    const snack_dtype dt = dtype_of(w0, "weight");
+    if (w0.dim() != 2) refuse(PyExc_ValueError, "weight: expected a matrix");
+    if (w0.size(0) > INT32_MAX || w0.size(1) > INT32_MAX)
+      refuse(PyExc_ValueError, "a size does not fit 32 bits");
+    const c10::DeviceGuard guard(w0.device());
+    const tokens_t ids = tokens(ids0, "ids", w0);
+    const std::vector<int64_t> sizes = with_axis(ids0.sizes(), w0.size(1));
+    if (out.defined()) same(out, "out", w0, sizes);
+    else out = at::empty(sizes, w0.options());
+    const matrix_t w = matrix(w0, "weight", false), y = matrix(out, "out", true);
+    void* s = stream();
+    check(unlocked([&] {
+            return lib.embed_fwd(dt, ptr(ids.t), ids.bytes, ids.t.numel(), ptr(w.t), w.ld,
+                                 (int32_t)w0.size(0), (int32_t)w0.size(1), (float)scale, ptr(out),
+                                 y.ld, s);
+          }),
+          "snack_embed_fwd");
+    if (a[3] != Py_None) written(out);
+    return wrap(out);
+  });
+}
+
+// embed_bwd(dy, ids, rows, scale, base, out) -> out
+PyObject* embed_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 6) refuse(PyExc_TypeError, "6 arguments expected");
+    const Tensor &dy0 = tensor(a[0], "dy"), &ids0 = tensor(a[1], "ids");
+    const long long V = PyLong_AsLongLong(a[2]);
+    if (PyErr_Occurred()) throw refused();
+    const double scale = number(a[3]);
+    const Tensor base0 = maybe(a[4], "base");
+    Tensor out = maybe(a[5], "out");
+    const snack_dtype dt = dtype_of(dy0, "dy");
+    if (dy0.dim() < 1) refuse(PyExc_ValueError, "dy: expected rows");
+    const int64_t D = dy0.size(dy0.dim() - 1);
+    if (V < 0 || V > INT32_MAX || D > INT32_MAX)
+      refuse(PyExc_ValueError, "a size does not fit 31 bits");
+    same(dy0, "dy", dy0, with_axis(ids0.sizes(), D));
+    const c10::DeviceGuard guard(dy0.device());
+    const tokens_t ids = tokens(ids0, "ids", dy0);
+    if (base0.defined()) same(base0, "base", dy0, {V, D});
+    if (out.defined()) same(out, "out", dy0, {V, D});
+    else out = at::empty({V, D}, dy0.options());
+    const matrix_t dy = matrix(dy0, "dy", false), w = matrix(out, "out", true);
+    matrix_t base = w;
+    if (base0.defined()) base = matrix(base0, "base", false);
+    size_t need = 0;
+    check(lib.embed_workspace(dt, ids.t.numel(), (int32_t)V, (int32_t)D, &need),
+          "snack_embed_workspace");
+    const Tensor ws = scratch(dy0, need);
+    void* s = stream();
+    check(unlocked([&] {
+            return lib.embed_bwd(dt, ptr(ids.t), ids.bytes, ids.t.numel(), ptr(dy.t), dy.ld,
+                                 (int32_t)V, (int32_t)D, (float)scale,
+                                 base0.defined() ? ptr(base.t) : nullptr, base.ld, ptr(out), w.ld,
+                                 ptr(ws), need, s);
+          }),
+          "snack_embed_bwd");
+    if (a[5] != Py_None) written(out);
+    return wrap(out);
+  });
+}
+
+struct logits_t { matrix_t x; tokens_t t; int32_t V; int64_t T; snack_dtype dt; };
+
+logits_t logits_of(const Tensor& x0, const Tensor& t0) {
+  const snack_dtype dt = dtype_of(x0, "logits");
+  if (x0.dim() < 1) refuse(PyExc_ValueError, "logits: expected rows");
+  const int64_t V = x0.size(x0.dim() - 1);
+  if (V < 1 || V > INT32_MAX) refuse(PyExc_ValueError, "logits: rows must have 1 to 2^31 - 1");
+  same(x0, "targets and logits", x0, with_axis(t0.sizes(), V));
+  return {matrix(x0, "logits", false), tokens(t0, "targets", x0), (int32_t)V, t0.numel(), dt};
+}
+
+// logp_fwd(logits, targets) -> (logp, norm)
+PyObject* logp_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 2) refuse(PyExc_TypeError, "2 arguments expected");
+    const Tensor &x0 = tensor(a[0], "logits"), &t0 = tensor(a[1], "targets");
+    const c10::DeviceGuard guard(x0.device());
+    const logits_t l = logits_of(x0, t0);
+    const auto f32 = x0.options().dtype(at::kFloat);
+    const Tensor logp = at::empty(t0.sizes(), f32), norm = at::empty(with_axis(t0.sizes(), 2), f32);
+    size_t need = 0;
+    check(lib.logp_workspace(l.dt, l.T, l.V, &need), "snack_logp_workspace");
+    const Tensor ws = scratch(x0, need);
+    void* s = stream();
+    check(unlocked([&] {
+            return lib.logp_fwd(l.dt, ptr(l.x.t), l.x.ld, l.T, l.V, ptr(l.t.t), l.t.bytes,
+                                (float*)ptr(logp), (float*)ptr(norm), ptr(ws), need, s);
+          }),
+          "snack_logp_fwd");
+    return tuple({logp, norm});
+  });
+}
+
+// logp_bwd(dlogp, logits, targets, norm, out) -> out
+PyObject* logp_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 5) refuse(PyExc_TypeError, "5 arguments expected");
+    const Tensor &g0 = tensor(a[0], "dlogp"), &x0 = tensor(a[1], "logits"),
+                 &t0 = tensor(a[2], "targets"), &n0 = tensor(a[3], "norm");
+    Tensor out = maybe(a[4], "out");
+    const c10::DeviceGuard guard(x0.device());
+    const logits_t l = logits_of(x0, t0);
+    for (const Tensor* t : {&g0, &n0})
+      if (t->scalar_type() != at::kFloat || t->device() != x0.device())
+        refuse(PyExc_TypeError, "dlogp and norm: expected float32 on the logits' device");
+    if (g0.sizes() != t0.sizes() || n0.sizes() != at::IntArrayRef(with_axis(t0.sizes(), 2)))
+      refuse(PyExc_ValueError, "dlogp: expected the targets' shape, norm: one axis of 2 more");
+    const Tensor g = g0.contiguous(), norm = n0.contiguous();
+    if (out.defined()) same(out, "out", x0, x0.sizes());
+    else out = at::empty(x0.sizes(), x0.options());
+    const matrix_t y = matrix(out, "out", true);
+    void* s = stream();
+    check(unlocked([&] {
+            return lib.logp_bwd(l.dt, (const float*)ptr(g), ptr(l.x.t), l.x.ld, l.T, l.V,
+                                ptr(l.t.t), l.t.bytes, (const float*)ptr(norm), ptr(out), y.ld, s);
+          }),
+          "snack_logp_bwd");
+    if (a[4] != Py_None) written(out);
+    return wrap(out);
+  });
+}
+
+// The sequences of per-token tensors, and the tensors made contiguous.
+struct answers_t {
+  snack_seqs q;
+  Tensor logps, starts, mask;
+  size_t need;
+};
+
+Tensor per_token(PyObject* o, const char* name, const Tensor& logps) {
+  Tensor t = maybe(o, name);
+  if (!t.defined()) return t;
+  same(t, name, logps, logps.sizes());
+  return t.contiguous();
+}
+
+answers_t answers_of(PyObject* logps0, PyObject* starts0, PyObject* mask0) {
+  answers_t r{};
+  const Tensor& lp = tensor(logps0, "logps");
+  if (lp.scalar_type() != at::kFloat || !lp.is_cuda())
+    refuse(PyExc_TypeError, "logps: expected float32 on the GPU");
+  if (lp.numel() > INT32_MAX) refuse(PyExc_ValueError, "too many tokens");
+  r.logps = lp.contiguous();
+  r.starts = maybe(starts0, "starts");
+  int64_t S;
+  if (r.starts.defined()) {
+    if (r.starts.scalar_type() != at::kInt || r.starts.dim() != 1 || r.starts.numel() < 1 ||
+        r.starts.device() != lp.device())
+      refuse(PyExc_ValueError, "starts: expected a vector of int32 on the device of logps, one "
+             "more than sequences");
+    r.starts = r.starts.contiguous();
+    S = r.starts.numel() - 1;
+  } else {
+    if (lp.dim() != 2 && lp.dim() != 1)
+      refuse(PyExc_ValueError, "logps: without starts, a row for each sequence expected");
+    S = lp.dim() == 2 ? lp.size(0) : 1;
+  }
+  if (S > INT32_MAX) refuse(PyExc_ValueError, "too many sequences");
+  r.mask = maybe(mask0, "mask");
+  if (r.mask.defined()) {
+    if ((r.mask.scalar_type() != at::kBool && r.mask.scalar_type() != at::kByte) ||
+        r.mask.device() != lp.device() || r.mask.sizes() != lp.sizes())
+      refuse(PyExc_ValueError, "mask: expected bool or uint8 of the shape and device of logps");
+    r.mask = r.mask.contiguous();
+  }
+  r.q = {(int32_t)S, (int32_t)lp.numel(), (const int32_t*)ptr(r.starts),
+         r.mask.defined() && lp.numel() ? (const uint8_t*)ptr(r.mask) : nullptr};
+  check(lib.seqs_workspace(r.q.S, r.q.T, &r.need), "snack_seqs_workspace");
+  return r;
+}
+
+const float* dloss_of(PyObject* o, const Tensor& logps, Tensor& keep) {
+  keep = maybe(o, "dloss");
+  if (keep.defined() && (keep.scalar_type() != at::kFloat || keep.numel() != 1 ||
+                         keep.device() != logps.device()))
+    refuse(PyExc_TypeError, "dloss: expected one float32 on the device of logps");
+  return (const float*)ptr(keep);
+}
+
+// preference(logps, starts, ref, mask, beta, smoothing, form, average, dloss, loss?, grad?)
+//   -> (loss, rewards, grad)
+PyObject* preference(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 11) refuse(PyExc_TypeError, "11 arguments expected");
+    const answers_t b = answers_of(a[0], a[1], a[3]);
+    const Tensor& lp0 = tensor(a[0], "logps");
+    const Tensor ref = per_token(a[2], "ref", lp0);
+    const long form = PyLong_AsLong(a[6]);
+    if (PyErr_Occurred()) throw refused();
+    const snack_pref pref{number(a[4]), number(a[5]), (int32_t)form, truth(a[7])};
+    const bool want_loss = truth(a[9]), want = truth(a[10]);
+    Tensor dl;
+    const float* dloss = dloss_of(a[8], lp0, dl);
+    const c10::DeviceGuard guard(lp0.device());
+    Tensor loss, rewards, grad;
+    if (want_loss) {
+      loss = at::empty({}, b.logps.options());
+      rewards = at::empty({b.q.S / 2, 2}, b.logps.options());
+    }
+    if (want) grad = at::empty(lp0.sizes(), b.logps.options());
+    const Tensor ws = scratch(b.logps, b.need);
+    void* s = stream();
+    check(unlocked([&] {
+            return lib.preference(&b.q, &pref, (const float*)ptr(b.logps), (const float*)ptr(ref),
+                                  dloss, (float*)ptr(loss), (float*)ptr(rewards),
+                                  (float*)ptr(grad), ptr(ws), b.need, s);
+          }),
+          "snack_preference");
+    return tuple({loss, rewards, grad});
+  });
+}
+
+// policy(logps, old, advantages, starts, ref, mask, low, high, kl, by tokens?, sequence means?,
+//        dloss, loss?, grad?) -> (loss, stats, grad)
+PyObject* policy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 14) refuse(PyExc_TypeError, "14 arguments expected");
+    const answers_t b = answers_of(a[0], a[3], a[5]);
+    const Tensor& lp0 = tensor(a[0], "logps");
+    const Tensor old = per_token(a[1], "old", lp0), ref = per_token(a[4], "ref", lp0);
+    const snack_policy policy{number(a[6]), number(a[7]), number(a[8]), truth(a[9]), truth(a[10])};
+    const Tensor& adv0 = tensor(a[2], "advantages");
+    if (adv0.scalar_type() != at::kFloat || adv0.device() != lp0.device())
+      refuse(PyExc_TypeError, "advantages: expected float32 on the device of logps");
+    if (policy.by_token ? adv0.sizes() != lp0.sizes() : adv0.dim() != 1 || adv0.size(0) != b.q.S)
+      refuse(PyExc_ValueError, "advantages: expected one for each %s",
+             policy.by_token ? "token" : "sequence");
+    const Tensor adv = adv0.contiguous();
+    const bool want_loss = truth(a[12]), want = truth(a[13]);
+    Tensor dl;
+    const float* dloss = dloss_of(a[11], lp0, dl);
+    const c10::DeviceGuard guard(lp0.device());
+    Tensor loss, stats, grad;
+    if (want_loss) {
+      loss = at::empty({}, b.logps.options());
+      stats = at::empty({2}, b.logps.options());
+    }
+    if (want) grad = at::empty(lp0.sizes(), b.logps.options());
+    const Tensor ws = scratch(b.logps, b.need);
+    void* s = stream();
+    check(unlocked([&] {
+            return lib.policy_loss(&b.q, &policy, (const float*)ptr(b.logps),
+                                   (const float*)ptr(old), (const float*)ptr(ref),
+                                   (const float*)ptr(adv), dloss, (float*)ptr(loss),
+                                   (float*)ptr(stats), (float*)ptr(grad), ptr(ws), b.need, s);
+          }),
+          "snack_policy_loss");
+    return tuple({loss, stats, grad});
+  });
+}
+
 // bind(check, addresses of the library's functions in library_t's order)
 PyObject* bind(PyObject*, PyObject* args) {
-  unsigned long long p[6];
-  PyObject* check;
-  if (!PyArg_ParseTuple(args, "OKKKKKK", &check, &p[0], &p[1], &p[2], &p[3], &p[4], &p[5]))
+  constexpr Py_ssize_t N = offsetof(library_t, check) / sizeof(void*);
+  if (PyTuple_GET_SIZE(args) != N + 1) {
+    PyErr_Format(PyExc_TypeError, "%zd arguments expected", N + 1);
     return nullptr;
-  lib.lora_workspace = (decltype(lib.lora_workspace))p[0];
-  lib.lora_fwd = (decltype(lib.lora_fwd))p[1];
-  lib.lora_bwd = (decltype(lib.lora_bwd))p[2];
-  lib.grad_workspace = (decltype(lib.grad_workspace))p[3];
-  lib.grad_norm = (decltype(lib.grad_norm))p[4];
-  lib.grad_clip = (decltype(lib.grad_clip))p[5];
+  }
+  void* p[N];
+  for (Py_ssize_t i = 0; i < N; ++i) {
+    p[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(args, i + 1));
+    if (PyErr_Occurred()) return nullptr;
+  }
+  std::memcpy(&lib, p, sizeof(p));
+  PyObject* check = PyTuple_GET_ITEM(args, 0);
   Py_INCREF(check);
   lib.check = check;
   Py_RETURN_NONE;
@@ -347,6 +732,13 @@ PyMethodDef methods[] = {
     {"lora_fwd", (PyCFunction)(void (*)(void))lora_fwd, METH_FASTCALL, nullptr},
     {"lora_bwd", (PyCFunction)(void (*)(void))lora_bwd, METH_FASTCALL, nullptr},
     {"clip", (PyCFunction)(void (*)(void))clip, METH_FASTCALL, nullptr},
+    {"dropout", (PyCFunction)(void (*)(void))dropout, METH_FASTCALL, nullptr},
+    {"embed_fwd", (PyCFunction)(void (*)(void))embed_fwd, METH_FASTCALL, nullptr},
+    {"embed_bwd", (PyCFunction)(void (*)(void))embed_bwd, METH_FASTCALL, nullptr},
+    {"logp_fwd", (PyCFunction)(void (*)(void))logp_fwd, METH_FASTCALL, nullptr},
+    {"logp_bwd", (PyCFunction)(void (*)(void))logp_bwd, METH_FASTCALL, nullptr},
+    {"preference", (PyCFunction)(void (*)(void))preference, METH_FASTCALL, nullptr},
+    {"policy", (PyCFunction)(void (*)(void))policy, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, methods,
                           nullptr, nullptr, nullptr, nullptr};
