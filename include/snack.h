@@ -742,8 +742,8 @@ SNACK_API snack_status snack_logp_bwd(snack_dtype dtype, const float* dlogp, con
  * gradient.  A batch is S sequences among T tokens: sequence j has the tokens
  * from starts[j] up to starts[j + 1] (device, S + 1 int32, not decreasing, in
  * [0, T]; NULL: T / S tokens each).  mask (nullable, T bytes): tokens whose
- * byte is 0 do not count, are not read, and have gradient 0, as tokens of no
- * sequence have.  Per token arrays are fp32 and contiguous.
+ * byte is 0 do not count, whatever their values, and have gradient 0, as tokens
+ * of no sequence have.  Per token arrays are fp32 and contiguous.
  *
  * snack_preference: sequence 2p is preferred to 2p + 1.  With
  *     d_j = sum over j's counted tokens of (logps - ref)  (average: divided by

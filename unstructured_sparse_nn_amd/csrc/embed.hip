@@ -4,12 +4,13 @@
 //   dW[v, :] = base[v, :] + scale sum_{i : ids[i] = v} dY[i, :]
 //
 // The lookup is a copy of rows.  The gradient sorts the tokens by their number
-// first (k_embed_sort) and then sums each table row's tokens in their order
+// first (k_embed_sort, which also writes the rows that no token has: most of a
+// table) and then sums each table row's tokens in the sorted order
 // (k_embed_sum), so no float is added by an atomic and the same inputs give the
 // same bits.  A text's most frequent token has many times the mean: rows of
-// more than RUN tokens are summed in pieces of the sorted order, RUN tokens
+// more than RUN tokens are summed in pieces of the sorted order, RUN places
 // each, which k_embed_join adds.  Bound by memory: dY once, every row of dW
-// once, most of which are zeros.
+// once.
 #include "common.h"
 #include "internal.h"
 #include "pieces.h"
@@ -45,43 +46,71 @@ __global__ __launch_bounds__(256) void k_embed(ids_t ids, int64_t Tn, const T* _
 }
 
 // --------------------------------------------------------------------- sort
-constexpr int32_t RUN = 32;         // sorted tokens of a piece
+constexpr int32_t RUN = 32;         // sorted places of a piece
 constexpr int SORT_WAVES = 16;
 constexpr int32_t MAX_RANGE = 512;  // table rows of a sorting workgroup
 
+// A place of the sorted order: its token and table row, and the places [begin,
+// end) of that row.
+struct __attribute__((aligned(16))) place_t { int32_t token, row, begin, end; };
+
+struct sum_arg {
+  const void* dY;
+  int64_t lddy;
+  int32_t V, D;
+  float scale;
+  const void* base;
+  int64_t ldb;
+  void* dW;
+  int64_t lddw;
+  const place_t* order;
+  const int32_t* all;  // places that the order has
+  float* part;         // two slots of per * EL floats for each RUN places
+  uint32_t per;
+};
+
+// acc times the scale, and base, into row v.
+template <typename T>
+__device__ __forceinline__ void put_row(const sum_arg& a, int32_t v, cut_t c,
+                                        float (&acc)[EL<T>]) {
+  float b[EL<T>] = {};
+  if (a.base) floats_of(load_cut((const T*)a.base + (int64_t)v * a.ldb, c, a.D), b);
+#pragma unroll
+  for (int e = 0; e < EL<T>; ++e) acc[e] = fmaf(acc[e], a.scale, b[e]);
+  store_cut((T*)a.dW + (int64_t)v * a.lddw, c, a.D, to_frag(acc));
+}
+
 // Each workgroup owns `range` rows of the table and reads all token numbers:
 // those below its rows give the place where its own begin, so the workgroups
-// need nothing of each other.  Its waves take consecutive shares of the tokens,
-// count them by row, and walk them again to place them, in order.
-// first[v] is where row v's tokens start (first[V]: how many there are), order
-// the tokens, rows the table row of each place.
-__global__ __launch_bounds__(SORT_WAVES * 64) void k_embed_sort(ids_t ids, int32_t Tn, int32_t V,
-                                                                int32_t range,
-                                                                int32_t* __restrict__ first,
-                                                                int32_t* __restrict__ order,
-                                                                int32_t* __restrict__ rows) {
+// need nothing of each other.  Its waves take every 16th block of 64 tokens,
+// count theirs by row, and walk them again to place them: a row's tokens are in
+// the order of waves, blocks and lanes.  (With consecutive shares, the waves of
+// all workgroups read addresses that are a multiple of 4 KB apart, one channel of
+// the L2: 9.7 us for 8,192 tokens instead of 6.)  Between the two walks it writes
+// the rows that have no token.
+template <typename T>
+__global__ __launch_bounds__(SORT_WAVES * 64) void k_embed_sort(sum_arg a, ids_t ids, int32_t Tn,
+                                                                int32_t range) {
   extern __shared__ int32_t lds[];
-  int32_t *count = lds, *below_of = lds + SORT_WAVES * range, *scan = below_of + SORT_WAVES;
+  int32_t *count = lds, *begin_of = count + SORT_WAVES * range, *end_of = begin_of + range,
+          *below_of = end_of + range, *scan = below_of + SORT_WAVES;
   const int w = threadIdx.x / 64, lane = lane_id();
-  const int32_t lo = blockIdx.x * range, hi = min(lo + range, V);
+  const int32_t lo = blockIdx.x * range, hi = min(lo + range, a.V);
   for (int32_t q = threadIdx.x; q < SORT_WAVES * range; q += SORT_WAVES * 64) count[q] = 0;
   __syncthreads();
-  const int64_t steps = ((int64_t)Tn + 63) / 64;
-  const int32_t s0 = (int32_t)(steps * w / SORT_WAVES), s1 = (int32_t)(steps * (w + 1) / SORT_WAVES);
-  constexpr int U = 4;
+  constexpr int U = 4, STEP = SORT_WAVES * 64;
   int32_t* mine = count + w * range;
   int32_t below = 0;
-  auto load = [&](int32_t step, int32_t (&v)[U]) {
+  auto load = [&](int64_t from, int32_t (&v)[U]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t i = (int64_t)(step + u) * 64 + lane;
-      v[u] = ids.get(min(i, (int64_t)Tn - 1), V);
-      if (i >= Tn || step + u >= s1) v[u] = -1;
-    }
+    for (int u = 0; u < U; ++u) v[u] = ids.get(min(from + u * STEP, (int64_t)Tn - 1), a.V);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (from + u * STEP >= Tn) v[u] = -1;
   };
-  for (int32_t step = s0; step < s1; step += U) {
+  for (int64_t at = 0; at < Tn; at += U * STEP) {
     int32_t v[U];
-    load(step, v);
+    load(at + threadIdx.x, v);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       below += __popcll(__ballot(v[u] >= 0 && v[u] < lo));
@@ -94,27 +123,41 @@ __global__ __launch_bounds__(SORT_WAVES * 64) void k_embed_sort(ids_t ids, int32
 #pragma unroll
   for (int q = 0; q < SORT_WAVES; ++q) all_below += below_of[q];
   const int32_t r = threadIdx.x;
-  if (r < range)
-    for (int q = 0; q < SORT_WAVES; ++q) own += count[q * range + r];
-  int32_t at = all_below + block_excl_scan_i32<SORT_WAVES * 64>(own, scan, &total);
   if (r < range) {
-    if (lo + r < V) first[lo + r] = at;
+#pragma unroll
+    for (int q = 0; q < SORT_WAVES; ++q) own += count[q * range + r];
+  }
+  int32_t place = all_below + block_excl_scan_i32<SORT_WAVES * 64>(own, scan, &total);
+  if (r < range) {
+    begin_of[r] = place;
+    end_of[r] = place + own;
+#pragma unroll
     for (int q = 0; q < SORT_WAVES; ++q) {
       const int32_t n = count[q * range + r];
-      count[q * range + r] = at;
-      at += n;
+      count[q * range + r] = place;
+      place += n;
     }
   }
-  if (threadIdx.x == 0 && hi == V) first[V] = all_below + total;
+  if (threadIdx.x == 0 && hi == a.V) *const_cast<int32_t*>(a.all) = all_below + total;
   __syncthreads();
+  if (a.base != a.dW) {  // in place nothing is added to them
+    const uint32_t n = (uint32_t)(hi - lo) * a.per;
+    for (uint32_t g = threadIdx.x; g < n; g += SORT_WAVES * 64) {
+      const int32_t row = (int32_t)(g / a.per);
+      if (begin_of[row] != end_of[row]) continue;
+      float acc[EL<T>] = {};
+      put_row<T>(a, lo + row, cut_of<T>((int32_t)(g % a.per), a.D), acc);
+    }
+  }
   if (total == 0) return;
-  for (int32_t step = s0; step < s1; step += U) {
+  place_t* order = const_cast<place_t*>(a.order);
+  for (int64_t at = 0; at < Tn; at += U * STEP) {
     int32_t v[U];
-    load(step, v);
+    load(at + threadIdx.x, v);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool in = v[u] >= lo && v[u] < hi;
-      // lanes of one row at a time, in the order of their tokens
+      // lanes of one row at a time
       for (uint64_t todo = __ballot(in); todo;) {
         const int leader = __ffsll((unsigned long long)todo) - 1;
         const int32_t row = __shfl(v[u], leader);
@@ -122,10 +165,9 @@ __global__ __launch_bounds__(SORT_WAVES * 64) void k_embed_sort(ids_t ids, int32
         int32_t to = 0;
         if (lane == leader) to = atomicAdd(&mine[row - lo], __popcll(same));
         to = __shfl(to, leader) + __popcll(same & lanemask_lt());
-        if (in && v[u] == row) {
-          order[to] = (step + u) * 64 + lane;
-          rows[to] = row;
-        }
+        if (in && v[u] == row)
+          order[to] = place_t{(int32_t)(at + u * STEP) + (int32_t)threadIdx.x, row,
+                              begin_of[row - lo], end_of[row - lo]};
         todo &= ~same;
       }
     }
@@ -133,21 +175,7 @@ __global__ __launch_bounds__(SORT_WAVES * 64) void k_embed_sort(ids_t ids, int32
 }
 
 // ---------------------------------------------------------------------- sums
-struct sum_arg {
-  const void* dY;
-  int64_t lddy;
-  int32_t V, D;
-  float scale;
-  const void* base;
-  int64_t ldb;
-  void* dW;
-  int64_t lddw;
-  const int32_t *first, *order, *rows;
-  float* part;  // two slots of per * EL floats for each RUN places
-  uint32_t per;
-};
-
-// acc += rows [k, end) of the order, at cut c.
+// acc += the tokens of places [k, end), at cut c.
 template <typename T>
 __device__ __forceinline__ void add_tokens(const sum_arg& a, int32_t k, int32_t end, cut_t c,
                                            float (&acc)[EL<T>]) {
@@ -157,7 +185,7 @@ __device__ __forceinline__ void add_tokens(const sum_arg& a, int32_t k, int32_t 
     frag<T> f[U];
     int32_t tok[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) tok[u] = a.order[min(k + u, end - 1)];
+    for (int u = 0; u < U; ++u) tok[u] = a.order[min(k + u, end - 1)].token;
 #pragma unroll
     for (int u = 0; u < U; ++u) f[u] = load_cut(dY + (int64_t)tok[u] * a.lddy, c, a.D);
 #pragma unroll
@@ -170,48 +198,37 @@ __device__ __forceinline__ void add_tokens(const sum_arg& a, int32_t k, int32_t 
   }
 }
 
+// The first `blocks` workgroups take the places at which a table row begins, the
+// others the pieces of rows of more than RUN tokens: of each RUN places those of
+// such a row that began before (slot 0) and of one that begins there (slot 1);
+// it goes on past them, so there is one at most.
 template <typename T>
-__device__ __forceinline__ void put_row(const sum_arg& a, int32_t v, cut_t c,
-                                        float (&acc)[EL<T>]) {
-  float b[EL<T>] = {};
-  if (a.base) floats_of(load_cut((const T*)a.base + (int64_t)v * a.ldb, c, a.D), b);
-#pragma unroll
-  for (int e = 0; e < EL<T>; ++e) acc[e] = fmaf(acc[e], a.scale, b[e]);
-  store_cut((T*)a.dW + (int64_t)v * a.lddw, c, a.D, to_frag(acc));
-}
-
-// The first `blocks` workgroups take the table's rows, the others the pieces
-// of rows of more than RUN tokens: of each RUN places those of such a row that
-// began before (slot 0) and of one that begins there (slot 1); it goes on past
-// them, so there is one at most.
-template <typename T>
-__global__ __launch_bounds__(256) void k_embed_sum(sum_arg a, uint32_t blocks, int32_t Tn) {
+__global__ __launch_bounds__(256) void k_embed_sum(sum_arg a, uint32_t blocks) {
   constexpr int E = EL<T>;
   float acc[E] = {};
+  const int32_t all = *a.all;
   if (blockIdx.x < blocks) {
     const uint32_t g = blockIdx.x * 256u + threadIdx.x;
-    const uint32_t v = g / a.per;
-    if (v >= (uint32_t)a.V) return;
-    const int32_t k = a.first[v], end = a.first[v + 1];
-    if (end - k > RUN) return;
-    if (end == k && a.base == a.dW) return;  // in place: nothing is added
+    const int32_t k = (int32_t)(g / a.per);
+    if (k >= all) return;
+    const place_t p = a.order[k];
+    if (p.begin != k || p.end - k > RUN) return;
     const cut_t c = cut_of<T>((int32_t)(g % a.per), a.D);
-    add_tokens<T>(a, k, end, c, acc);
-    put_row<T>(a, (int32_t)v, c, acc);
+    add_tokens<T>(a, k, p.end, c, acc);
+    put_row<T>(a, p.row, c, acc);
     return;
   }
   const uint32_t g = (blockIdx.x - blocks) * 256u + threadIdx.x;
   const uint32_t slot = g / a.per, q = g % a.per;
-  const int32_t from = (int32_t)min((int64_t)(slot / 2) * RUN, (int64_t)Tn), all = a.first[a.V];
+  const int64_t from = (int64_t)(slot / 2) * RUN;
   if (from >= all) return;
-  const int32_t to = min(from + RUN, all);
-  const int32_t v = a.rows[slot & 1 ? to - 1 : from];
-  const int32_t begin = a.first[v], end = a.first[v + 1];
-  if (end - begin <= RUN || (begin < from) == (slot & 1)) return;
-  add_tokens<T>(a, max(begin, from), min(end, to), cut_of<T>((int32_t)q, a.D), acc);
-  float* p = a.part + ((int64_t)slot * a.per + q) * E;
+  const int32_t to = (int32_t)min(from + RUN, (int64_t)all);
+  const place_t p = a.order[slot & 1 ? to - 1 : from];
+  if (p.end - p.begin <= RUN || (p.begin < from) == (slot & 1)) return;
+  add_tokens<T>(a, max(p.begin, (int32_t)from), min(p.end, to), cut_of<T>((int32_t)q, a.D), acc);
+  float* part = a.part + ((int64_t)slot * a.per + q) * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) p[e] = acc[e];
+  for (int e = 0; e < E; ++e) part[e] = acc[e];
 }
 
 // Rows of more than RUN tokens: one that begins among the RUN places of this
@@ -220,12 +237,11 @@ template <typename T>
 __global__ __launch_bounds__(256) void k_embed_join(sum_arg a) {
   constexpr int E = EL<T>;
   __shared__ float lds[4][64][E + 1];
-  const int32_t tile = blockIdx.x, from = tile * RUN, all = a.first[a.V];
+  const int32_t tile = blockIdx.x, from = tile * RUN, all = *a.all;
   if (from >= all) return;
-  const int32_t v = a.rows[min(from + RUN, all) - 1];
-  const int32_t begin = a.first[v], end = a.first[v + 1];
-  if (end - begin <= RUN || begin < from) return;
-  const int32_t n = (end - 1) / RUN - tile + 1;  // slots: this tile's second, the others' first
+  const place_t at = a.order[min(from + RUN, all) - 1];
+  if (at.end - at.begin <= RUN || at.begin < from) return;
+  const int32_t n = (at.end - 1) / RUN - tile + 1;  // slots: this tile's second, the others' first
   const int w = threadIdx.x / 64, lane = lane_id();
   const uint32_t q = blockIdx.y * 64 + lane;
   float acc[E] = {};
@@ -246,31 +262,30 @@ __global__ __launch_bounds__(256) void k_embed_join(sum_arg a) {
 #pragma unroll
   for (int e = 0; e < E; ++e)
     acc[e] = ((lds[0][lane][e] + lds[1][lane][e]) + lds[2][lane][e]) + lds[3][lane][e];
-  put_row<T>(a, v, cut_of<T>((int32_t)q, a.D), acc);
+  put_row<T>(a, at.row, cut_of<T>((int32_t)q, a.D), acc);
 }
 
 struct plan_t {
   int64_t per, tiles;  // tiles: 0 if no row can have more than RUN tokens
   int32_t range;
-  size_t first, order, rows, part, total;
+  size_t all, order, part, total;
 };
 
 plan_t plan_of(snack_dtype dt, int64_t Tn, int32_t V, int32_t D) {
   plan_t p{};
   p.per = cdiv(D, dt == SNACK_BF16 ? 8 : 4);
   p.tiles = Tn > RUN ? cdiv(Tn, RUN) : 0;
-  // about 256 sorting workgroups, for every one reads all token numbers
-  p.range = 64;
-  while (p.range < MAX_RANGE && (int64_t)p.range * 256 < V) p.range *= 2;
+  // two sorting workgroups on a CU, with 32 rows at least: every one reads all
+  // token numbers
+  p.range = (int32_t)std::min<int64_t>(MAX_RANGE, std::max<int64_t>(32, cdiv(V, 512)));
   size_t o = 0;
   auto take = [&](size_t b) {
     const size_t at = o;
     o = align_up(o + b, 256);
     return at;
   };
-  p.first = take(4 * ((size_t)V + 1));
-  p.order = take(4 * (size_t)Tn);
-  p.rows = take(4 * (size_t)Tn);
+  p.all = take(4);
+  p.order = take(sizeof(place_t) * (size_t)Tn);
   p.part = take((size_t)p.tiles * 2 * p.per * (dt == SNACK_BF16 ? 32 : 16));
   p.total = std::max<size_t>(o, 256);
   return p;
@@ -283,20 +298,20 @@ snack_status check_embed(snack_dtype dt, int32_t id_bytes, int64_t Tn, int32_t V
   // what a launch of each kernel holds
   const int64_t per = cdiv(D, dt == SNACK_BF16 ? 8 : 4);
   if (Tn > MAX_TOKENS || V > MAX_ROWS || D > MAX_FEATURES) return SNACK_E_OVERFLOW;
-  if (per > 0 && (Tn > MAX_PIECES / per || V + Tn / (RUN / 2) + 2 > MAX_PIECES / per))
+  if (per > 0 && (Tn + Tn / (RUN / 2) + 2 > MAX_PIECES / per || V > MAX_PIECES / per))
     return SNACK_E_OVERFLOW;
   return SNACK_OK;
 }
 
 template <typename T>
 void run_bwd(ids_t ids, int32_t Tn, const plan_t& p, const sum_arg& a, hipStream_t s) {
-  const int64_t groups = std::max<int64_t>(1, cdiv(a.V, p.range));
-  hipLaunchKernelGGL(k_embed_sort, dim3((unsigned)groups), dim3(SORT_WAVES * 64),
-                     4 * (SORT_WAVES * (size_t)p.range + 2 * SORT_WAVES), s, ids, Tn, a.V, p.range,
-                     (int32_t*)a.first, (int32_t*)a.order, (int32_t*)a.rows);
-  const int64_t blocks = cdiv(a.V * p.per, 256), more = cdiv(2 * p.tiles * p.per, 256);
+  hipLaunchKernelGGL(k_embed_sort<T>, dim3((unsigned)cdiv(a.V, p.range)), dim3(SORT_WAVES * 64),
+                     4 * ((SORT_WAVES + 2) * (size_t)p.range + 2 * SORT_WAVES), s, a, ids, Tn,
+                     p.range);
+  if (Tn == 0) return;
+  const int64_t blocks = cdiv(Tn * p.per, 256), more = cdiv(2 * p.tiles * p.per, 256);
   hipLaunchKernelGGL(k_embed_sum<T>, dim3((unsigned)(blocks + more)), dim3(256), 0, s, a,
-                     (uint32_t)blocks, Tn);
+                     (uint32_t)blocks);
   if (p.tiles > 0)
     hipLaunchKernelGGL(k_embed_join<T>, dim3((unsigned)p.tiles, (unsigned)cdiv(p.per, 64)),
                        dim3(256), 0, s, a);
@@ -361,9 +376,8 @@ snack_status snack_embed_bwd(snack_dtype dtype, const void* ids, int32_t id_byte
   if (any_overlap(out, in)) return SNACK_E_SHAPE;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   char* b = (char*)ws;
-  const sum_arg a{dY, lddy, V, D, scale, base, ldb, dW, lddw, (const int32_t*)(b + p.first),
-                  (const int32_t*)(b + p.order), (const int32_t*)(b + p.rows),
-                  (float*)(b + p.part), (uint32_t)p.per};
+  const sum_arg a{dY, lddy, V, D, scale, base, ldb, dW, lddw, (const place_t*)(b + p.order),
+                  (const int32_t*)(b + p.all), (float*)(b + p.part), (uint32_t)p.per};
   const ids_t of{ids, id_bytes == 8};
   if (dtype == SNACK_BF16) run_bwd<bf16>(of, (int32_t)T, p, a, s);
   else run_bwd<float>(of, (int32_t)T, p, a, s);

@@ -12,15 +12,23 @@
 //   loss = sum of f over all tokens / their number, or the mean over the
 //          sequences of their tokens' mean
 //
-// Both need a sum over each sequence (or over all of them) before any token's
-// gradient: k_seq_sums leaves sums of slices of the sequences, k_seq_grads adds
-// them up again in each workgroup that needs them and writes the gradients and
-// the loss.  Batches of a few thousand tokens take one workgroup and one launch
-// (k_seq_small), for two launches cost more than what they would share.  Sums
-// are 64-bit in a fixed order; whether a ratio is past its border is decided
-// on logarithms in 64 bits.  A token's terms are fp32.  Bound by memory where the
-// batch is large: two to five floats a token, read twice (the second time from
-// the caches up to 256 MB), and one written.
+// The sequences are cut into items of at most 2^log_p tokens, a wave's work each,
+// so that one long answer among short ones is many waves'.  A preference's
+// gradients need the sums of its sequences first:
+//   k_pref_sums    the sums of every item
+//   k_pref_finish  the items of a sequence follow each other: their sums, each
+//                  pair's loss and what the gradients of its tokens are
+//   k_pref_grads   the gradients, and the loss
+// A policy's need only how many tokens count, which is known where there is no
+// mask, and is cheap to find where it is short:
+//   k_policy_counts  the counts of every item (a mask of a large batch)
+//   k_policy         gradients, and the sums of every workgroup's items
+//   k_policy_finish  the loss and the statistics
+// Small batches take one workgroup and one launch (k_seq_small), whose waves keep
+// their tokens in registers.  Sums are 64-bit in a fixed order; whether a ratio is
+// past its border is decided on logarithms in 64 bits.  A token's terms are fp32.
+// Bound by memory where the batch is large: two to five floats a token read and
+// one written; by launches and trips to memory where it is not.
 #include <cmath>
 
 #include "common.h"
@@ -32,23 +40,61 @@ namespace {
 
 // ---------------------------------------------------------------- sequences
 struct batch_t {
-  const int32_t* starts;  // [S + 1], or NULL: T / S tokens each
+  const int32_t* starts;  // [S + 1], or NULL: `each` tokens in every sequence
   const uint8_t* mask;    // [T], or NULL: every token counts
   int32_t S, T, each;
+  int32_t log_p, items;
 };
-struct span2 { int32_t a, b; };
 
 // Places that do not fit are cut to [0, T], so a call with wrong ones stays
 // inside its arrays.
-__device__ __forceinline__ span2 seq_of(const batch_t& q, int32_t i) {
-  if (!q.starts) return {i * q.each, (i + 1) * q.each};
-  const int32_t a = min(max(q.starts[i], 0), q.T);
-  return {a, min(max(q.starts[i + 1], a), q.T)};
+__device__ __forceinline__ int32_t start_of(const batch_t& q, int32_t i) {
+  return q.starts ? min(max(q.starts[i], 0), q.T) : i * q.each;
 }
-// Slice c of C.
-__device__ __forceinline__ span2 slice_of(span2 s, int32_t c, int32_t C) {
-  const int64_t n = s.b - s.a;
-  return {s.a + (int32_t)(n * c / C), s.a + (int32_t)(n * (c + 1) / C)};
+
+// Sequence i's items are those from first_item(i) up to first_item(i + 1): with
+// starts a_i, from a_i / P + i up to a_(i+1) / P + i + 1, at least as many as it
+// needs (the last may be empty), without a sum over the sequences before it.
+__device__ __forceinline__ int32_t first_item(const batch_t& q, int32_t i, int32_t start) {
+  return (start >> q.log_p) + i;
+}
+
+struct item_t { int32_t seq, a, b; };  // its sequence, and its tokens
+
+// Item x of the sequence that begins at a; items before the first sequence's or
+// past the last one's have no tokens.
+__device__ __forceinline__ item_t item_at(const batch_t& q, int32_t x, int32_t seq, int32_t a,
+                                          int32_t next) {
+  const int32_t b = max(next, a), x0 = first_item(q, seq, a);
+  int64_t from = b;
+  if (x >= x0) from = a + ((int64_t)(x - x0) << q.log_p);
+  return {seq, (int32_t)min(from, (int64_t)b),
+          (int32_t)min(from + (1 << q.log_p), (int64_t)b)};
+}
+
+// The sequence of item x is the last one whose first item is not past x: a
+// search that cuts the sequences into 63 with every trip to memory; the last trip
+// brings the sequence's own start and the next one's too.
+__device__ __forceinline__ item_t item_of(const batch_t& q, int32_t x) {
+  int32_t lo = 0, n = q.S;
+  for (;;) {
+    const int32_t step = (n + 62) / 63;
+    const int64_t at = (int64_t)lane_id() * step;
+    const int32_t i = lo + (int32_t)min(at, (int64_t)n), start = start_of(q, i);
+    // none where x comes before the first sequence's items (and a count is unsigned)
+    const int32_t found = (int32_t)__popcll(__ballot(at < n && first_item(q, i, start) <= x));
+    const int32_t last = max(found - 1, 0);
+    lo += last * step;
+    if (step == 1) return item_at(q, x, lo, __shfl(start, last), __shfl(start, last + 1));
+    n = min(step, n - last * step);
+  }
+}
+
+// The items of sequence i.
+struct range_t { int32_t a, b; };
+__device__ __forceinline__ range_t items_of(const batch_t& q, int32_t i) {
+  const int32_t a = start_of(q, i), b = max(start_of(q, i + 1), a);
+  return {first_item(q, i, a), min(first_item(q, i + 1, b), q.items)};
 }
 
 __device__ __forceinline__ double wave_sum(double x) {
@@ -56,33 +102,31 @@ __device__ __forceinline__ double wave_sum(double x) {
   for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
   return x;
 }
+__device__ __forceinline__ double count_lanes(bool x) { return (double)__popcll(__ballot(x)); }
 
-// The sums of a sequence or a part of it.  Preference: f is d's sum.
-struct sums_t { double f, kl, cut; int64_t n; };
+// The sums of an item, a sequence or the batch.  Preference: f is d's sum.  cut
+// and n are whole.
+struct sums_t { double f, kl, cut, n; };
 __device__ __forceinline__ sums_t operator+(const sums_t& a, const sums_t& b) {
   return {a.f + b.f, a.kl + b.kl, a.cut + b.cut, a.n + b.n};
 }
-__device__ __forceinline__ sums_t wave_sum(const sums_t& a) {
-  sums_t o = a;
-#pragma unroll
-  for (int d = 32; d; d >>= 1)
-    o = o + sums_t{__shfl_xor(o.f, d), __shfl_xor(o.kl, d), __shfl_xor(o.cut, d),
-                   (int64_t)__shfl_xor((long long)o.n, d)};
-  return o;
+__device__ __forceinline__ sums_t wave_sum(const sums_t& s) {
+  return {wave_sum(s.f), wave_sum(s.kl), wave_sum(s.cut), wave_sum(s.n)};
 }
 
 // ---------------------------------------------------------------- preference
 struct pref_t {
+  static constexpr bool POLICY = false;
   const float *logps, *ref;
   double beta, eps;
   int32_t form, average;
 
-  __device__ __forceinline__ void add(sums_t& s, int32_t i, int32_t) const {
-    s.f += ref ? (double)logps[i] - (double)ref[i] : (double)logps[i];
-    s.n += 1;
+  struct in_t { float lp, ref; };
+  __device__ __forceinline__ in_t load(int32_t i, int32_t) const {
+    return {logps[i], ref ? ref[i] : 0.f};
   }
   __device__ __forceinline__ double per(const sums_t& s) const {
-    return average ? 1.0 / (double)max(s.n, (int64_t)1) : 1.0;
+    return average ? 1.0 / fmax(s.n, 1.0) : 1.0;
   }
   // A pair's loss, and its derivative by h.
   __device__ __forceinline__ double pair(double h, double* dh) const {
@@ -107,12 +151,18 @@ struct pref_t {
 
 // -------------------------------------------------------------------- policy
 struct policy_t {
+  static constexpr bool POLICY = true;
   const float *logps, *old, *ref, *adv;
   double log_low, log_high;  // of 1 - low and 1 + high
   float low, high, kl;
-  int32_t by_token, by_sequence_mean;
+  int32_t by_token, sequence_mean;
 
   struct token_t { float f, df, kl; bool cut; };
+  struct in_t { float lp, old, ref, adv; };
+  __device__ __forceinline__ in_t load(int32_t i, int32_t seq) const {
+    const float lp = logps[i];
+    return {lp, old ? old[i] : lp, ref ? ref[i] : 0.f, adv[by_token ? i : seq]};
+  }
 
   // exp(k) - 1 - k without its cancellation near 0, and exp(k) - 1.
   __device__ __forceinline__ static float above(float k, float* em1) {
@@ -138,9 +188,9 @@ struct policy_t {
     return s;
   }
 
-  __device__ __forceinline__ token_t token(int32_t i, int32_t seq) const {
-    const float lp = logps[i], a = adv[by_token ? i : seq];
-    const double move = old ? (double)lp - (double)old[i] : (double)lp - (double)lp;
+  __device__ __forceinline__ token_t token(const in_t& v) const {
+    const float a = v.adv;
+    const double move = (double)v.lp - (double)v.old;
     const float r = expf((float)move);
     token_t o;
     o.cut = (a > 0.f && move > log_high) || (a < 0.f && move < log_low);
@@ -149,31 +199,17 @@ struct policy_t {
     o.kl = 0.f;
     if (ref) {
       float em1;
-      o.kl = above((float)((double)ref[i] - (double)lp), &em1);
+      o.kl = above((float)((double)v.ref - (double)v.lp), &em1);
       o.f = fmaf(kl, o.kl, o.f);
       o.df = fmaf(-kl, em1, o.df);
     }
     return o;
   }
-  __device__ __forceinline__ void add(sums_t& s, int32_t i, int32_t seq) const {
-    const token_t o = token(i, seq);
-    s.f += o.f;
-    s.kl += o.kl;
-    s.cut += o.cut;
-    s.n += 1;
+  // What a sequence's gradients are multiplied by, beside the loss's own.
+  __device__ __forceinline__ double weight(const batch_t& q, double seq_n, double all_n) const {
+    return 1.0 / (sequence_mean ? (double)q.S * fmax(seq_n, 1.0) : fmax(all_n, 1.0));
   }
 };
-
-// Threads first, first + step, ... of [s.a, s.b).
-template <typename L>
-__device__ __forceinline__ sums_t sum_slice(const batch_t& q, const L& loss, span2 s, int32_t seq,
-                                            int32_t first, int32_t step) {
-  sums_t o{0, 0, 0, 0};
-#pragma unroll 4
-  for (int64_t i = (int64_t)s.a + first; i < s.b; i += step)
-    if (!q.mask || q.mask[i]) loss.add(o, (int32_t)i, seq);
-  return o;
-}
 
 struct out_t {
   const float* dloss;  // device, or NULL: 1
@@ -181,222 +217,437 @@ struct out_t {
   float* more;         // rewards [S] or stats [2], or NULL
   float* grad;         // [T], or NULL
 };
-
-// What a token's gradient takes from sums: preference, the coefficient of a
-// whole sequence; policy, the weight of its tokens.
-struct totals_t { int64_t n; };
-
-__device__ __forceinline__ double weight_of(const policy_t& l, const batch_t& q, const sums_t& seq,
-                                            const totals_t& all) {
-  return l.by_sequence_mean ? 1.0 / ((double)q.S * (double)max(seq.n, (int64_t)1))
-                            : 1.0 / (double)max(all.n, (int64_t)1);
+__device__ __forceinline__ double upstream(const out_t& out) {
+  return out.dloss ? (double)*out.dloss : 1.0;
 }
 
-template <typename L>
-__device__ __forceinline__ void write_slice(const batch_t& q, const L& loss, span2 s, int32_t seq,
-                                            double c, float* grad, int32_t first, int32_t step) {
-#pragma unroll 4
-  for (int64_t i = (int64_t)s.a + first; i < s.b; i += step) {
-    float g = 0.f;
-    if (!q.mask || q.mask[i]) {
-      if constexpr (std::is_same<L, pref_t>::value) g = (float)c;
-      else g = (float)((double)loss.token((int32_t)i, seq).df * c);
+// A lane's U tokens of an item, 64 apart, all loaded at once (those past its end
+// are its first one, if it has any).
+template <typename L, int U> struct tokens_t {
+  typename L::in_t v[U];
+  bool in[U], counts[U];
+
+  __device__ __forceinline__ void load(const batch_t& q, const L& loss, const item_t& it,
+                                       int32_t from) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int32_t at = from + u * 64 + lane_id();
+      in[u] = at < it.b;
+      const int32_t i = in[u] ? at : it.a;
+      counts[u] = in[u] && (q.mask ? q.mask[i] != 0 : true);
+      v[u] = loss.load(i, it.seq);
     }
-    grad[i] = g;
   }
+  // Adds them to this lane's f and kl and to the wave's counts; g: what their
+  // gradients are but for the weight.
+  __device__ __forceinline__ void add(const L& loss, sums_t& s, float (&g)[U]) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      s.n += count_lanes(counts[u]);
+      if constexpr (L::POLICY) {
+        const auto o = loss.token(v[u]);
+        s.cut += count_lanes(counts[u] && o.cut);
+        s.f += counts[u] ? (double)o.f : 0.0;
+        s.kl += counts[u] ? (double)o.kl : 0.0;
+        g[u] = counts[u] ? o.df : 0.f;
+      } else {
+        s.f += counts[u] ? (double)v[u].lp - (double)v[u].ref : 0.0;
+      }
+    }
+  }
+};
+template <typename L>
+__device__ __forceinline__ void wave_totals(sums_t& s) {
+  s.f = wave_sum(s.f);
+  if (L::POLICY) s.kl = wave_sum(s.kl);
 }
 
 // Tokens of no sequence: their gradient is 0.
 __device__ __forceinline__ void write_outside(const batch_t& q, float* grad, int64_t first,
                                               int64_t step) {
-  if (!q.starts || q.S == 0) {
-    const int64_t from = (int64_t)q.S * q.each;
-    for (int64_t i = from + first; i < q.T; i += step) grad[i] = 0.f;
-    return;
-  }
-  const int32_t a = seq_of(q, 0).a, b = seq_of(q, q.S - 1).b;
+  const int32_t a = q.S > 0 ? start_of(q, 0) : q.T;
+  const int32_t b = q.S > 0 ? max(start_of(q, q.S), start_of(q, q.S - 1)) : q.T;
   for (int64_t i = first; i < a; i += step) grad[i] = 0.f;
-  for (int64_t i = (int64_t)b + first; i < q.T; i += step) grad[i] = 0.f;
+  for (int64_t i = b + first; i < q.T; i += step) grad[i] = 0.f;
 }
 
-// -------------------------------------------------------- one workgroup, one launch
+// A pair's loss; rewards and the two coefficients.
+__device__ __forceinline__ double finish_pair(const batch_t& q, const pref_t& loss,
+                                              const sums_t& x, const sums_t& y, int32_t p,
+                                              const out_t& out, double* coef) {
+  const double px = loss.per(x), py = loss.per(y), dx = x.f * px, dy = y.f * py;
+  double dh;
+  const double f = loss.pair(dx - dy, &dh);
+  if (out.more) {
+    out.more[2 * p] = (float)(loss.beta * dx);
+    out.more[2 * p + 1] = (float)(loss.beta * dy);
+  }
+  dh *= upstream(out) / (double)(q.S / 2);
+  coef[2 * p] = dh * px;
+  coef[2 * p + 1] = -dh * py;
+  return f;
+}
+__device__ __forceinline__ void finish_stats(const sums_t& all, const out_t& out) {
+  const double n = fmax(all.n, 1.0);
+  if (out.more) out.more[0] = (float)(all.kl / n), out.more[1] = (float)(all.cut / n);
+}
+
+// ------------------------------------------------------- one workgroup, one launch
 constexpr int SMALL_WAVES = 16;
-constexpr int32_t SMALL_SEQS = 256, SMALL_TOKENS = 8192;
+constexpr int32_t SMALL_LOG_P = 7, SMALL_SEQS = 127;
+constexpr int SMALL_EACH = 4;  // items of a wave
+
+// The starts of all sequences, two a lane.
+struct starts_t {
+  int32_t lo, hi;
+  __device__ __forceinline__ int32_t at(int32_t i) const {
+    const int32_t a = __shfl(lo, i & 63), b = __shfl(hi, i & 63);
+    return i < 64 ? a : b;
+  }
+};
 
 template <typename L>
 __global__ __launch_bounds__(SMALL_WAVES * 64) void k_seq_small(batch_t q, L loss, out_t out) {
-  __shared__ sums_t sums[SMALL_SEQS];
+  constexpr int K = SMALL_EACH, U = 1 << (SMALL_LOG_P - 6);
+  __shared__ sums_t sums[K * SMALL_WAVES];
+  __shared__ double coef[SMALL_SEQS + 1];
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64), lane = lane_id();
-  for (int32_t i = w; i < q.S; i += SMALL_WAVES) {
-    const sums_t s = wave_sum(sum_slice(q, loss, seq_of(q, i), i, lane, 64));
-    if (lane == 0) sums[i] = s;
+  starts_t st{0, 0};
+  if (q.S > 0) st = {start_of(q, min(lane, q.S)), start_of(q, min(64 + lane, q.S))};
+  const int32_t first_lo = first_item(q, lane, st.lo), first_hi = first_item(q, 64 + lane, st.hi);
+  item_t it[K];
+  tokens_t<L, U> t[K];
+  float g[K][U];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int32_t x = k * SMALL_WAVES + w;
+    it[k] = {0, 0, 0};
+    if (x >= q.items) continue;
+    const int32_t found = (int32_t)__popcll(__ballot(lane < q.S && first_lo <= x)) +
+                          (int32_t)__popcll(__ballot(64 + lane < q.S && first_hi <= x));
+    const int32_t seq = max(found - 1, 0);
+    it[k] = item_at(q, x, seq, st.at(seq), st.at(seq + 1));
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (it[k].a < it[k].b) t[k].load(q, loss, it[k], it[k].a);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int32_t x = k * SMALL_WAVES + w;
+    if (x >= q.items) continue;
+    sums_t s{0, 0, 0, 0};
+    if (it[k].a < it[k].b) {
+      t[k].add(loss, s, g[k]);
+      wave_totals<L>(s);
+    }
+    if (lane == 0) sums[x] = s;
   }
   __syncthreads();
-  const double up = out.dloss ? (double)*out.dloss : 1.0;
-  if constexpr (std::is_same<L, pref_t>::value) {
-    const double share = 1.0 / (double)max(q.S / 2, 1);
-    if (w == 0) {
-      double f = 0;
-      for (int32_t p = lane; p < q.S / 2; p += 64) {
-        const sums_t &a = sums[2 * p], &b = sums[2 * p + 1];
-        const double da = a.f * loss.per(a), db = b.f * loss.per(b);
-        double dh;
-        f += loss.pair(da - db, &dh);
-        if (out.more) {
-          out.more[2 * p] = (float)(loss.beta * da);
-          out.more[2 * p + 1] = (float)(loss.beta * db);
+  if (w == 0) {
+    double f = 0;
+    auto total = [&](int32_t i) {  // of sequence i < S
+      const int32_t a = st.at(i), b = max(st.at(i + 1), a);
+      const int32_t x1 = min(first_item(q, i + 1, b), q.items);
+      sums_t s{0, 0, 0, 0};
+      for (int32_t x = first_item(q, i, a); x < x1; ++x) s = s + sums[x];
+      return s;
+    };
+    if constexpr (!L::POLICY) {
+      const int32_t pairs = q.S / 2, p = min(lane, max(pairs - 1, 0));
+      if (pairs > 0) {
+        const sums_t x = total(2 * p), y = total(2 * p + 1);
+        if (lane < pairs) f = finish_pair(q, loss, x, y, p, out, coef);
+      }
+      f = wave_sum(f) / (double)max(pairs, 1);
+    } else {
+      sums_t all{0, 0, 0, 0};
+      for (int32_t x = lane; x < q.items; x += 64) all = all + sums[x];
+      all = wave_sum(all);
+      const double up = upstream(out);
+      for (int32_t i0 = 0; i0 < q.S; i0 += 64) {
+        const int32_t i = min(i0 + lane, q.S - 1);
+        const sums_t s = total(i);
+        if (i0 + lane < q.S) {
+          const double weight = loss.weight(q, s.n, all.n);
+          f += s.f * weight;
+          coef[i] = weight * up;
         }
       }
       f = wave_sum(f);
-      if (lane == 0 && out.loss) *out.loss = (float)(f * share);
+      if (lane == 0) finish_stats(all, out);
     }
-    if (!out.grad) return;
-    for (int32_t i = w; i < q.S; i += SMALL_WAVES) {
-      const sums_t &a = sums[i & ~1], &b = sums[i | 1];
-      double dh;
-      loss.pair(a.f * loss.per(a) - b.f * loss.per(b), &dh);
-      const double c = (i & 1 ? -dh : dh) * loss.per(sums[i]) * share * up;
-      write_slice(q, loss, seq_of(q, i), i, c, out.grad, lane, 64);
-    }
-  } else {
-    sums_t s{0, 0, 0, 0};
-    totals_t all{0};
-    for (int32_t i = lane; i < q.S; i += 64) s = s + sums[i];
-    s = wave_sum(s);
-    all.n = s.n;
-    if (w == 0) {
-      double f = 0;
-      for (int32_t i = lane; i < q.S; i += 64)
-        f += sums[i].f * weight_of(loss, q, sums[i], all);
-      f = wave_sum(f);
-      const double n = (double)max(s.n, (int64_t)1);
-      if (lane == 0) {
-        if (out.loss) *out.loss = (float)f;
-        if (out.more) out.more[0] = (float)(s.kl / n), out.more[1] = (float)(s.cut / n);
+    if (lane == 0 && out.loss) *out.loss = (float)f;
+  }
+  if (!out.grad) return;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (it[k].a >= it[k].b) continue;
+    const double c = coef[it[k].seq];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (t[k].in[u]) {
+        const double v = L::POLICY ? (double)g[k][u] * c : c;
+        out.grad[it[k].a + u * 64 + lane] = t[k].counts[u] ? (float)v : 0.f;
       }
-    }
-    if (!out.grad) return;
-    for (int32_t i = w; i < q.S; i += SMALL_WAVES)
-      write_slice(q, loss, seq_of(q, i), i, weight_of(loss, q, sums[i], all) * up, out.grad, lane,
-                  64);
   }
   write_outside(q, out.grad, threadIdx.x, SMALL_WAVES * 64);
 }
 
-// ------------------------------------------------------------------ two launches
-// Item x is slice x % C of sequence x / C; ws has its sums.
-template <typename L>
-__global__ __launch_bounds__(256) void k_seq_sums(batch_t q, L loss, int32_t C,
-                                                  sums_t* __restrict__ ws) {
-  __shared__ sums_t lds[4];
-  for (int64_t x = blockIdx.x; x < (int64_t)q.S * C; x += gridDim.x) {
-    const int32_t i = (int32_t)(x / C);
-    const sums_t s = wave_sum(sum_slice(q, loss, slice_of(seq_of(q, i), (int32_t)(x % C), C), i,
-                                        threadIdx.x, 256));
-    if (lane_id() == 0) lds[threadIdx.x / 64] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) ws[x] = ((lds[0] + lds[1]) + lds[2]) + lds[3];
-    __syncthreads();
-  }
+// ------------------------------------------------------------- several launches
+constexpr int32_t LOG_P = 9;
+__device__ __forceinline__ int32_t wave_of_block() {
+  return __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
 }
 
-__device__ __forceinline__ sums_t seq_sums(const sums_t* __restrict__ ws, int32_t i, int32_t C) {
-  sums_t s{0, 0, 0, 0};
-  for (int32_t c = 0; c < C; ++c) s = s + ws[(int64_t)i * C + c];
-  return s;
-}
-// One value a thread, added in a fixed order; all threads get it.
+template <int W>
 __device__ __forceinline__ sums_t block_sum(sums_t s, sums_t* lds) {
   s = wave_sum(s);
   if (lane_id() == 0) lds[threadIdx.x / 64] = s;
   __syncthreads();
-  s = ((lds[0] + lds[1]) + lds[2]) + lds[3];
-  __syncthreads();
+  s = lds[0];
+#pragma unroll
+  for (int w = 1; w < W; ++w) s = s + lds[w];
   return s;
 }
 
-// The last workgroup writes the loss and the sums' means, the others gradients.
-template <typename L>
-__global__ __launch_bounds__(256) void k_seq_grads(batch_t q, L loss, int32_t C,
-                                                   const sums_t* __restrict__ ws, out_t out) {
+__global__ __launch_bounds__(256) void k_pref_sums(batch_t q, pref_t loss,
+                                                   sums_t* __restrict__ sums,
+                                                   item_t* __restrict__ items) {
+  constexpr int U = 1 << (LOG_P - 6);
+  const int32_t x = blockIdx.x * 4 + wave_of_block();
+  if (x >= q.items) return;
+  const item_t it = item_of(q, x);
+  sums_t s{0, 0, 0, 0};
+  if (it.a < it.b) {
+    tokens_t<pref_t, U> t;
+    float g[U];
+    t.load(q, loss, it, it.a);
+    t.add(loss, s, g);
+    wave_totals<pref_t>(s);
+  }
+  if (lane_id() == 0) sums[x] = s, items[x] = it;
+}
+
+__device__ __forceinline__ sums_t range_sums(const sums_t* __restrict__ sums, range_t r) {
+  sums_t s{0, 0, 0, 0};
+  for (int32_t x = r.a + lane_id(); x < r.b; x += 64) s = s + sums[x];
+  return wave_sum(s);
+}
+
+// A wave for each pair.  coef: of each sequence's gradients; terms: of the loss.
+__global__ __launch_bounds__(256) void k_pref_finish(batch_t q, pref_t loss,
+                                                     const sums_t* __restrict__ sums, out_t out,
+                                                     double* __restrict__ coef,
+                                                     double* __restrict__ terms) {
+  const int32_t p = blockIdx.x * 4 + wave_of_block();
+  if (p >= q.S / 2) return;
+  const sums_t x = range_sums(sums, items_of(q, 2 * p)),
+               y = range_sums(sums, items_of(q, 2 * p + 1));
+  if (lane_id() == 0) terms[p] = finish_pair(q, loss, x, y, p, out, coef) / (double)(q.S / 2);
+}
+
+// The first workgroup adds the loss's terms, if it is wanted; the others write
+// gradients.
+__global__ __launch_bounds__(256) void k_pref_grads(batch_t q, const item_t* __restrict__ items,
+                                                    const double* __restrict__ coef,
+                                                    const double* __restrict__ terms,
+                                                    float* __restrict__ loss,
+                                                    float* __restrict__ grad) {
+  constexpr int U = 1 << (LOG_P - 6);
   __shared__ sums_t lds[4];
-  const double up = out.dloss ? (double)*out.dloss : 1.0;
-  const bool last = blockIdx.x + 1 == gridDim.x;
-  const int32_t t = threadIdx.x, grads = (int32_t)gridDim.x - 1;
-  const int64_t items = (int64_t)q.S * C;
-  if constexpr (std::is_same<L, pref_t>::value) {
-    const double share = 1.0 / (double)max(q.S / 2, 1);
-    if (last) {
-      sums_t f{0, 0, 0, 0};
-      for (int32_t p = t; p < q.S / 2; p += 256) {
-        const sums_t a = seq_sums(ws, 2 * p, C), b = seq_sums(ws, 2 * p + 1, C);
-        const double da = a.f * loss.per(a), db = b.f * loss.per(b);
-        double dh;
-        f.f += loss.pair(da - db, &dh);
-        if (out.more) {
-          out.more[2 * p] = (float)(loss.beta * da);
-          out.more[2 * p + 1] = (float)(loss.beta * db);
-        }
+  const int32_t with_loss = loss ? 1 : 0;
+  if ((int32_t)blockIdx.x < with_loss) {
+    sums_t s{0, 0, 0, 0};
+#pragma unroll 4
+    for (int32_t i = threadIdx.x; i < q.S / 2; i += 256) s.f += terms[i];
+    s = block_sum<4>(s, lds);
+    if (threadIdx.x == 0) *loss = (float)s.f;
+    return;
+  }
+  const int32_t b = blockIdx.x - with_loss, lane = lane_id();
+  const int32_t x = b * 4 + wave_of_block();
+  if (x < q.items) {
+    const item_t it = items[x];
+    if (it.a < it.b) {
+      const float c = (float)coef[it.seq];
+      bool counts[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int32_t at = it.a + u * 64 + lane;
+        counts[u] = q.mask ? q.mask[at < it.b ? at : it.a] != 0 : true;
       }
-      f = block_sum(f, lds);
-      if (t == 0 && out.loss) *out.loss = (float)(f.f * share);
-      return;
-    }
-    for (int64_t x = blockIdx.x; x < items; x += grads) {
-      const int32_t i = (int32_t)(x / C);
-      const sums_t a = seq_sums(ws, i & ~1, C), b = seq_sums(ws, i | 1, C);
-      double dh;
-      loss.pair(a.f * loss.per(a) - b.f * loss.per(b), &dh);
-      const double c = (i & 1 ? -dh * loss.per(b) : dh * loss.per(a)) * share * up;
-      write_slice(q, loss, slice_of(seq_of(q, i), (int32_t)(x % C), C), i, c, out.grad, t, 256);
-    }
-  } else {
-    totals_t all{0};
-    if (last || !loss.by_sequence_mean) {
-      sums_t s{0, 0, 0, 0};
-      if (last) for (int64_t x = t; x < items; x += 256) s = s + ws[x];
-      else for (int64_t x = t; x < items; x += 256) s.n += ws[x].n;
-      s = block_sum(s, lds);
-      all.n = s.n;
-      if (last) {
-        sums_t f{0, 0, 0, 0};
-        for (int32_t i = t; i < q.S; i += 256) {
-          const sums_t o = seq_sums(ws, i, C);
-          f.f += o.f * weight_of(loss, q, o, all);
-        }
-        f = block_sum(f, lds);
-        const double n = (double)max(s.n, (int64_t)1);
-        if (t == 0) {
-          if (out.loss) *out.loss = (float)f.f;
-          if (out.more) out.more[0] = (float)(s.kl / n), out.more[1] = (float)(s.cut / n);
-        }
-        return;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int32_t at = it.a + u * 64 + lane;
+        if (at < it.b) grad[at] = counts[u] ? c : 0.f;
       }
-    }
-    for (int64_t x = blockIdx.x; x < items; x += grads) {
-      const int32_t i = (int32_t)(x / C);
-      sums_t own{0, 0, 0, 0};
-      if (loss.by_sequence_mean) own = seq_sums(ws, i, C);
-      write_slice(q, loss, slice_of(seq_of(q, i), (int32_t)(x % C), C), i,
-                  weight_of(loss, q, own, all) * up, out.grad, t, 256);
     }
   }
-  write_outside(q, out.grad, (int64_t)blockIdx.x * 256 + t, (int64_t)grads * 256);
+  write_outside(q, grad, (int64_t)b * 256 + threadIdx.x,
+                ((int64_t)gridDim.x - with_loss) * 256);
+}
+
+// ---- policy
+// Tokens of [a, b) whose byte is set, by `threads` threads, 16 bytes at a time.
+__device__ __forceinline__ int32_t count_bytes(const uint8_t* mask, int32_t a, int32_t b,
+                                               int32_t thread, int32_t threads) {
+  int32_t n = 0;
+  const int32_t whole = (b - a) / 16;
+  for (int32_t i = thread; i < whole; i += threads) {
+    uint32_t v[4];
+    __builtin_memcpy(v, mask + a + (int64_t)i * 16, 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t low = v[k] & 0x7F7F7F7Fu;  // the top bit of a byte that is not 0
+      n += __builtin_popcount(((low + 0x7F7F7F7Fu) | v[k]) & 0x80808080u);
+    }
+  }
+  const int32_t i = a + whole * 16 + thread;
+  if (i < b) n += mask[i] != 0;
+  return n;
+}
+__device__ __forceinline__ int32_t wave_sum(int32_t x) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
+  return x;
+}
+
+__global__ __launch_bounds__(256) void k_policy_counts(batch_t q, int32_t* __restrict__ counts,
+                                                       int32_t* __restrict__ totals) {
+  __shared__ int32_t lds[4];
+  const int32_t w = wave_of_block(), x = blockIdx.x * 4 + w;
+  int32_t n = 0;
+  if (x < q.items) {
+    const item_t it = item_of(q, x);
+    if (it.a < it.b) n = wave_sum(count_bytes(q.mask, it.a, it.b, lane_id(), 64));
+    if (lane_id() == 0) counts[x] = n;
+  }
+  if (lane_id() == 0) lds[w] = n;
+  __syncthreads();
+  if (threadIdx.x == 0) totals[blockIdx.x] = lds[0] + lds[1] + lds[2] + lds[3];
+}
+
+// counts (nullable): what k_policy_counts has left; without them the workgroup
+// counts what it needs.  sums: of the workgroup's items, f with its weight.
+template <int LOG>
+__global__ __launch_bounds__(256) void k_policy(batch_t q, policy_t loss, out_t out,
+                                                const int32_t* __restrict__ counts,
+                                                const int32_t* __restrict__ totals,
+                                                int32_t n_totals, sums_t* __restrict__ sums) {
+  constexpr int U = 1 << (LOG - 6);
+  __shared__ sums_t lds[4];
+  __shared__ int32_t ones[4];
+  const int32_t w = wave_of_block(), lane = lane_id(), x = blockIdx.x * 4 + w;
+  const bool mine = x < q.items;
+  item_t it{0, 0, 0};
+  if (mine) it = item_of(q, x);
+  tokens_t<policy_t, U> t;
+  if (it.a < it.b) t.load(q, loss, it, it.a);
+  double n = 0;  // tokens that the loss's mean is over: of the batch, or of the sequence
+  if (!loss.sequence_mean) {
+    int32_t part = 0;
+    if (!q.mask) {
+      n = (double)max(start_of(q, q.S) - start_of(q, 0), 0);
+    } else {
+      if (totals) {
+#pragma unroll 4
+        for (int32_t i = threadIdx.x; i < n_totals; i += 256) part += totals[i];
+      } else {
+        const int32_t a = start_of(q, 0);
+        part = count_bytes(q.mask, a, max(start_of(q, q.S), a), threadIdx.x, 256);
+      }
+      part = wave_sum(part);
+      if (lane == 0) ones[w] = part;
+      __syncthreads();
+      n = (double)(ones[0] + ones[1] + ones[2] + ones[3]);
+    }
+  } else if (it.a < it.b) {
+    const int32_t a = start_of(q, it.seq), b = max(start_of(q, it.seq + 1), a);
+    if (!q.mask) {
+      n = (double)(b - a);
+    } else {
+      int32_t part = 0;
+      if (counts) {
+        const int32_t x1 = min(first_item(q, it.seq + 1, b), q.items);
+        for (int32_t i = first_item(q, it.seq, a) + lane; i < x1; i += 64) part += counts[i];
+      } else {
+        part = count_bytes(q.mask, a, b, lane, 64);
+      }
+      n = (double)wave_sum(part);
+    }
+  }
+  const double weight = loss.weight(q, n, n), c = weight * upstream(out);
+  sums_t s{0, 0, 0, 0};
+  if (it.a < it.b) {
+    float g[U];
+    t.add(loss, s, g);
+    wave_totals<policy_t>(s);
+    s.f *= weight;
+    if (out.grad) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (t.in[u]) out.grad[it.a + u * 64 + lane] = t.counts[u] ? (float)((double)g[u] * c) : 0.f;
+    }
+  }
+  if (lane == 0) lds[w] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) sums[blockIdx.x] = ((lds[0] + lds[1]) + lds[2]) + lds[3];
+  if (out.grad)
+    write_outside(q, out.grad, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+}
+
+__global__ __launch_bounds__(1024) void k_policy_finish(const sums_t* __restrict__ sums,
+                                                        int32_t n, out_t out) {
+  __shared__ sums_t lds[16];
+  sums_t s{0, 0, 0, 0};
+#pragma unroll 4
+  for (int32_t i = threadIdx.x; i < n; i += 1024) s = s + sums[i];
+  s = block_sum<16>(s, lds);
+  if (threadIdx.x != 0) return;
+  finish_stats(s, out);
+  if (out.loss) *out.loss = (float)s.f;
 }
 
 // ---------------------------------------------------------------------- host
 constexpr int32_t MAX_SEQS = 1 << 24;
 
-struct plan_t { bool small; int32_t C, blocks; size_t total; };
+// Items are small (128 tokens) where there are few: a wave's tokens are then two a
+// lane.
+constexpr int32_t MEDIUM_ITEMS = 2048;
+// Masks up to this many bytes are counted by every workgroup that needs them.
+constexpr int32_t COUNT_TOKENS = 16384;
 
-plan_t plan_of(int32_t S, int32_t Tn) {
+struct plan_t {
+  bool small;
+  int32_t log_p, items, blocks;
+  size_t sums, coef, terms, table, counts, totals, total;
+};
+
+plan_t plan_of(int32_t S, int32_t Tn, bool policy) {
   plan_t p{};
-  p.small = S <= SMALL_SEQS && Tn <= SMALL_TOKENS;
-  // slices: workgroups for every CU to have four, 1,024 tokens each at least
-  p.C = (int32_t)std::max<int64_t>(
-      1, std::min<int64_t>(1024 / std::max(S, 1), cdiv(Tn, 1024ll * std::max(S, 1))));
-  p.blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>((int64_t)S * p.C, 2048));
-  p.total = p.small ? 0 : (size_t)S * p.C * sizeof(sums_t);
+  auto items = [&](int32_t log_p) { return S == 0 ? 0 : S + (Tn >> log_p); };
+  p.small = S <= SMALL_SEQS && items(SMALL_LOG_P) <= SMALL_EACH * SMALL_WAVES;
+  p.log_p = p.small || (policy && items(SMALL_LOG_P) <= MEDIUM_ITEMS) ? SMALL_LOG_P : LOG_P;
+  p.items = items(p.log_p);
+  p.blocks = (int32_t)cdiv(p.items, 4);
+  if (p.small) return p;
+  size_t o = 0;
+  auto take = [&](size_t b) {
+    const size_t at = o;
+    o = align_up(o + b, 256);
+    return at;
+  };
+  p.sums = take((size_t)(policy ? p.blocks : p.items) * sizeof(sums_t));
+  if (policy) {
+    p.counts = take((size_t)p.items * 4);
+    p.totals = take((size_t)p.blocks * 4);
+  } else {
+    p.table = take((size_t)p.items * sizeof(item_t));
+    p.coef = take((size_t)S * sizeof(double));
+    p.terms = take((size_t)S / 2 * sizeof(double));
+  }
+  p.total = o;
   return p;
 }
 
@@ -409,18 +660,36 @@ snack_status check_batch(const snack_seqs* q) {
 }
 
 template <typename L>
-snack_status run(const snack_seqs* b, const L& loss, const out_t& out, void* ws, size_t ws_bytes,
-                 hipStream_t s) {
-  const plan_t p = plan_of(b->S, b->T);
+snack_status run(const snack_seqs* b, const plan_t& p, const L& loss, const out_t& out, void* ws,
+                 size_t ws_bytes, hipStream_t s) {
   if (p.total > 0 && !ws) return SNACK_E_NULL;
   if (ws_bytes < p.total) return SNACK_E_WORKSPACE;
-  const batch_t q{b->starts, b->mask, b->S, b->T, b->S > 0 ? b->T / b->S : 0};
+  const batch_t q{b->starts, b->mask, b->S, b->T, b->S > 0 ? b->T / b->S : 0, p.log_p, p.items};
+  char* w = (char*)ws;
+  sums_t* sums = (sums_t*)(w + p.sums);
   if (p.small) {
     hipLaunchKernelGGL(k_seq_small<L>, dim3(1), dim3(SMALL_WAVES * 64), 0, s, q, loss, out);
+  } else if constexpr (L::POLICY) {
+    int32_t *counts = nullptr, *totals = nullptr;
+    if (q.mask && q.T > COUNT_TOKENS) {
+      counts = (int32_t*)(w + p.counts), totals = (int32_t*)(w + p.totals);
+      hipLaunchKernelGGL(k_policy_counts, dim3(p.blocks), dim3(256), 0, s, q, counts, totals);
+    }
+    auto kernel = p.log_p == LOG_P ? k_policy<LOG_P> : k_policy<SMALL_LOG_P>;
+    hipLaunchKernelGGL(kernel, dim3(p.blocks), dim3(256), 0, s, q, loss, out, counts, totals,
+                       p.blocks, sums);
+    if (out.loss || out.more)
+      hipLaunchKernelGGL(k_policy_finish, dim3(1), dim3(1024), 0, s, sums, p.blocks, out);
   } else {
-    hipLaunchKernelGGL(k_seq_sums<L>, dim3(p.blocks), dim3(256), 0, s, q, loss, p.C, (sums_t*)ws);
-    hipLaunchKernelGGL(k_seq_grads<L>, dim3(out.grad ? p.blocks + 1 : 1), dim3(256), 0, s, q, loss,
-                       p.C, (const sums_t*)ws, out);
+    item_t* table = (item_t*)(w + p.table);
+    double *coef = (double*)(w + p.coef), *terms = (double*)(w + p.terms);
+    hipLaunchKernelGGL(k_pref_sums, dim3(p.blocks), dim3(256), 0, s, q, loss, sums, table);
+    hipLaunchKernelGGL(k_pref_finish, dim3((unsigned)cdiv(b->S / 2, 4)), dim3(256), 0, s, q, loss,
+                       sums, out, coef, terms);
+    const int32_t blocks = (out.loss ? 1 : 0) + (out.grad ? p.blocks : 0);
+    if (blocks > 0)
+      hipLaunchKernelGGL(k_pref_grads, dim3(blocks), dim3(256), 0, s, q, table, coef, terms,
+                         out.loss, out.grad);
   }
   SNK_CHECK_LAUNCH();
   return SNACK_OK;
@@ -438,7 +707,7 @@ snack_status snack_seqs_workspace(int32_t S, int32_t T, size_t* bytes) {
   const int32_t some = 0;
   const snack_seqs q{S, T, &some, nullptr};
   if (snack_status st = check_batch(&q)) return st;
-  *bytes = plan_of(S, T).total;
+  *bytes = std::max(plan_of(S, T, false).total, plan_of(S, T, true).total);
   return SNACK_OK;
 }
 
@@ -454,13 +723,13 @@ snack_status snack_preference(const snack_seqs* batch, const snack_pref* pref, c
     return SNACK_E_SHAPE;
   if (batch->T > 0 && !logps) return SNACK_E_NULL;
   const __int128 t = 4 * (__int128)batch->T, n = batch->S;
-  const plan_t p = plan_of(batch->S, batch->T);
+  const plan_t p = plan_of(batch->S, batch->T, false);
   const span_t out[] = {{loss, 4}, {rewards, 4 * n}, {dlogps, t}, {ws, (__int128)p.total}};
   const span_t in[] = {{logps, t}, {ref, t}, {dloss, 4}, {batch->starts, 4 * (n + 1)},
                        {batch->mask, batch->T}};
   if (any_overlap(out, in)) return SNACK_E_SHAPE;
   const pref_t l{logps, ref, pref->beta, pref->smoothing, pref->form, pref->average};
-  return run(batch, l, out_t{dloss, loss, rewards, dlogps}, ws, ws_bytes,
+  return run(batch, p, l, out_t{dloss, loss, rewards, dlogps}, ws, ws_bytes,
              reinterpret_cast<hipStream_t>(stream));
 }
 
@@ -478,7 +747,7 @@ snack_status snack_policy_loss(const snack_seqs* batch, const snack_policy* poli
   const int64_t na = policy->by_token ? batch->T : batch->S;
   if ((batch->T > 0 && !logps) || (na > 0 && !advantages)) return SNACK_E_NULL;
   const __int128 t = 4 * (__int128)batch->T, n = batch->S;
-  const plan_t p = plan_of(batch->S, batch->T);
+  const plan_t p = plan_of(batch->S, batch->T, true);
   const span_t out[] = {{loss, 4}, {stats, 8}, {dlogps, t}, {ws, (__int128)p.total}};
   const span_t in[] = {{logps, t}, {old, t}, {ref, t}, {advantages, 4 * (__int128)na}, {dloss, 4},
                        {batch->starts, 4 * (n + 1)}, {batch->mask, batch->T}};
@@ -486,7 +755,7 @@ snack_status snack_policy_loss(const snack_seqs* batch, const snack_policy* poli
   const policy_t l{logps, old, ref, advantages, std::log1p(-policy->low), std::log1p(policy->high),
                    (float)(1.0 - policy->low), (float)(1.0 + policy->high), (float)policy->kl,
                    policy->by_token, policy->sequence_mean};
-  return run(batch, l, out_t{dloss, loss, stats, dlogps}, ws, ws_bytes,
+  return run(batch, p, l, out_t{dloss, loss, stats, dlogps}, ws, ws_bytes,
              reinterpret_cast<hipStream_t>(stream));
 }
 
