@@ -693,7 +693,7 @@ SNACK_API snack_status snack_dropout(snack_dtype dtype, const void* X, int64_t l
  * snack_embed_workspace: bytes of ws for the gradient.  Asynchronous; same bits
  * for the same inputs.  Errors: SNACK_E_NULL, SNACK_E_DTYPE (dtype, id_bytes),
  * SNACK_E_SHAPE (sizes, strides, overlap), SNACK_E_OVERFLOW (T > 2^28, V > 2^30,
- * D > 2^23, or 2^32 - 2^20 pieces of 16 bytes in the T or V rows),
+ * D > 2^23, or more than 2^32 - 2^20 pieces of 16 bytes in V + T + T / 8 + 4 rows),
  * SNACK_E_WORKSPACE.
  */
 SNACK_API snack_status snack_embed_fwd(snack_dtype dtype, const void* ids, int32_t id_bytes,

@@ -543,7 +543,7 @@ def test_workspaces():
         snk.snack_embed_workspace(7, 1, 1, 1)
     with pytest.raises(snk.SnackError):
         snk.snack_logp_workspace(b.F32, 1, 0)
-    # sums of rows with many tokens, two slots for every 32
+    # sums of rows with many tokens, two slots for every 32 at least
     assert snk.snack_embed_workspace(b.BF16, 6400, 10, 64) >= 2 * 200 * 64 * 4
     assert b.raw_status("snack_embed_workspace", 0, 1, 1, 1, None) == -1
     assert b.raw_status("snack_logp_workspace", 0, 1, 1, None) == -1

@@ -4,13 +4,15 @@
 //   dW[v, :] = base[v, :] + scale sum_{i : ids[i] = v} dY[i, :]
 //
 // The lookup is a copy of rows.  The gradient sorts the tokens by their number
-// first (k_embed_sort, which also writes the rows that no token has: most of a
-// table) and then sums each table row's tokens in the sorted order
+// first (k_embed_sort) and then sums each table row's tokens in the sorted order
 // (k_embed_sum), so no float is added by an atomic and the same inputs give the
 // same bits.  A text's most frequent token has many times the mean: rows of
 // more than RUN tokens are summed in pieces of the sorted order, RUN places
-// each, which k_embed_join adds.  Bound by memory: dY once, every row of dW
-// once.
+// each, which k_embed_join adds.  Rows without a token, most of a table, are
+// written beside the sums.  Bound by memory where the table is large: dY once,
+// every row of dW once; elsewhere by the three launches and their trips to memory.
+#include <type_traits>
+
 #include "common.h"
 #include "internal.h"
 #include "pieces.h"
@@ -46,13 +48,12 @@ __global__ __launch_bounds__(256) void k_embed(ids_t ids, int64_t Tn, const T* _
 }
 
 // --------------------------------------------------------------------- sort
-constexpr int32_t RUN = 32;         // sorted places of a piece
-constexpr int SORT_WAVES = 16;
+constexpr int32_t RUN = 16;         // sorted places of a piece
 constexpr int32_t MAX_RANGE = 512;  // table rows of a sorting workgroup
 
-// A place of the sorted order: its token and table row, and the places [begin,
-// end) of that row.
-struct __attribute__((aligned(16))) place_t { int32_t token, row, begin, end; };
+// A place of the sorted order: its table row, and the places [begin, end) of that
+// row.  Places past the last token have begin -1.
+struct __attribute__((aligned(16))) place_t { int32_t row, begin, end, zero; };
 
 struct sum_arg {
   const void* dY;
@@ -64,130 +65,182 @@ struct sum_arg {
   void* dW;
   int64_t lddw;
   const place_t* order;
-  const int32_t* all;  // places that the order has
-  float* part;         // two slots of per * EL floats for each RUN places
+  const int32_t* tokens;  // of each place, and RUN more
+  const uint8_t* used;    // whether a table row has tokens
+  float* part;            // two slots of per * EL floats for each RUN places
   uint32_t per;
 };
 
-// acc times the scale, and base, into row v.
 template <typename T>
-__device__ __forceinline__ void put_row(const sum_arg& a, int32_t v, cut_t c,
-                                        float (&acc)[EL<T>]) {
-  float b[EL<T>] = {};
-  if (a.base) floats_of(load_cut((const T*)a.base + (int64_t)v * a.ldb, c, a.D), b);
+__device__ __forceinline__ frag<T> load_base(const sum_arg& a, int32_t v, cut_t c) {
+  if (!a.base) return frag<T>{};
+  return load_cut((const T*)a.base + (int64_t)v * a.ldb, c, a.D);
+}
+template <typename T>
+__device__ __forceinline__ void store_row(const sum_arg& a, int32_t v, cut_t c, const frag<T>& f) {
+  store_cut((T*)a.dW + (int64_t)v * a.lddw, c, a.D, f);
+}
+// base and acc times the scale.
+template <typename T>
+__device__ __forceinline__ frag<T> with_base(const sum_arg& a, const frag<T>& base,
+                                             const float (&acc)[EL<T>]) {
+  float b[EL<T>];
+  floats_of(base, b);
 #pragma unroll
-  for (int e = 0; e < EL<T>; ++e) acc[e] = fmaf(acc[e], a.scale, b[e]);
-  store_cut((T*)a.dW + (int64_t)v * a.lddw, c, a.D, to_frag(acc));
+  for (int e = 0; e < EL<T>; ++e) b[e] = fmaf(acc[e], a.scale, b[e]);
+  return to_frag(b);
 }
 
 // Each workgroup owns `range` rows of the table and reads all token numbers:
 // those below its rows give the place where its own begin, so the workgroups
-// need nothing of each other.  Its waves take every 16th block of 64 tokens,
-// count theirs by row, and walk them again to place them: a row's tokens are in
-// the order of waves, blocks and lanes.  (With consecutive shares, the waves of
-// all workgroups read addresses that are a multiple of 4 KB apart, one channel of
-// the L2: 9.7 us for 8,192 tokens instead of 6.)  Between the two walks it writes
-// the rows that have no token.
-template <typename T>
-__global__ __launch_bounds__(SORT_WAVES * 64) void k_embed_sort(sum_arg a, ids_t ids, int32_t Tn,
-                                                                int32_t range) {
+// need nothing of each other.  What each costs is a few instructions for every
+// number, all workgroups together T V / range of them.  Its W waves take every
+// W-th block of 64 tokens, count theirs by row and list them, and place them when
+// all are counted: a row's tokens are in the order of waves, blocks and lanes.
+// (With consecutive shares, the waves of all workgroups read addresses that are a
+// multiple of 4 KB apart, one channel of the L2.)  Waves with more than LIST tokens
+// read the numbers again instead.
+constexpr int LIST = 512;
+
+template <int W, typename I>
+__global__ __launch_bounds__(W * 64) void k_embed_sort(const I* __restrict__ ids, int32_t Tn,
+                                                       int32_t V, int32_t range, int32_t bits,
+                                                       place_t* __restrict__ order,
+                                                       int32_t* __restrict__ tokens,
+                                                       uint8_t* __restrict__ used) {
+  typedef typename std::make_unsigned<I>::type UI;
   extern __shared__ int32_t lds[];
-  int32_t *count = lds, *begin_of = count + SORT_WAVES * range, *end_of = begin_of + range,
-          *below_of = end_of + range, *scan = below_of + SORT_WAVES;
-  const int w = threadIdx.x / 64, lane = lane_id();
-  const int32_t lo = blockIdx.x * range, hi = min(lo + range, a.V);
-  for (int32_t q = threadIdx.x; q < SORT_WAVES * range; q += SORT_WAVES * 64) count[q] = 0;
-  __syncthreads();
-  constexpr int U = 4, STEP = SORT_WAVES * 64;
-  int32_t* mine = count + w * range;
-  int32_t below = 0;
-  auto load = [&](int64_t from, int32_t (&v)[U]) {
+  int32_t *count = lds, *begin_of = count + W * range, *end_of = begin_of + range,
+          *below_of = end_of + range, *scan = below_of + W, *list = scan + W;
+  uint16_t* list_row = reinterpret_cast<uint16_t*>(list + W * LIST);
+  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64), lane = lane_id();
+  const int32_t lo = blockIdx.x * range, hi = min(lo + range, V);
+  constexpr int U = 4, STEP = W * 64;
+  int32_t *mine = count + w * range, *my_token = list + w * LIST;
+  uint16_t* my_row = list_row + w * LIST;
+  I v[U];
+  auto load = [&](int64_t at) {
+    if (at + U * STEP <= Tn) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = ids.get(min(from + u * STEP, (int64_t)Tn - 1), a.V);
+      for (int u = 0; u < U; ++u) v[u] = ids[at + u * STEP + threadIdx.x];
+    } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (from + u * STEP >= Tn) v[u] = -1;
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = at + u * STEP + threadIdx.x;
+        v[u] = i < Tn ? ids[i] : (I)-1;
+      }
+    }
   };
-  for (int64_t at = 0; at < Tn; at += U * STEP) {
-    int32_t v[U];
-    load(at + threadIdx.x, v);
+  // Whether v is one of this workgroup's rows, and which; as an unsigned number a
+  // negative one is past every table.
+  auto row_of = [&](I v, int32_t* row) {
+    const UI d = (UI)v - (UI)lo;
+    *row = (int32_t)d;
+    return d < (UI)(hi - lo);
+  };
+  load(0);
+  for (int32_t q = threadIdx.x; q < W * range; q += STEP) count[q] = 0;
+  __syncthreads();
+  int32_t below = 0, hits = 0;
+  for (int64_t at = 0; at < Tn;) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      below += __popcll(__ballot(v[u] >= 0 && v[u] < lo));
-      if (v[u] >= lo && v[u] < hi) atomicAdd(&mine[v[u] - lo], 1);
+      below += (int32_t)__popcll(__ballot((UI)v[u] < (UI)lo));
+      int32_t row;
+      const bool in = row_of(v[u], &row);
+      const uint64_t mask = __ballot(in);
+      if (mask) {
+        const int32_t to = hits + (int32_t)__popcll(mask & lanemask_lt());
+        if (in) atomicAdd(&mine[row], 1);
+        if (in && to < LIST) {
+          my_token[to] = (int32_t)at + u * STEP + (int32_t)threadIdx.x;
+          my_row[to] = (uint16_t)row;
+        }
+        hits += (int32_t)__popcll(mask);
+      }
     }
+    at += U * STEP;
+    if (at < Tn) load(at);
   }
   if (lane == 0) below_of[w] = below;
   __syncthreads();
   int32_t all_below = 0, total = 0, own = 0;
 #pragma unroll
-  for (int q = 0; q < SORT_WAVES; ++q) all_below += below_of[q];
+  for (int q = 0; q < W; ++q) all_below += below_of[q];
   const int32_t r = threadIdx.x;
   if (r < range) {
 #pragma unroll
-    for (int q = 0; q < SORT_WAVES; ++q) own += count[q * range + r];
+    for (int q = 0; q < W; ++q) own += count[q * range + r];
+    if (lo + r < V) used[lo + r] = own > 0;
   }
-  int32_t place = all_below + block_excl_scan_i32<SORT_WAVES * 64>(own, scan, &total);
+  int32_t place = all_below + block_excl_scan_i32<STEP>(own, scan, &total);
+  if (hi == V)  // places that no token takes
+    for (int64_t k = (int64_t)all_below + total + threadIdx.x; k < Tn; k += STEP)
+      order[k] = place_t{-1, -1, -1, 0};
+  if (total == 0) return;
   if (r < range) {
     begin_of[r] = place;
     end_of[r] = place + own;
 #pragma unroll
-    for (int q = 0; q < SORT_WAVES; ++q) {
+    for (int q = 0; q < W; ++q) {
       const int32_t n = count[q * range + r];
       count[q * range + r] = place;
       place += n;
     }
   }
-  if (threadIdx.x == 0 && hi == a.V) *const_cast<int32_t*>(a.all) = all_below + total;
   __syncthreads();
-  if (a.base != a.dW) {  // in place nothing is added to them
-    const uint32_t n = (uint32_t)(hi - lo) * a.per;
-    for (uint32_t g = threadIdx.x; g < n; g += SORT_WAVES * 64) {
-      const int32_t row = (int32_t)(g / a.per);
-      if (begin_of[row] != end_of[row]) continue;
-      float acc[EL<T>] = {};
-      put_row<T>(a, lo + row, cut_of<T>((int32_t)(g % a.per), a.D), acc);
+  auto put = [&](bool in, int32_t row, int32_t token) {
+    uint64_t same = __ballot(in);  // lanes of the same row
+    for (int32_t k = 0; k < bits; ++k) {
+      const bool bit = (row >> k) & 1;
+      const uint64_t set = __ballot(bit);
+      same &= bit ? set : ~set;
     }
-  }
-  if (total == 0) return;
-  place_t* order = const_cast<place_t*>(a.order);
-  for (int64_t at = 0; at < Tn; at += U * STEP) {
-    int32_t v[U];
-    load(at + threadIdx.x, v);
+    int32_t to = 0;
+    const int32_t before = (int32_t)__popcll(same & lanemask_lt());
+    if (in && before == 0) to = atomicAdd(&mine[row], (int32_t)__popcll(same));
+    to = __shfl(to, same ? __ffsll((unsigned long long)same) - 1 : 0) + before;
+    if (in) {
+      tokens[to] = token;
+      order[to] = place_t{row + lo, begin_of[row], end_of[row], 0};
+    }
+  };
+  if (hits <= LIST) {
+    for (int32_t h = 0; h < hits; h += 64) {
+      const bool in = h + lane < hits;
+      put(in, in ? my_row[h + lane] : 0, in ? my_token[h + lane] : 0);
+    }
+  } else {
+    load(0);
+    for (int64_t at = 0; at < Tn; at += U * STEP) {
+      int32_t row[U];
+      bool in[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool in = v[u] >= lo && v[u] < hi;
-      // lanes of one row at a time
-      for (uint64_t todo = __ballot(in); todo;) {
-        const int leader = __ffsll((unsigned long long)todo) - 1;
-        const int32_t row = __shfl(v[u], leader);
-        const uint64_t same = __ballot(in && v[u] == row);
-        int32_t to = 0;
-        if (lane == leader) to = atomicAdd(&mine[row - lo], __popcll(same));
-        to = __shfl(to, leader) + __popcll(same & lanemask_lt());
-        if (in && v[u] == row)
-          order[to] = place_t{(int32_t)(at + u * STEP) + (int32_t)threadIdx.x, row,
-                              begin_of[row - lo], end_of[row - lo]};
-        todo &= ~same;
-      }
+      for (int u = 0; u < U; ++u) in[u] = row_of(v[u], &row[u]);
+      if (at + U * STEP < Tn) load(at + U * STEP);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (__ballot(in[u]))
+          put(in[u], in[u] ? row[u] : 0, (int32_t)at + u * STEP + (int32_t)threadIdx.x);
     }
   }
 }
 
 // ---------------------------------------------------------------------- sums
-// acc += the tokens of places [k, end), at cut c.
+// The sum of the tokens of places [k, end), RUN at most, at cut c.
 template <typename T>
-__device__ __forceinline__ void add_tokens(const sum_arg& a, int32_t k, int32_t end, cut_t c,
+__device__ __forceinline__ void sum_tokens(const sum_arg& a, int32_t k, int32_t end, cut_t c,
                                            float (&acc)[EL<T>]) {
-  constexpr int U = 4;
+  constexpr int U = RUN / 2;
   const T* dY = (const T*)a.dY;
+#pragma unroll 1
   for (; k < end; k += U) {
     frag<T> f[U];
     int32_t tok[U];
+    __builtin_memcpy(tok, a.tokens + k, sizeof(tok));
 #pragma unroll
-    for (int u = 0; u < U; ++u) tok[u] = a.order[min(k + u, end - 1)].token;
-#pragma unroll
-    for (int u = 0; u < U; ++u) f[u] = load_cut(dY + (int64_t)tok[u] * a.lddy, c, a.D);
+    for (int u = 0; u < U; ++u)
+      f[u] = load_cut(dY + (int64_t)(k + u < end ? tok[u] : tok[0]) * a.lddy, c, a.D);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float v[EL<T>];
@@ -198,94 +251,121 @@ __device__ __forceinline__ void add_tokens(const sum_arg& a, int32_t k, int32_t 
   }
 }
 
-// The first `blocks` workgroups take the places at which a table row begins, the
-// others the pieces of rows of more than RUN tokens: of each RUN places those of
-// such a row that began before (slot 0) and of one that begins there (slot 1);
-// it goes on past them, so there is one at most.
+// Workgroups up to `sums` take the places at which a table row begins; up to
+// `pieces` the pieces of rows of more than RUN tokens: of each RUN places those of
+// such a row that began before (slot 0) and of one that begins there (slot 1; it
+// goes on past them, so there is one at most); the others the rows without a token.
 template <typename T>
-__global__ __launch_bounds__(256) void k_embed_sum(sum_arg a, uint32_t blocks) {
+__global__ __launch_bounds__(256) void k_embed_sum(sum_arg a, int32_t Tn, uint32_t sums,
+                                                   uint32_t pieces) {
   constexpr int E = EL<T>;
   float acc[E] = {};
-  const int32_t all = *a.all;
-  if (blockIdx.x < blocks) {
+  if (blockIdx.x < sums) {
     const uint32_t g = blockIdx.x * 256u + threadIdx.x;
     const int32_t k = (int32_t)(g / a.per);
-    if (k >= all) return;
+    if (k >= Tn) return;
     const place_t p = a.order[k];
     if (p.begin != k || p.end - k > RUN) return;
     const cut_t c = cut_of<T>((int32_t)(g % a.per), a.D);
-    add_tokens<T>(a, k, p.end, c, acc);
-    put_row<T>(a, p.row, c, acc);
+    const frag<T> base = load_base<T>(a, p.row, c);
+    sum_tokens<T>(a, k, p.end, c, acc);
+    store_row(a, p.row, c, with_base(a, base, acc));
     return;
   }
-  const uint32_t g = (blockIdx.x - blocks) * 256u + threadIdx.x;
-  const uint32_t slot = g / a.per, q = g % a.per;
-  const int64_t from = (int64_t)(slot / 2) * RUN;
-  if (from >= all) return;
-  const int32_t to = (int32_t)min(from + RUN, (int64_t)all);
-  const place_t p = a.order[slot & 1 ? to - 1 : from];
-  if (p.end - p.begin <= RUN || (p.begin < from) == (slot & 1)) return;
-  add_tokens<T>(a, max(p.begin, (int32_t)from), min(p.end, to), cut_of<T>((int32_t)q, a.D), acc);
-  float* part = a.part + ((int64_t)slot * a.per + q) * E;
+  if (blockIdx.x < pieces) {
+    const uint32_t g = (blockIdx.x - sums) * 256u + threadIdx.x;
+    const uint32_t slot = g / a.per, q = g % a.per;
+    const int64_t from = (int64_t)(slot / 2) * RUN;
+    if (from >= Tn) return;
+    // a row of more than RUN places that ends past the last whole piece has slot 0
+    const int64_t last = min(from + RUN, (int64_t)Tn) - 1;
+    const place_t p = a.order[slot & 1 ? last : from];
+    if (p.begin < 0 || p.end - p.begin <= RUN || (p.begin < from) == (slot & 1)) return;
+    sum_tokens<T>(a, max(p.begin, (int32_t)from), (int32_t)min((int64_t)p.end, from + RUN),
+                  cut_of<T>((int32_t)q, a.D), acc);
+    float* part = a.part + ((int64_t)slot * a.per + q) * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) part[e] = acc[e];
+    for (int e = 0; e < E; ++e) part[e] = acc[e];
+    return;
+  }
+  const uint32_t g = (blockIdx.x - pieces) * 256u + threadIdx.x;
+  const int32_t v = (int32_t)(g / a.per);
+  if (v >= a.V || a.used[v]) return;
+  const cut_t c = cut_of<T>((int32_t)(g % a.per), a.D);
+  store_row(a, v, c, load_base<T>(a, v, c));
 }
 
-// Rows of more than RUN tokens: one that begins among the RUN places of this
-// workgroup, 64 pieces of it; the waves add consecutive shares of its slots.
+// Rows of more than RUN tokens: those that begin in the JOIN pieces of this
+// workgroup, 64 of the row's columns' pieces; the waves add consecutive shares of
+// a row's slots.
+constexpr int32_t JOIN = 16;
+constexpr int JOIN_WAVES = 16;
+
 template <typename T>
-__global__ __launch_bounds__(256) void k_embed_join(sum_arg a) {
+__global__ __launch_bounds__(JOIN_WAVES * 64) void k_embed_join(sum_arg a, int32_t Tn) {
   constexpr int E = EL<T>;
-  __shared__ float lds[4][64][E + 1];
-  const int32_t tile = blockIdx.x, from = tile * RUN, all = *a.all;
-  if (from >= all) return;
-  const place_t at = a.order[min(from + RUN, all) - 1];
-  if (at.end - at.begin <= RUN || at.begin < from) return;
-  const int32_t n = (at.end - 1) / RUN - tile + 1;  // slots: this tile's second, the others' first
+  __shared__ float lds[JOIN_WAVES][64][E + 1];
   const int w = threadIdx.x / 64, lane = lane_id();
+  const int64_t from = ((int64_t)blockIdx.x * JOIN + lane) * RUN;
+  place_t at{0, 0, 0, 0};
+  if (lane < JOIN && from < Tn) at = a.order[min(from + RUN, (int64_t)Tn) - 1];
+  uint64_t todo = __ballot(at.end - at.begin > RUN && at.begin >= from);
   const uint32_t q = blockIdx.y * 64 + lane;
-  float acc[E] = {};
-  if (q < a.per) {
-    const int32_t j1 = (int32_t)((int64_t)n * (w + 1) / 4);
-#pragma unroll 4
-    for (int32_t j = (int32_t)((int64_t)n * w / 4); j < j1; ++j) {
-      const int64_t slot = 2ll * (tile + j) + (j == 0);
-      const float* p = a.part + (slot * a.per + q) * E;
+  for (; todo; todo &= todo - 1) {
+    const int l = __ffsll((unsigned long long)todo) - 1;
+    const int32_t tile = blockIdx.x * JOIN + l, row = __shfl(at.row, l);
+    // slots: this piece's second, the others' first
+    const int32_t n = (__shfl(at.end, l) - 1) / RUN - tile + 1;
+    const cut_t c = cut_of<T>((int32_t)min(q, a.per - 1), a.D);
+    frag<T> base{};
+    float acc[E] = {};
+    if (q < a.per) {
+      if (w == 0) base = load_base<T>(a, row, c);
+      const int32_t j1 = (int32_t)((int64_t)n * (w + 1) / JOIN_WAVES);
+#pragma unroll 8
+      for (int32_t j = (int32_t)((int64_t)n * w / JOIN_WAVES); j < j1; ++j) {
+        const int64_t slot = 2ll * (tile + j) + (j == 0);
+        const float* p = a.part + (slot * a.per + q) * E;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += p[e];
+        for (int e = 0; e < E; ++e) acc[e] += p[e];
+      }
     }
+#pragma unroll
+    for (int e = 0; e < E; ++e) lds[w][lane][e] = acc[e];
+    __syncthreads();
+    if (w == 0 && q < a.per) {
+#pragma unroll
+      for (int k = 1; k < JOIN_WAVES; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += lds[k][lane][e];
+      store_row(a, row, c, with_base(a, base, acc));
+    }
+    __syncthreads();
   }
-#pragma unroll
-  for (int e = 0; e < E; ++e) lds[w][lane][e] = acc[e];
-  __syncthreads();
-  if (w != 0 || q >= a.per) return;
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    acc[e] = ((lds[0][lane][e] + lds[1][lane][e]) + lds[2][lane][e]) + lds[3][lane][e];
-  put_row<T>(a, at.row, cut_of<T>((int32_t)q, a.D), acc);
 }
 
 struct plan_t {
   int64_t per, tiles;  // tiles: 0 if no row can have more than RUN tokens
-  int32_t range;
-  size_t all, order, part, total;
+  int32_t range, waves;
+  size_t order, tokens, used, part, total;
 };
 
 plan_t plan_of(snack_dtype dt, int64_t Tn, int32_t V, int32_t D) {
   plan_t p{};
   p.per = cdiv(D, dt == SNACK_BF16 ? 8 : 4);
   p.tiles = Tn > RUN ? cdiv(Tn, RUN) : 0;
-  // two sorting workgroups on a CU, with 32 rows at least: every one reads all
-  // token numbers
-  p.range = (int32_t)std::min<int64_t>(MAX_RANGE, std::max<int64_t>(32, cdiv(V, 512)));
+  // a sorting workgroup on a CU, with 32 rows at least
+  p.range = (int32_t)std::min<int64_t>(MAX_RANGE, std::max<int64_t>(32, cdiv(V, 256)));
+  p.waves = Tn <= 2048 && p.range <= 256 ? 4 : 16;
   size_t o = 0;
   auto take = [&](size_t b) {
     const size_t at = o;
     o = align_up(o + b, 256);
     return at;
   };
-  p.all = take(4);
   p.order = take(sizeof(place_t) * (size_t)Tn);
+  p.tokens = take(4 * ((size_t)Tn + RUN));
+  p.used = take((size_t)V);
   p.part = take((size_t)p.tiles * 2 * p.per * (dt == SNACK_BF16 ? 32 : 16));
   p.total = std::max<size_t>(o, 256);
   return p;
@@ -298,23 +378,35 @@ snack_status check_embed(snack_dtype dt, int32_t id_bytes, int64_t Tn, int32_t V
   // what a launch of each kernel holds
   const int64_t per = cdiv(D, dt == SNACK_BF16 ? 8 : 4);
   if (Tn > MAX_TOKENS || V > MAX_ROWS || D > MAX_FEATURES) return SNACK_E_OVERFLOW;
-  if (per > 0 && (Tn + Tn / (RUN / 2) + 2 > MAX_PIECES / per || V > MAX_PIECES / per))
+  if (per > 0 && V + Tn + Tn / (RUN / 2) + 4 > MAX_PIECES / per)
     return SNACK_E_OVERFLOW;
   return SNACK_OK;
 }
 
+template <int W, typename I>
+void launch_sort(const void* ids, int32_t Tn, const plan_t& p, const sum_arg& a, hipStream_t s) {
+  int32_t bits = 0;
+  while ((1 << bits) < p.range) ++bits;
+  hipLaunchKernelGGL((k_embed_sort<W, I>), dim3((unsigned)cdiv(a.V, p.range)), dim3(W * 64),
+                     4 * ((size_t)(W + 2) * p.range + 2 * W + W * LIST) + 2 * W * LIST, s, (const I*)ids, Tn,
+                     a.V, p.range, bits, const_cast<place_t*>(a.order),
+                     const_cast<int32_t*>(a.tokens), const_cast<uint8_t*>(a.used));
+}
+
 template <typename T>
 void run_bwd(ids_t ids, int32_t Tn, const plan_t& p, const sum_arg& a, hipStream_t s) {
-  hipLaunchKernelGGL(k_embed_sort<T>, dim3((unsigned)cdiv(a.V, p.range)), dim3(SORT_WAVES * 64),
-                     4 * ((SORT_WAVES + 2) * (size_t)p.range + 2 * SORT_WAVES), s, a, ids, Tn,
-                     p.range);
-  if (Tn == 0) return;
-  const int64_t blocks = cdiv(Tn * p.per, 256), more = cdiv(2 * p.tiles * p.per, 256);
-  hipLaunchKernelGGL(k_embed_sum<T>, dim3((unsigned)(blocks + more)), dim3(256), 0, s, a,
-                     (uint32_t)blocks);
+  auto sort = p.waves == 4 ? (ids.wide ? launch_sort<4, int64_t> : launch_sort<4, int32_t>)
+                           : (ids.wide ? launch_sort<16, int64_t> : launch_sort<16, int32_t>);
+  sort(ids.p, Tn, p, a, s);
+  const int64_t sums = cdiv(Tn * p.per, 256), pieces = sums + cdiv(2 * p.tiles * p.per, 256),
+                blocks = pieces + (a.base != a.dW ? cdiv(a.V * p.per, 256) : 0);
+  if (blocks > 0)
+    hipLaunchKernelGGL(k_embed_sum<T>, dim3((unsigned)blocks), dim3(256), 0, s, a, Tn,
+                       (uint32_t)sums, (uint32_t)pieces);
   if (p.tiles > 0)
-    hipLaunchKernelGGL(k_embed_join<T>, dim3((unsigned)p.tiles, (unsigned)cdiv(p.per, 64)),
-                       dim3(256), 0, s, a);
+    hipLaunchKernelGGL(k_embed_join<T>,
+                       dim3((unsigned)cdiv(p.tiles, JOIN), (unsigned)cdiv(p.per, 64)),
+                       dim3(JOIN_WAVES * 64), 0, s, a, Tn);
 }
 
 }  // namespace
@@ -377,7 +469,8 @@ snack_status snack_embed_bwd(snack_dtype dtype, const void* ids, int32_t id_byte
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   char* b = (char*)ws;
   const sum_arg a{dY, lddy, V, D, scale, base, ldb, dW, lddw, (const place_t*)(b + p.order),
-                  (const int32_t*)(b + p.all), (float*)(b + p.part), (uint32_t)p.per};
+                  (const int32_t*)(b + p.tokens), (const uint8_t*)(b + p.used),
+                  (float*)(b + p.part), (uint32_t)p.per};
   const ids_t of{ids, id_bytes == 8};
   if (dtype == SNACK_BF16) run_bwd<bf16>(of, (int32_t)T, p, a, s);
   else run_bwd<float>(of, (int32_t)T, p, a, s);

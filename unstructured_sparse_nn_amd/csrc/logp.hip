@@ -56,24 +56,24 @@ __device__ __forceinline__ void add_pieces(soft_t& a, const frag<T> (&f)[U]) {
   a = {m, s + s1};
 }
 
-// n elements at x for the 256 threads of a workgroup.
-template <typename T>
-__device__ __forceinline__ soft_t soft_of(const T* x, int64_t n) {
+// n elements at x for N threads, of which this one is number t.
+template <int N, typename T>
+__device__ __forceinline__ soft_t soft_of(const T* x, int32_t n, int32_t t) {
   constexpr int E = EL<T>, U = 4;
   soft_t a{LOWEST, 0.f};
-  const int64_t whole = n / E;
-  int64_t q = threadIdx.x;
-  for (; q + (U - 1) * 256 < whole; q += U * 256) {
+  const int32_t whole = n / E;
+  int32_t q = t;
+  for (; q + (U - 1) * N < whole; q += U * N) {
     frag<T> f[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) f[u] = load_frag(x + (q + u * 256) * E);
+    for (int u = 0; u < U; ++u) f[u] = load_frag(x + (int64_t)(q + u * N) * E);
     add_pieces<T, U>(a, f);
   }
-  for (; q < whole; q += 256) {
-    const frag<T> f[1] = {load_frag(x + q * E)};
+  for (; q < whole; q += N) {
+    const frag<T> f[1] = {load_frag(x + (int64_t)q * E)};
     add_pieces<T, 1>(a, f);
   }
-  const int64_t i = whole * E + threadIdx.x;
+  const int32_t i = whole * E + t;
   if (i < n) a = join(a, soft_t{fmaxf(elem<T>::to_f(x[i]), LOWEST),
                                 exp_of(elem<T>::to_f(x[i]) - fmaxf(elem<T>::to_f(x[i]), LOWEST))});
   return a;
@@ -88,29 +88,34 @@ __device__ __forceinline__ void put_logp(soft_t a, float x, int32_t t, int64_t i
   norm[i] = make_float2(a.m, l);
 }
 
-// Workgroup (c, i): part c of row i; with one part a row it ends there.
-template <typename T>
-__global__ __launch_bounds__(256) void k_logp(const T* __restrict__ x, int64_t ldx, int32_t V,
-                                              ids_t ids, int32_t parts, int32_t each,
-                                              float* __restrict__ logp, float2* __restrict__ norm,
-                                              float2* __restrict__ part) {
-  __shared__ soft_t lds[4];
-  const int64_t i = blockIdx.x / parts;
-  const int32_t c = blockIdx.x % parts;
+// W waves for part c of row i; with one part a row it ends there.  Workgroups
+// have 4 waves at least.
+template <typename T, int W>
+__global__ __launch_bounds__(W < 4 ? 256 : W * 64) void k_logp(
+    const T* __restrict__ x, int64_t ldx, int64_t Tn, int32_t V, ids_t ids, int32_t parts,
+    int32_t each, float* __restrict__ logp, float2* __restrict__ norm, float2* __restrict__ part) {
+  constexpr int ROWS = W < 4 ? 4 / W : 1;  // of a workgroup
+  __shared__ soft_t lds[W];
+  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
+  const int64_t i = blockIdx.x / parts * (int64_t)ROWS + w / W;
+  if (W < 4 && i >= Tn) return;
+  const int32_t c = blockIdx.x % parts, t = threadIdx.x % (W * 64);
   const T* row = x + i * ldx;
-  int32_t t = 0;
+  int32_t target = 0;
   float xt = 0.f;
-  if (parts == 1 && threadIdx.x == 0) {
-    t = ids.get(i, V);
-    if (t >= 0) xt = elem<T>::to_f(row[t]);
+  if (parts == 1 && t == 0) {
+    target = ids.get(i, V);
+    if (target >= 0) xt = elem<T>::to_f(row[target]);
   }
-  soft_t a = soft_of<T>(row + (int64_t)c * each, min(each, V - c * each));
-  a = wave_join(a);
-  if (lane_id() == 0) lds[threadIdx.x / 64] = a;
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  a = join(join(lds[0], lds[1]), join(lds[2], lds[3]));
-  if (parts == 1) put_logp(a, xt, t, i, logp, norm);
+  soft_t a = wave_join(soft_of<W * 64>(row + (int64_t)c * each, min(each, V - c * each), t));
+  if constexpr (W > 1) {
+    if (t % 64 == 0) lds[w] = a;
+    __syncthreads();
+    if (w != 0) return;
+    a = wave_join(t < W ? lds[t] : soft_t{LOWEST, 0.f});
+  }
+  if (t != 0) return;
+  if (parts == 1) put_logp(a, xt, target, i, logp, norm);
   else part[blockIdx.x] = make_float2(a.m, a.s);
 }
 
@@ -133,17 +138,37 @@ __global__ __launch_bounds__(64) void k_logp_join(const T* __restrict__ x, int64
   if (lane_id() == 0) put_logp(a, xt, t, i, logp, norm);
 }
 
+// One piece of a row's gradient: lane's piece c, f its logits.
+template <typename T>
+__device__ __forceinline__ frag<T> grad_piece(const frag<T>& f, cut_t c, int32_t t, float g,
+                                              float2 n) {
+  constexpr int E = EL<T>;
+  const bool zero = g == 0.f || n.y == -__builtin_inff();  // or a row of -infinity only
+  float v[E];
+  floats_of(f, v);
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = zero ? 0.f : -g * exp_of((v[e] - n.x) - n.y);
+  if ((uint32_t)(t - c.at) < (uint32_t)E && !zero) {  // one piece of the row
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] += c.at + e == t ? g : 0.f;
+  }
+  return to_frag(v);
+}
+__device__ __forceinline__ float grad_of(int32_t t, const float* dlogp, int64_t i) {
+  return t == -1 ? 0.f : t == -2 ? __builtin_nanf("") : dlogp[i];
+}
+
 // Workgroup (c, i): 256 U pieces of row i.
 template <typename T>
 __global__ __launch_bounds__(256) void k_logp_grad(const T* x, int64_t ldx, int32_t V, ids_t ids,
                                                    const float* __restrict__ dlogp,
                                                    const float2* __restrict__ norm, T* dx,
                                                    int64_t lddx, uint32_t blocks) {
-  constexpr int E = EL<T>, U = 4;
+  constexpr int U = 4;
   const int64_t i = blockIdx.x / blocks;
   const int32_t first = (int32_t)(blockIdx.x % blocks) * (256 * U) + (int32_t)threadIdx.x;
-  const int32_t per = (V + E - 1) / E, t = ids.get(i, V);
-  const float g = t == -1 ? 0.f : t == -2 ? __builtin_nanf("") : dlogp[i];
+  const int32_t per = (V + EL<T> - 1) / EL<T>, t = ids.get(i, V);
+  const float g = grad_of(t, dlogp, i);
   const float2 n = norm[i];
   x += i * ldx;
   dx += i * lddx;
@@ -153,36 +178,46 @@ __global__ __launch_bounds__(256) void k_logp_grad(const T* x, int64_t ldx, int3
     for (int u = 0; u < U; ++u)
       f[u] = load_cut(x, cut_of<T>(min(first + u * 256, per - 1), V), V);
   }
-  const bool none = n.y == -__builtin_inff();  // a row of -infinity only
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (first + u * 256 >= per) break;
     const cut_t c = cut_of<T>(first + u * 256, V);
-    float v[E];
-    floats_of(f[u], v);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      v[e] = g == 0.f || none ? 0.f : -g * exp_of((v[e] - n.x) - n.y);
-    }
-    if ((uint32_t)(t - c.at) < (uint32_t)E) {  // one piece of the row
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] += c.at + e == t && !none ? g : 0.f;
-    }
-    store_cut(dx, c, V, to_frag(v));
+    store_cut(dx, c, V, grad_piece(f[u], c, t, g, n));
   }
+}
+
+// Short rows: a thread for each piece of all of them.
+template <typename T>
+__global__ __launch_bounds__(256) void k_logp_grad_short(const T* x, int64_t ldx, int64_t Tn,
+                                                         int32_t V, ids_t ids,
+                                                         const float* __restrict__ dlogp,
+                                                         const float2* __restrict__ norm, T* dx,
+                                                         int64_t lddx, uint32_t per) {
+  const uint32_t at = blockIdx.x * 256u + threadIdx.x;
+  const int64_t i = at / per;
+  if (i >= Tn) return;
+  const cut_t c = cut_of<T>((int32_t)(at % per), V);
+  const int32_t t = ids.get(i, V);
+  const float g = grad_of(t, dlogp, i);
+  frag<T> f{};
+  if (g != 0.f) f = load_cut(x + i * ldx, c, V);
+  store_cut(dx + i * lddx, c, V, grad_piece(f, c, t, g, norm[i]));
 }
 
 struct parts_t { int32_t parts, each; };
 
-// Parts of a row: workgroups enough for every CU to have eight, each with four
-// pieces a thread at least.
+// Rows up to this many pieces are short: one wave reads them in four loads.
+constexpr int32_t SHORT = 256;
+
+// Rows are cut where they are so few that one workgroup would take longer over
+// its row than the second launch does, and so long that every part has work.
 parts_t parts_of(snack_dtype dt, int64_t Tn, int32_t V) {
   const int32_t e = dt == SNACK_BF16 ? 8 : 4;
-  const int64_t least = 1024 * e;
-  int64_t parts = std::min<int64_t>(cdiv(2048, std::max<int64_t>(Tn, 1)), cdiv(V, least));
-  if (Tn >= 1024) parts = 1;
-  const int64_t each = cdiv(cdiv(V, std::max<int64_t>(parts, 1)), 256 * e) * 256 * e;
-  return {(int32_t)std::max<int64_t>(1, cdiv(V, each)), (int32_t)each};
+  const int64_t pieces = cdiv(V, e);
+  int64_t parts = 1;
+  if (pieces > 32768) parts = std::min<int64_t>(cdiv(1024, std::max<int64_t>(Tn, 1)), pieces / 2048);
+  const int64_t each = cdiv(cdiv(V, parts), 256 * e) * 256 * e;
+  return {(int32_t)std::max<int64_t>(1, cdiv(V, each)), (int32_t)std::min<int64_t>(each, INT32_MAX)};
 }
 
 snack_status check_logp(snack_dtype dt, int32_t id_bytes, int64_t Tn, int32_t V, int64_t ld) {
@@ -199,8 +234,12 @@ snack_status check_logp(snack_dtype dt, int32_t id_bytes, int64_t Tn, int32_t V,
 template <typename T>
 void run_fwd(const T* x, int64_t ldx, int64_t Tn, int32_t V, ids_t ids, float* logp, float2* norm,
              float2* part, parts_t p, hipStream_t s) {
-  hipLaunchKernelGGL(k_logp<T>, dim3((unsigned)(Tn * p.parts)), dim3(256), 0, s, x, ldx, V, ids,
-                     p.parts, p.each, logp, norm, part);
+  const int64_t pieces = cdiv(V, EL<T>);
+  const int W = pieces <= SHORT ? 1 : Tn * p.parts < 1024 ? 16 : 4;
+  auto kernel = W == 1 ? k_logp<T, 1> : W == 4 ? k_logp<T, 4> : k_logp<T, 16>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(W == 1 ? cdiv(Tn, 4) : Tn * p.parts)),
+                     dim3(W == 16 ? 1024 : 256), 0, s, x, ldx, Tn, V, ids, p.parts, p.each, logp,
+                     norm, part);
   if (p.parts > 1)
     hipLaunchKernelGGL(k_logp_join<T>, dim3((unsigned)Tn), dim3(64), 0, s, x, ldx, V, ids, p.parts,
                        part, logp, norm);
@@ -209,9 +248,13 @@ void run_fwd(const T* x, int64_t ldx, int64_t Tn, int32_t V, ids_t ids, float* l
 template <typename T>
 void run_bwd(const T* x, int64_t ldx, int64_t Tn, int32_t V, ids_t ids, const float* dlogp,
              const float2* norm, T* dx, int64_t lddx, hipStream_t s) {
-  const int64_t blocks = cdiv(V, 1024 * EL<T>);
-  hipLaunchKernelGGL(k_logp_grad<T>, dim3((unsigned)(Tn * blocks)), dim3(256), 0, s, x, ldx, V,
-                     ids, dlogp, norm, dx, lddx, (uint32_t)blocks);
+  const int64_t pieces = cdiv(V, EL<T>), blocks = cdiv(pieces, 1024);
+  if (pieces <= 2 * SHORT && Tn * pieces <= MAX_PIECES)
+    hipLaunchKernelGGL(k_logp_grad_short<T>, dim3((unsigned)cdiv(Tn * pieces, 256)), dim3(256), 0, s,
+                       x, ldx, Tn, V, ids, dlogp, norm, dx, lddx, (uint32_t)pieces);
+  else
+    hipLaunchKernelGGL(k_logp_grad<T>, dim3((unsigned)(Tn * blocks)), dim3(256), 0, s, x, ldx, V,
+                       ids, dlogp, norm, dx, lddx, (uint32_t)blocks);
 }
 
 }  // namespace
