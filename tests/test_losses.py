@@ -84,7 +84,7 @@ def preference(d, beta, eps, form, average, ref, mask, up=1.0):
 
 
 BATCHES = [(2, 0), (2, 1), (2, 7), (4, 64), (6, 1000), (16, 4097), (256, 8192), (258, 8192),
-           (20, 8193), (2, 30000), (514, 100003), (3000, 9000)]
+           (20, 8193), (2, 30000), (514, 100003), (3000, 9000), (9000, 30011)]
 
 
 @gpu

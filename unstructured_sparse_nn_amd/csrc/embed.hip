@@ -190,11 +190,15 @@ __global__ __launch_bounds__(W * 64) void k_embed_sort(const I* __restrict__ ids
   }
   __syncthreads();
   auto put = [&](bool in, int32_t row, int32_t token) {
-    uint64_t same = __ballot(in);  // lanes of the same row
-    for (int32_t k = 0; k < bits; ++k) {
-      const bool bit = (row >> k) & 1;
-      const uint64_t set = __ballot(bit);
-      same &= bit ? set : ~set;
+    // lanes of the same row: all, where one token fills a text, or bit by bit
+    uint64_t same = __ballot(in);
+    const int32_t one = __shfl(row, __ffsll((unsigned long long)same) - 1);
+    if (__ballot(in && row != one)) {
+      for (int32_t k = 0; k < bits; ++k) {
+        const bool bit = (row >> k) & 1;
+        const uint64_t set = __ballot(bit);
+        same &= bit ? set : ~set;
+      }
     }
     int32_t to = 0;
     const int32_t before = (int32_t)__popcll(same & lanemask_lt());
@@ -227,26 +231,33 @@ __global__ __launch_bounds__(W * 64) void k_embed_sort(const I* __restrict__ ids
 }
 
 // ---------------------------------------------------------------------- sums
-// The sum of the tokens of places [k, end), RUN at most, at cut c.
+// The tokens of RUN places.
+struct run_t { int32_t token[RUN]; };
+__device__ __forceinline__ run_t load_run(const sum_arg& a, int64_t k) {
+  run_t r;
+  __builtin_memcpy(r.token, a.tokens + k, sizeof(r.token));
+  return r;
+}
+
+// The sum of the first n <= RUN of them, at cut c: half of them loaded at once.
 template <typename T>
-__device__ __forceinline__ void sum_tokens(const sum_arg& a, int32_t k, int32_t end, cut_t c,
-                                           float (&acc)[EL<T>]) {
+__device__ __forceinline__ void sum_run(const sum_arg& a, const run_t& r, int32_t n, cut_t c,
+                                        float (&acc)[EL<T>]) {
   constexpr int U = RUN / 2;
   const T* dY = (const T*)a.dY;
-#pragma unroll 1
-  for (; k < end; k += U) {
+#pragma unroll
+  for (int h = 0; h < RUN; h += U) {
+    if (h >= n) break;
     frag<T> f[U];
-    int32_t tok[U];
-    __builtin_memcpy(tok, a.tokens + k, sizeof(tok));
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      f[u] = load_cut(dY + (int64_t)(k + u < end ? tok[u] : tok[0]) * a.lddy, c, a.D);
+      f[u] = load_cut(dY + (int64_t)(h + u < n ? r.token[h + u] : r.token[0]) * a.lddy, c, a.D);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float v[EL<T>];
       floats_of(f[u], v);
 #pragma unroll
-      for (int e = 0; e < EL<T>; ++e) acc[e] += k + u < end ? v[e] : 0.f;
+      for (int e = 0; e < EL<T>; ++e) acc[e] += h + u < n ? v[e] : 0.f;
     }
   }
 }
@@ -254,7 +265,8 @@ __device__ __forceinline__ void sum_tokens(const sum_arg& a, int32_t k, int32_t 
 // Workgroups up to `sums` take the places at which a table row begins; up to
 // `pieces` the pieces of rows of more than RUN tokens: of each RUN places those of
 // such a row that began before (slot 0) and of one that begins there (slot 1; it
-// goes on past them, so there is one at most); the others the rows without a token.
+// goes on past them, so there is one at most); the others the rows without a token,
+// whose stores fill the sums' trips to memory.
 template <typename T>
 __global__ __launch_bounds__(256) void k_embed_sum(sum_arg a, int32_t Tn, uint32_t sums,
                                                    uint32_t pieces) {
@@ -265,10 +277,11 @@ __global__ __launch_bounds__(256) void k_embed_sum(sum_arg a, int32_t Tn, uint32
     const int32_t k = (int32_t)(g / a.per);
     if (k >= Tn) return;
     const place_t p = a.order[k];
+    const run_t r = load_run(a, k);
     if (p.begin != k || p.end - k > RUN) return;
     const cut_t c = cut_of<T>((int32_t)(g % a.per), a.D);
     const frag<T> base = load_base<T>(a, p.row, c);
-    sum_tokens<T>(a, k, p.end, c, acc);
+    sum_run<T>(a, r, p.end - k, c, acc);
     store_row(a, p.row, c, with_base(a, base, acc));
     return;
   }
@@ -277,12 +290,12 @@ __global__ __launch_bounds__(256) void k_embed_sum(sum_arg a, int32_t Tn, uint32
     const uint32_t slot = g / a.per, q = g % a.per;
     const int64_t from = (int64_t)(slot / 2) * RUN;
     if (from >= Tn) return;
-    // a row of more than RUN places that ends past the last whole piece has slot 0
     const int64_t last = min(from + RUN, (int64_t)Tn) - 1;
     const place_t p = a.order[slot & 1 ? last : from];
     if (p.begin < 0 || p.end - p.begin <= RUN || (p.begin < from) == (slot & 1)) return;
-    sum_tokens<T>(a, max(p.begin, (int32_t)from), (int32_t)min((int64_t)p.end, from + RUN),
-                  cut_of<T>((int32_t)q, a.D), acc);
+    const int64_t k = max((int64_t)p.begin, from);
+    sum_run<T>(a, load_run(a, k), (int32_t)(min((int64_t)p.end, from + RUN) - k),
+               cut_of<T>((int32_t)q, a.D), acc);
     float* part = a.part + ((int64_t)slot * a.per + q) * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) part[e] = acc[e];
@@ -295,35 +308,37 @@ __global__ __launch_bounds__(256) void k_embed_sum(sum_arg a, int32_t Tn, uint32
   store_row(a, v, c, load_base<T>(a, v, c));
 }
 
-// Rows of more than RUN tokens: those that begin in the JOIN pieces of this
-// workgroup, 64 of the row's columns' pieces; the waves add consecutive shares of
-// a row's slots.
-constexpr int32_t JOIN = 16;
-constexpr int JOIN_WAVES = 16;
+// Rows of more than RUN tokens: workgroup (tiles, slab) takes those that begin in
+// JOIN pieces of the order, SLAB pieces of their columns; groups of SLAB lanes add
+// consecutive shares of a row's slots.
+constexpr int32_t JOIN = 4;
+constexpr int JOIN_THREADS = 256, SLAB = 16;
 
 template <typename T>
-__global__ __launch_bounds__(JOIN_WAVES * 64) void k_embed_join(sum_arg a, int32_t Tn) {
-  constexpr int E = EL<T>;
-  __shared__ float lds[JOIN_WAVES][64][E + 1];
-  const int w = threadIdx.x / 64, lane = lane_id();
-  const int64_t from = ((int64_t)blockIdx.x * JOIN + lane) * RUN;
+__global__ __launch_bounds__(JOIN_THREADS) void k_embed_join(sum_arg a, int32_t Tn,
+                                                             uint32_t slabs) {
+  constexpr int E = EL<T>, GROUPS = JOIN_THREADS / SLAB, WAVES = JOIN_THREADS / 64;
+  __shared__ float lds[WAVES][SLAB * E + 1];
+  const int lane = lane_id(), group = threadIdx.x / SLAB, col = threadIdx.x % SLAB;
+  const int32_t tiles = (int32_t)(blockIdx.x / slabs) * JOIN;
+  const int64_t from = ((int64_t)tiles + lane) * RUN;
   place_t at{0, 0, 0, 0};
   if (lane < JOIN && from < Tn) at = a.order[min(from + RUN, (int64_t)Tn) - 1];
-  uint64_t todo = __ballot(at.end - at.begin > RUN && at.begin >= from);
-  const uint32_t q = blockIdx.y * 64 + lane;
-  for (; todo; todo &= todo - 1) {
+  const uint32_t q = blockIdx.x % slabs * SLAB + col;
+  for (uint64_t todo = __ballot(at.end - at.begin > RUN && at.begin >= from); todo;
+       todo &= todo - 1) {
     const int l = __ffsll((unsigned long long)todo) - 1;
-    const int32_t tile = blockIdx.x * JOIN + l, row = __shfl(at.row, l);
+    const int32_t tile = tiles + l, row = __shfl(at.row, l);
     // slots: this piece's second, the others' first
     const int32_t n = (__shfl(at.end, l) - 1) / RUN - tile + 1;
     const cut_t c = cut_of<T>((int32_t)min(q, a.per - 1), a.D);
     frag<T> base{};
     float acc[E] = {};
     if (q < a.per) {
-      if (w == 0) base = load_base<T>(a, row, c);
-      const int32_t j1 = (int32_t)((int64_t)n * (w + 1) / JOIN_WAVES);
+      if (group == 0) base = load_base<T>(a, row, c);
+      const int32_t j1 = (int32_t)((int64_t)n * (group + 1) / GROUPS);
 #pragma unroll 8
-      for (int32_t j = (int32_t)((int64_t)n * w / JOIN_WAVES); j < j1; ++j) {
+      for (int32_t j = (int32_t)((int64_t)n * group / GROUPS); j < j1; ++j) {
         const int64_t slot = 2ll * (tile + j) + (j == 0);
         const float* p = a.part + (slot * a.per + q) * E;
 #pragma unroll
@@ -331,13 +346,17 @@ __global__ __launch_bounds__(JOIN_WAVES * 64) void k_embed_join(sum_arg a, int32
       }
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) lds[w][lane][e] = acc[e];
+    for (int e = 0; e < E; ++e) {
+#pragma unroll
+      for (int d = SLAB; d < 64; d <<= 1) acc[e] += __shfl_xor(acc[e], d);
+      if (lane < SLAB) lds[threadIdx.x / 64][col * E + e] = acc[e];
+    }
     __syncthreads();
-    if (w == 0 && q < a.per) {
+    if (group == 0 && q < a.per) {
 #pragma unroll
-      for (int k = 1; k < JOIN_WAVES; ++k)
+      for (int k = 1; k < WAVES; ++k)
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += lds[k][lane][e];
+        for (int e = 0; e < E; ++e) acc[e] += lds[k][col * E + e];
       store_row(a, row, c, with_base(a, base, acc));
     }
     __syncthreads();
@@ -345,7 +364,7 @@ __global__ __launch_bounds__(JOIN_WAVES * 64) void k_embed_join(sum_arg a, int32
 }
 
 struct plan_t {
-  int64_t per, tiles;  // tiles: 0 if no row can have more than RUN tokens
+  int64_t per, tiles;  // pieces of a row; of the order, if a row can have more than RUN tokens
   int32_t range, waves;
   size_t order, tokens, used, part, total;
 };
@@ -371,6 +390,10 @@ plan_t plan_of(snack_dtype dt, int64_t Tn, int32_t V, int32_t D) {
   return p;
 }
 
+int64_t joins_of(int64_t Tn, int64_t per) {
+  return Tn > RUN ? cdiv(cdiv(Tn, RUN), JOIN) * cdiv(per, SLAB) : 0;
+}
+
 snack_status check_embed(snack_dtype dt, int32_t id_bytes, int64_t Tn, int32_t V, int32_t D) {
   if (dt != SNACK_F32 && dt != SNACK_BF16) return SNACK_E_DTYPE;
   if (id_bytes != 4 && id_bytes != 8) return SNACK_E_DTYPE;
@@ -378,8 +401,7 @@ snack_status check_embed(snack_dtype dt, int32_t id_bytes, int64_t Tn, int32_t V
   // what a launch of each kernel holds
   const int64_t per = cdiv(D, dt == SNACK_BF16 ? 8 : 4);
   if (Tn > MAX_TOKENS || V > MAX_ROWS || D > MAX_FEATURES) return SNACK_E_OVERFLOW;
-  if (per > 0 && V + Tn + Tn / (RUN / 2) + 4 > MAX_PIECES / per)
-    return SNACK_E_OVERFLOW;
+  if (per > 0 && V + Tn + Tn / (RUN / 2) + 4 > MAX_PIECES / per) return SNACK_E_OVERFLOW;
   return SNACK_OK;
 }
 
@@ -404,9 +426,8 @@ void run_bwd(ids_t ids, int32_t Tn, const plan_t& p, const sum_arg& a, hipStream
     hipLaunchKernelGGL(k_embed_sum<T>, dim3((unsigned)blocks), dim3(256), 0, s, a, Tn,
                        (uint32_t)sums, (uint32_t)pieces);
   if (p.tiles > 0)
-    hipLaunchKernelGGL(k_embed_join<T>,
-                       dim3((unsigned)cdiv(p.tiles, JOIN), (unsigned)cdiv(p.per, 64)),
-                       dim3(JOIN_WAVES * 64), 0, s, a, Tn);
+    hipLaunchKernelGGL(k_embed_join<T>, dim3((unsigned)joins_of(Tn, p.per)), dim3(JOIN_THREADS), 0,
+                       s, a, Tn, (uint32_t)cdiv(p.per, SLAB));
 }
 
 }  // namespace

@@ -30,9 +30,11 @@ __device__ __forceinline__ soft_t join(soft_t a, soft_t b) {
   const float m = fmaxf(a.m, b.m);
   return {m, a.s * exp_of(a.m - m) + b.s * exp_of(b.m - m)};
 }
-__device__ __forceinline__ soft_t wave_join(soft_t a) {
+// Of each N lanes.
+template <int N>
+__device__ __forceinline__ soft_t lanes_join(soft_t a) {
 #pragma unroll
-  for (int d = 32; d; d >>= 1)
+  for (int d = N / 2; d; d >>= 1)
     a = join(a, soft_t{__shfl_xor(a.m, d), __shfl_xor(a.s, d)});
   return a;
 }
@@ -88,18 +90,17 @@ __device__ __forceinline__ void put_logp(soft_t a, float x, int32_t t, int64_t i
   norm[i] = make_float2(a.m, l);
 }
 
-// W waves for part c of row i; with one part a row it ends there.  Workgroups
-// have 4 waves at least.
-template <typename T, int W>
-__global__ __launch_bounds__(W < 4 ? 256 : W * 64) void k_logp(
+// N threads for part c of row i; with one part a row it ends there.  Workgroups
+// have 256 threads at least.
+template <typename T, int N>
+__global__ __launch_bounds__(N < 256 ? 256 : N) void k_logp(
     const T* __restrict__ x, int64_t ldx, int64_t Tn, int32_t V, ids_t ids, int32_t parts,
     int32_t each, float* __restrict__ logp, float2* __restrict__ norm, float2* __restrict__ part) {
-  constexpr int ROWS = W < 4 ? 4 / W : 1;  // of a workgroup
-  __shared__ soft_t lds[W];
-  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
-  const int64_t i = blockIdx.x / parts * (int64_t)ROWS + w / W;
-  if (W < 4 && i >= Tn) return;
-  const int32_t c = blockIdx.x % parts, t = threadIdx.x % (W * 64);
+  constexpr int ROWS = N < 256 ? 256 / N : 1;  // of a workgroup
+  int64_t i = blockIdx.x / parts * (int64_t)ROWS + threadIdx.x / N;
+  const bool mine = i < Tn;
+  if (!mine) i = Tn - 1;  // the wave's other rows need its lanes
+  const int32_t c = blockIdx.x % parts, t = threadIdx.x % N;
   const T* row = x + i * ldx;
   int32_t target = 0;
   float xt = 0.f;
@@ -107,14 +108,17 @@ __global__ __launch_bounds__(W < 4 ? 256 : W * 64) void k_logp(
     target = ids.get(i, V);
     if (target >= 0) xt = elem<T>::to_f(row[target]);
   }
-  soft_t a = wave_join(soft_of<W * 64>(row + (int64_t)c * each, min(each, V - c * each), t));
-  if constexpr (W > 1) {
-    if (t % 64 == 0) lds[w] = a;
+  soft_t a = lanes_join<(N < 64 ? N : 64)>(
+      soft_of<N>(row + (int64_t)c * each, min(each, V - c * each), t));
+  if constexpr (N > 64) {
+    constexpr int W = N / 64;
+    __shared__ soft_t lds[W];
+    if (t % 64 == 0) lds[t / 64] = a;
     __syncthreads();
-    if (w != 0) return;
-    a = wave_join(t < W ? lds[t] : soft_t{LOWEST, 0.f});
+    if (t >= 64) return;
+    a = lanes_join<64>(t < W ? lds[t] : soft_t{LOWEST, 0.f});
   }
-  if (t != 0) return;
+  if (t != 0 || !mine) return;
   if (parts == 1) put_logp(a, xt, target, i, logp, norm);
   else part[blockIdx.x] = make_float2(a.m, a.s);
 }
@@ -134,7 +138,7 @@ __global__ __launch_bounds__(64) void k_logp_join(const T* __restrict__ x, int64
     const float2 p = part[i * parts + c];
     a = join(a, soft_t{p.x, p.y});
   }
-  a = wave_join(a);
+  a = lanes_join<64>(a);
   if (lane_id() == 0) put_logp(a, xt, t, i, logp, norm);
 }
 
@@ -209,13 +213,16 @@ struct parts_t { int32_t parts, each; };
 // Rows up to this many pieces are short: one wave reads them in four loads.
 constexpr int32_t SHORT = 256;
 
-// Rows are cut where they are so few that one workgroup would take longer over
-// its row than the second launch does, and so long that every part has work.
+// A workgroup of 16 waves takes 3 us and 1 us more for every 22,000 of its row's
+// logits (their exponentials, four a cycle): rows of more than CUT are cut where
+// they leave CUs idle, although adding the parts is a launch more (one row of
+// 128,000: 9.0 us whole, 5.7 us in 16 parts; of 32,000: 4.9 us whole).
+constexpr int32_t CUT = 49152;
 parts_t parts_of(snack_dtype dt, int64_t Tn, int32_t V) {
   const int32_t e = dt == SNACK_BF16 ? 8 : 4;
-  const int64_t pieces = cdiv(V, e);
   int64_t parts = 1;
-  if (pieces > 32768) parts = std::min<int64_t>(cdiv(1024, std::max<int64_t>(Tn, 1)), pieces / 2048);
+  if (V > CUT && Tn < 256)
+    parts = std::min<int64_t>(cdiv(512, std::max<int64_t>(Tn, 1)), V / 8192);
   const int64_t each = cdiv(cdiv(V, parts), 256 * e) * 256 * e;
   return {(int32_t)std::max<int64_t>(1, cdiv(V, each)), (int32_t)std::min<int64_t>(each, INT32_MAX)};
 }
@@ -235,11 +242,15 @@ template <typename T>
 void run_fwd(const T* x, int64_t ldx, int64_t Tn, int32_t V, ids_t ids, float* logp, float2* norm,
              float2* part, parts_t p, hipStream_t s) {
   const int64_t pieces = cdiv(V, EL<T>);
-  const int W = pieces <= SHORT ? 1 : Tn * p.parts < 1024 ? 16 : 4;
-  auto kernel = W == 1 ? k_logp<T, 1> : W == 4 ? k_logp<T, 4> : k_logp<T, 16>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(W == 1 ? cdiv(Tn, 4) : Tn * p.parts)),
-                     dim3(W == 16 ? 1024 : 256), 0, s, x, ldx, Tn, V, ids, p.parts, p.each, logp,
-                     norm, part);
+  // up to four pieces a thread, and 16 waves where rows are few: one wave a row of
+  // 300 logits, 16,384 of them, 9.3 us, 16 lanes 6 us; 900 rows of 32,000 logits 4 waves
+  // 22 us, 16 waves 15 us
+  const int N = pieces <= SHORT / 4 ? 16 : pieces <= SHORT ? 64 : p.parts == 1 && Tn < 1024 ? 1024 : 256;
+  auto kernel = N == 16 ? k_logp<T, 16> : N == 64 ? k_logp<T, 64> : N == 256 ? k_logp<T, 256>
+                                                                            : k_logp<T, 1024>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(N < 256 ? cdiv(Tn * N, 256) : Tn * p.parts)),
+                     dim3(std::max(N, 256)), 0, s, x, ldx, Tn, V, ids, p.parts, p.each, logp, norm,
+                     part);
   if (p.parts > 1)
     hipLaunchKernelGGL(k_logp_join<T>, dim3((unsigned)Tn), dim3(64), 0, s, x, ldx, V, ids, p.parts,
                        part, logp, norm);

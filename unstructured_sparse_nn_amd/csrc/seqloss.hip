@@ -59,7 +59,10 @@ __device__ __forceinline__ int32_t first_item(const batch_t& q, int32_t i, int32
   return (start >> q.log_p) + i;
 }
 
-struct item_t { int32_t seq, a, b; };  // its sequence, and its tokens
+struct item_t {
+  int32_t seq, from, end;  // its sequence, and that one's tokens
+  int32_t a, b;            // its tokens
+};
 
 // Item x of the sequence that begins at a; items before the first sequence's or
 // past the last one's have no tokens.
@@ -68,7 +71,7 @@ __device__ __forceinline__ item_t item_at(const batch_t& q, int32_t x, int32_t s
   const int32_t b = max(next, a), x0 = first_item(q, seq, a);
   int64_t from = b;
   if (x >= x0) from = a + ((int64_t)(x - x0) << q.log_p);
-  return {seq, (int32_t)min(from, (int64_t)b),
+  return {seq, a, b, (int32_t)min(from, (int64_t)b),
           (int32_t)min(from + (1 << q.log_p), (int64_t)b)};
 }
 
@@ -118,7 +121,7 @@ __device__ __forceinline__ sums_t wave_sum(const sums_t& s) {
 struct pref_t {
   static constexpr bool POLICY = false;
   const float *logps, *ref;
-  double beta, eps;
+  double beta, eps, share;  // share: of a pair in the loss
   int32_t form, average;
 
   struct in_t { float lp, ref; };
@@ -141,7 +144,7 @@ struct pref_t {
       return u * u;
     }
     const double t = exp(-fabs(z)), soft = log1p(t);  // log(1 + exp(z)) = soft + max(z, 0)
-    const double up = 1.0 / (1.0 + t), down = t / (1.0 + t);
+    const double up = 1.0 / (1.0 + t), down = t * up;
     const double sig = z >= 0 ? up : down, not_sig = z >= 0 ? down : up;
     *dh = beta * (eps * sig - (1.0 - eps) * not_sig);
     const double a = (1.0 - eps) * (soft + fmax(-z, 0.0)), b = eps * (soft + fmax(z, 0.0));
@@ -271,10 +274,10 @@ __device__ __forceinline__ void write_outside(const batch_t& q, float* grad, int
   for (int64_t i = b + first; i < q.T; i += step) grad[i] = 0.f;
 }
 
-// A pair's loss; rewards and the two coefficients.
-__device__ __forceinline__ double finish_pair(const batch_t& q, const pref_t& loss,
-                                              const sums_t& x, const sums_t& y, int32_t p,
-                                              const out_t& out, double* coef) {
+// A pair's part of the loss; rewards and the two coefficients.
+__device__ __forceinline__ double finish_pair(const pref_t& loss, const sums_t& x,
+                                              const sums_t& y, int32_t p, const out_t& out,
+                                              double* coef) {
   const double px = loss.per(x), py = loss.per(y), dx = x.f * px, dy = y.f * py;
   double dh;
   const double f = loss.pair(dx - dy, &dh);
@@ -282,10 +285,10 @@ __device__ __forceinline__ double finish_pair(const batch_t& q, const pref_t& lo
     out.more[2 * p] = (float)(loss.beta * dx);
     out.more[2 * p + 1] = (float)(loss.beta * dy);
   }
-  dh *= upstream(out) / (double)(q.S / 2);
+  dh *= upstream(out) * loss.share;
   coef[2 * p] = dh * px;
   coef[2 * p + 1] = -dh * py;
-  return f;
+  return f * loss.share;
 }
 __device__ __forceinline__ void finish_stats(const sums_t& all, const out_t& out) {
   const double n = fmax(all.n, 1.0);
@@ -295,7 +298,7 @@ __device__ __forceinline__ void finish_stats(const sums_t& all, const out_t& out
 // ------------------------------------------------------- one workgroup, one launch
 constexpr int SMALL_WAVES = 16;
 constexpr int32_t SMALL_LOG_P = 7, SMALL_SEQS = 127;
-constexpr int SMALL_EACH = 4;  // items of a wave
+constexpr int SMALL_EACH = 2;  // items of a wave
 
 // The starts of all sequences, two a lane.
 struct starts_t {
@@ -321,7 +324,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void k_seq_small(batch_t q, L los
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int32_t x = k * SMALL_WAVES + w;
-    it[k] = {0, 0, 0};
+    it[k] = {};
     if (x >= q.items) continue;
     const int32_t found = (int32_t)__popcll(__ballot(lane < q.S && first_lo <= x)) +
                           (int32_t)__popcll(__ballot(64 + lane < q.S && first_hi <= x));
@@ -349,6 +352,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void k_seq_small(batch_t q, L los
       const int32_t a = st.at(i), b = max(st.at(i + 1), a);
       const int32_t x1 = min(first_item(q, i + 1, b), q.items);
       sums_t s{0, 0, 0, 0};
+#pragma unroll 4
       for (int32_t x = first_item(q, i, a); x < x1; ++x) s = s + sums[x];
       return s;
     };
@@ -356,9 +360,9 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void k_seq_small(batch_t q, L los
       const int32_t pairs = q.S / 2, p = min(lane, max(pairs - 1, 0));
       if (pairs > 0) {
         const sums_t x = total(2 * p), y = total(2 * p + 1);
-        if (lane < pairs) f = finish_pair(q, loss, x, y, p, out, coef);
+        if (lane < pairs) f = finish_pair(loss, x, y, p, out, coef);
       }
-      f = wave_sum(f) / (double)max(pairs, 1);
+      f = wave_sum(f);
     } else {
       sums_t all{0, 0, 0, 0};
       for (int32_t x = lane; x < q.items; x += 64) all = all + sums[x];
@@ -411,22 +415,36 @@ __device__ __forceinline__ sums_t block_sum(sums_t s, sums_t* lds) {
   return s;
 }
 
+// K items a wave, whose trips to memory overlap.  table: what k_pref_grads needs of
+// an item.
+struct __attribute__((aligned(16))) slot_t { int32_t seq, a, b, zero; };
+
+template <int K>
 __global__ __launch_bounds__(256) void k_pref_sums(batch_t q, pref_t loss,
                                                    sums_t* __restrict__ sums,
-                                                   item_t* __restrict__ items) {
+                                                   slot_t* __restrict__ table) {
   constexpr int U = 1 << (LOG_P - 6);
-  const int32_t x = blockIdx.x * 4 + wave_of_block();
-  if (x >= q.items) return;
-  const item_t it = item_of(q, x);
-  sums_t s{0, 0, 0, 0};
-  if (it.a < it.b) {
-    tokens_t<pref_t, U> t;
-    float g[U];
-    t.load(q, loss, it, it.a);
-    t.add(loss, s, g);
-    wave_totals<pref_t>(s);
+  item_t it[K];
+  tokens_t<pref_t, U> t[K];
+  const int32_t first = blockIdx.x * (4 * K) + wave_of_block();
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    it[k] = first + 4 * k < q.items ? item_of(q, first + 4 * k) : item_t{};
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (it[k].a < it[k].b) t[k].load(q, loss, it[k], it[k].a);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int32_t x = first + 4 * k;
+    if (x >= q.items) return;
+    sums_t s{0, 0, 0, 0};
+    if (it[k].a < it[k].b) {
+      float g[U];
+      t[k].add(loss, s, g);
+      wave_totals<pref_t>(s);
+    }
+    if (lane_id() == 0) sums[x] = s, table[x] = slot_t{it[k].seq, it[k].a, it[k].b, 0};
   }
-  if (lane_id() == 0) sums[x] = s, items[x] = it;
 }
 
 __device__ __forceinline__ sums_t range_sums(const sums_t* __restrict__ sums, range_t r) {
@@ -444,12 +462,13 @@ __global__ __launch_bounds__(256) void k_pref_finish(batch_t q, pref_t loss,
   if (p >= q.S / 2) return;
   const sums_t x = range_sums(sums, items_of(q, 2 * p)),
                y = range_sums(sums, items_of(q, 2 * p + 1));
-  if (lane_id() == 0) terms[p] = finish_pair(q, loss, x, y, p, out, coef) / (double)(q.S / 2);
+  if (lane_id() == 0) terms[p] = finish_pair(loss, x, y, p, out, coef);
 }
 
 // The first workgroup adds the loss's terms, if it is wanted; the others write
 // gradients.
-__global__ __launch_bounds__(256) void k_pref_grads(batch_t q, const item_t* __restrict__ items,
+template <int K>
+__global__ __launch_bounds__(256) void k_pref_grads(batch_t q, const slot_t* __restrict__ table,
                                                     const double* __restrict__ coef,
                                                     const double* __restrict__ terms,
                                                     float* __restrict__ loss,
@@ -466,24 +485,30 @@ __global__ __launch_bounds__(256) void k_pref_grads(batch_t q, const item_t* __r
     return;
   }
   const int32_t b = blockIdx.x - with_loss, lane = lane_id();
-  const int32_t x = b * 4 + wave_of_block();
-  if (x < q.items) {
-    const item_t it = items[x];
-    if (it.a < it.b) {
-      const float c = (float)coef[it.seq];
-      bool counts[U];
+  const int32_t first = b * (4 * K) + wave_of_block();
+  slot_t it[K];
+  bool counts[K][U];
+  float c[K];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int32_t at = it.a + u * 64 + lane;
-        counts[u] = q.mask ? q.mask[at < it.b ? at : it.a] != 0 : true;
-      }
+  for (int k = 0; k < K; ++k)
+    it[k] = first + 4 * k < q.items ? table[first + 4 * k] : slot_t{0, 0, 0, 0};
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int32_t at = it.a + u * 64 + lane;
-        if (at < it.b) grad[at] = counts[u] ? c : 0.f;
-      }
+  for (int k = 0; k < K; ++k) {
+    if (it[k].a >= it[k].b) continue;
+    c[k] = (float)coef[it[k].seq];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int32_t at = it[k].a + u * 64 + lane;
+      counts[k][u] = q.mask ? q.mask[at < it[k].b ? at : it[k].a] != 0 : true;
     }
   }
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int32_t at = it[k].a + u * 64 + lane;
+      if (at < it[k].b) grad[at] = counts[k][u] ? c[k] : 0.f;
+    }
   write_outside(q, grad, (int64_t)b * 256 + threadIdx.x,
                 ((int64_t)gridDim.x - with_loss) * 256);
 }
@@ -540,7 +565,7 @@ __global__ __launch_bounds__(256) void k_policy(batch_t q, policy_t loss, out_t 
   __shared__ int32_t ones[4];
   const int32_t w = wave_of_block(), lane = lane_id(), x = blockIdx.x * 4 + w;
   const bool mine = x < q.items;
-  item_t it{0, 0, 0};
+  item_t it{};
   if (mine) it = item_of(q, x);
   tokens_t<policy_t, U> t;
   if (it.a < it.b) t.load(q, loss, it, it.a);
@@ -563,16 +588,15 @@ __global__ __launch_bounds__(256) void k_policy(batch_t q, policy_t loss, out_t 
       n = (double)(ones[0] + ones[1] + ones[2] + ones[3]);
     }
   } else if (it.a < it.b) {
-    const int32_t a = start_of(q, it.seq), b = max(start_of(q, it.seq + 1), a);
     if (!q.mask) {
-      n = (double)(b - a);
+      n = (double)(it.end - it.from);
     } else {
       int32_t part = 0;
       if (counts) {
-        const int32_t x1 = min(first_item(q, it.seq + 1, b), q.items);
-        for (int32_t i = first_item(q, it.seq, a) + lane; i < x1; i += 64) part += counts[i];
+        const int32_t x1 = min(first_item(q, it.seq + 1, it.end), q.items);
+        for (int32_t i = first_item(q, it.seq, it.from) + lane; i < x1; i += 64) part += counts[i];
       } else {
-        part = count_bytes(q.mask, a, b, lane, 64);
+        part = count_bytes(q.mask, it.from, it.end, lane, 64);
       }
       n = (double)wave_sum(part);
     }
@@ -597,13 +621,14 @@ __global__ __launch_bounds__(256) void k_policy(batch_t q, policy_t loss, out_t 
     write_outside(q, out.grad, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
-__global__ __launch_bounds__(1024) void k_policy_finish(const sums_t* __restrict__ sums,
-                                                        int32_t n, out_t out) {
-  __shared__ sums_t lds[16];
+template <int W>
+__global__ __launch_bounds__(W * 64) void k_policy_finish(const sums_t* __restrict__ sums,
+                                                          int32_t n, out_t out) {
+  __shared__ sums_t lds[W];
   sums_t s{0, 0, 0, 0};
 #pragma unroll 4
-  for (int32_t i = threadIdx.x; i < n; i += 1024) s = s + sums[i];
-  s = block_sum<16>(s, lds);
+  for (int32_t i = threadIdx.x; i < n; i += W * 64) s = s + sums[i];
+  s = block_sum<W>(s, lds);
   if (threadIdx.x != 0) return;
   finish_stats(s, out);
   if (out.loss) *out.loss = (float)s.f;
@@ -643,7 +668,7 @@ plan_t plan_of(int32_t S, int32_t Tn, bool policy) {
     p.counts = take((size_t)p.items * 4);
     p.totals = take((size_t)p.blocks * 4);
   } else {
-    p.table = take((size_t)p.items * sizeof(item_t));
+    p.table = take((size_t)p.items * sizeof(slot_t));
     p.coef = take((size_t)S * sizeof(double));
     p.terms = take((size_t)S / 2 * sizeof(double));
   }
@@ -679,17 +704,22 @@ snack_status run(const snack_seqs* b, const plan_t& p, const L& loss, const out_
     hipLaunchKernelGGL(kernel, dim3(p.blocks), dim3(256), 0, s, q, loss, out, counts, totals,
                        p.blocks, sums);
     if (out.loss || out.more)
-      hipLaunchKernelGGL(k_policy_finish, dim3(1), dim3(1024), 0, s, sums, p.blocks, out);
+      hipLaunchKernelGGL(p.blocks <= 512 ? k_policy_finish<2> : k_policy_finish<16>, dim3(1),
+                         dim3(p.blocks <= 512 ? 128 : 1024), 0, s, sums, p.blocks, out);
   } else {
-    item_t* table = (item_t*)(w + p.table);
+    slot_t* table = (slot_t*)(w + p.table);
     double *coef = (double*)(w + p.coef), *terms = (double*)(w + p.terms);
-    hipLaunchKernelGGL(k_pref_sums, dim3(p.blocks), dim3(256), 0, s, q, loss, sums, table);
+    // two items a wave once the card has no place for a wave each
+    const int K = p.items > 8192 ? 2 : 1;
+    const int32_t groups = (int32_t)cdiv(p.items, 4 * K);
+    hipLaunchKernelGGL(K == 2 ? k_pref_sums<2> : k_pref_sums<1>, dim3(groups), dim3(256), 0, s, q,
+                       loss, sums, table);
     hipLaunchKernelGGL(k_pref_finish, dim3((unsigned)cdiv(b->S / 2, 4)), dim3(256), 0, s, q, loss,
                        sums, out, coef, terms);
-    const int32_t blocks = (out.loss ? 1 : 0) + (out.grad ? p.blocks : 0);
+    const int32_t blocks = (out.loss ? 1 : 0) + (out.grad ? groups : 0);
     if (blocks > 0)
-      hipLaunchKernelGGL(k_pref_grads, dim3(blocks), dim3(256), 0, s, q, table, coef, terms,
-                         out.loss, out.grad);
+      hipLaunchKernelGGL(K == 2 ? k_pref_grads<2> : k_pref_grads<1>, dim3(blocks), dim3(256), 0, s,
+                         q, table, coef, terms, out.loss, out.grad);
   }
   SNK_CHECK_LAUNCH();
   return SNACK_OK;
@@ -728,7 +758,8 @@ snack_status snack_preference(const snack_seqs* batch, const snack_pref* pref, c
   const span_t in[] = {{logps, t}, {ref, t}, {dloss, 4}, {batch->starts, 4 * (n + 1)},
                        {batch->mask, batch->T}};
   if (any_overlap(out, in)) return SNACK_E_SHAPE;
-  const pref_t l{logps, ref, pref->beta, pref->smoothing, pref->form, pref->average};
+  const pref_t l{logps, ref, pref->beta, pref->smoothing, 2.0 / std::max(batch->S, 2), pref->form,
+                 pref->average};
   return run(batch, p, l, out_t{dloss, loss, rewards, dlogps}, ws, ws_bytes,
              reinterpret_cast<hipStream_t>(stream));
 }
