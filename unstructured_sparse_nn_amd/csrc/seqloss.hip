@@ -105,7 +105,6 @@ __device__ __forceinline__ double wave_sum(double x) {
   for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
   return x;
 }
-__device__ __forceinline__ double count_lanes(bool x) { return (double)__popcll(__ballot(x)); }
 
 // The sums of an item, a sequence or the batch.  Preference: f is d's sum.  cut
 // and n are whole.
@@ -124,9 +123,16 @@ struct pref_t {
   double beta, eps, share;  // share: of a pair in the loss
   int32_t form, average;
 
-  struct in_t { float lp, ref; };
-  __device__ __forceinline__ in_t load(int32_t i, int32_t) const {
-    return {logps[i], ref ? ref[i] : 0.f};
+  template <int U> struct in_t { float lp[U], ref[U]; };
+  template <int U, typename P>
+  __device__ __forceinline__ void load(const P& at, int32_t n, int32_t, in_t<U>& v) const {
+    at.get(logps, n, v.lp);
+    if (ref) {
+      at.get(ref, n, v.ref);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) v.ref[u] = 0.f;
+    }
   }
   __device__ __forceinline__ double per(const sums_t& s) const {
     return average ? 1.0 / fmax(s.n, 1.0) : 1.0;
@@ -161,10 +167,19 @@ struct policy_t {
   int32_t by_token, sequence_mean;
 
   struct token_t { float f, df, kl; bool cut; };
-  struct in_t { float lp, old, ref, adv; };
-  __device__ __forceinline__ in_t load(int32_t i, int32_t seq) const {
-    const float lp = logps[i];
-    return {lp, old ? old[i] : lp, ref ? ref[i] : 0.f, adv[by_token ? i : seq]};
+  template <int U> struct in_t { float lp[U], old[U], ref[U], adv[U]; };
+  template <int U, typename P>
+  __device__ __forceinline__ void load(const P& at, int32_t n, int32_t seq, in_t<U>& v) const {
+    at.get(logps, n, v.lp);
+    if (old) at.get(old, n, v.old);
+    if (ref) at.get(ref, n, v.ref);
+    if (by_token) at.get(adv, n, v.adv);
+    const float a = by_token ? 0.f : adv[seq];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!old) v.old[u] = v.lp[u];
+      if (!by_token) v.adv[u] = a;
+    }
   }
 
   // exp(k) - 1 - k without its cancellation near 0, and exp(k) - 1.
@@ -191,9 +206,10 @@ struct policy_t {
     return s;
   }
 
-  __device__ __forceinline__ token_t token(const in_t& v) const {
-    const float a = v.adv;
-    const double move = (double)v.lp - (double)v.old;
+  template <int U>
+  __device__ __forceinline__ token_t token(const in_t<U>& v, int u) const {
+    const float a = v.adv[u];
+    const double move = (double)v.lp[u] - (double)v.old[u];
     const float r = expf((float)move);
     token_t o;
     o.cut = (a > 0.f && move > log_high) || (a < 0.f && move < log_low);
@@ -202,7 +218,7 @@ struct policy_t {
     o.kl = 0.f;
     if (ref) {
       float em1;
-      o.kl = above((float)((double)v.ref - (double)v.lp), &em1);
+      o.kl = above((float)((double)v.ref[u] - (double)v.lp[u]), &em1);
       o.f = fmaf(kl, o.kl, o.f);
       o.df = fmaf(-kl, em1, o.df);
     }
@@ -224,39 +240,105 @@ __device__ __forceinline__ double upstream(const out_t& out) {
   return out.dloss ? (double)*out.dloss : 1.0;
 }
 
-// A lane's U tokens of an item, 64 apart, all loaded at once (those past its end
-// are its first one, if it has any).
-template <typename L, int U> struct tokens_t {
-  typename L::in_t v[U];
-  bool in[U], counts[U];
+// A lane's U tokens of an item: runs of four (one, where U is less), which are
+// loaded and stored 16 bytes at once at any alignment: where every array is read
+// four bytes a lane, the addresses cost as much as the sums (2,048 pairs, 4 million
+// tokens: 17.7 us).  A run that would pass the end is taken from the last four
+// tokens; `in` says which of them are this lane's own, `counts` which the mask has.
+template <int U> struct places_t {
+  static constexpr int W = U >= 4 ? 4 : 1, G = U / W;
+  int32_t at[G];
+  uint32_t in[G], counts[G];
 
-  __device__ __forceinline__ void load(const batch_t& q, const L& loss, const item_t& it,
-                                       int32_t from) {
+  __device__ __forceinline__ void find(const batch_t& q, int32_t a, int32_t b) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int32_t at = from + u * 64 + lane_id();
-      in[u] = at < it.b;
-      const int32_t i = in[u] ? at : it.a;
-      counts[u] = in[u] && (q.mask ? q.mask[i] != 0 : true);
-      v[u] = loss.load(i, it.seq);
+    for (int g = 0; g < G; ++g) {
+      const int32_t start = a + (g * 64 + lane_id()) * W;
+      if (W == 1) {
+        at[g] = start < b ? start : a;
+        in[g] = start < b;
+        counts[g] = in[g];
+        if (q.mask) counts[g] &= q.mask[at[g]] != 0;
+      } else if (b - a >= W) {
+        at[g] = min(start, b - W);
+        in[g] = start < b ? 15u & (15u << (start - at[g])) : 0u;
+        counts[g] = in[g];
+        if (q.mask) {
+          uint32_t m;
+          __builtin_memcpy(&m, q.mask + at[g], 4);
+          // a bit of each byte that is not 0, and the four of them side by side
+          m = ((((m & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | m) & 0x80808080u) >> 7;
+          counts[g] &= (m * 0x01020408u) >> 24;
+        }
+      } else {  // fewer than four: the first lane's
+        at[g] = a;
+        in[g] = g == 0 && lane_id() == 0 ? (1u << (b - a)) - 1u : 0u;
+        counts[g] = in[g];
+        if (q.mask)
+          for (int32_t e = 0; e < b - a; ++e)
+            if (!q.mask[a + e]) counts[g] &= ~(1u << e);
+      }
     }
+  }
+  __device__ __forceinline__ bool has(int u) const { return counts[u / W] >> (u % W) & 1; }
+  // v, or 0 where the mask has a token not.
+  __device__ __forceinline__ void put(float* grad, const float (&v)[U]) const {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float o[W];
+#pragma unroll
+      for (int e = 0; e < W; ++e) o[e] = has(g * W + e) ? v[g * W + e] : 0.f;
+      if (in[g] == (1u << W) - 1u) {
+        __builtin_memcpy(grad + at[g], o, sizeof(o));
+      } else if (in[g]) {
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          if (in[g] >> e & 1) grad[at[g] + e] = o[e];
+      }
+    }
+  }
+  // Elements of a token array.
+  __device__ __forceinline__ void get(const float* p, int32_t n, float (&v)[U]) const {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (W == 1 || n >= W) {
+        __builtin_memcpy(&v[g * W], p + at[g], 4 * W);
+      } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[g * W + e] = p[at[g] + min(e, n - 1)];
+      }
+    }
+  }
+};
+
+template <typename L, int U> struct tokens_t {
+  places_t<U> at;
+  typename L::template in_t<U> v;
+
+  __device__ __forceinline__ void load(const batch_t& q, const L& loss, const item_t& it) {
+    at.find(q, it.a, it.b);
+    loss.template load<U>(at, it.b - it.a, it.seq, v);
   }
   // Adds them to this lane's f and kl and to the wave's counts; g: what their
   // gradients are but for the weight.
   __device__ __forceinline__ void add(const L& loss, sums_t& s, float (&g)[U]) const {
+    int32_t n = 0, cut = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      s.n += count_lanes(counts[u]);
+      const bool has = at.has(u);
+      n += (int32_t)__popcll(__ballot(has));
       if constexpr (L::POLICY) {
-        const auto o = loss.token(v[u]);
-        s.cut += count_lanes(counts[u] && o.cut);
-        s.f += counts[u] ? (double)o.f : 0.0;
-        s.kl += counts[u] ? (double)o.kl : 0.0;
-        g[u] = counts[u] ? o.df : 0.f;
+        const auto o = loss.template token<U>(v, u);
+        cut += (int32_t)__popcll(__ballot(has && o.cut));
+        s.f += (double)(has ? o.f : 0.f);
+        s.kl += (double)(has ? o.kl : 0.f);
+        g[u] = o.df;
       } else {
-        s.f += counts[u] ? (double)v[u].lp - (double)v[u].ref : 0.0;
+        s.f += has ? (double)v.lp[u] - (double)v.ref[u] : 0.0;
       }
     }
+    s.n += n;
+    s.cut += cut;
   }
 };
 template <typename L>
@@ -333,7 +415,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void k_seq_small(batch_t q, L los
   }
 #pragma unroll
   for (int k = 0; k < K; ++k)
-    if (it[k].a < it[k].b) t[k].load(q, loss, it[k], it[k].a);
+    if (it[k].a < it[k].b) t[k].load(q, loss, it[k]);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int32_t x = k * SMALL_WAVES + w;
@@ -389,11 +471,8 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void k_seq_small(batch_t q, L los
     if (it[k].a >= it[k].b) continue;
     const double c = coef[it[k].seq];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (t[k].in[u]) {
-        const double v = L::POLICY ? (double)g[k][u] * c : c;
-        out.grad[it[k].a + u * 64 + lane] = t[k].counts[u] ? (float)v : 0.f;
-      }
+    for (int u = 0; u < U; ++u) g[k][u] = (float)(L::POLICY ? (double)g[k][u] * c : c);
+    t[k].at.put(out.grad, g[k]);
   }
   write_outside(q, out.grad, threadIdx.x, SMALL_WAVES * 64);
 }
@@ -432,7 +511,7 @@ __global__ __launch_bounds__(256) void k_pref_sums(batch_t q, pref_t loss,
     it[k] = first + 4 * k < q.items ? item_of(q, first + 4 * k) : item_t{};
 #pragma unroll
   for (int k = 0; k < K; ++k)
-    if (it[k].a < it[k].b) t[k].load(q, loss, it[k], it[k].a);
+    if (it[k].a < it[k].b) t[k].load(q, loss, it[k]);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int32_t x = first + 4 * k;
@@ -484,10 +563,10 @@ __global__ __launch_bounds__(256) void k_pref_grads(batch_t q, const slot_t* __r
     if (threadIdx.x == 0) *loss = (float)s.f;
     return;
   }
-  const int32_t b = blockIdx.x - with_loss, lane = lane_id();
+  const int32_t b = blockIdx.x - with_loss;
   const int32_t first = b * (4 * K) + wave_of_block();
   slot_t it[K];
-  bool counts[K][U];
+  places_t<U> at[K];
   float c[K];
 #pragma unroll
   for (int k = 0; k < K; ++k)
@@ -496,19 +575,16 @@ __global__ __launch_bounds__(256) void k_pref_grads(batch_t q, const slot_t* __r
   for (int k = 0; k < K; ++k) {
     if (it[k].a >= it[k].b) continue;
     c[k] = (float)coef[it[k].seq];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int32_t at = it[k].a + u * 64 + lane;
-      counts[k][u] = q.mask ? q.mask[at < it[k].b ? at : it[k].a] != 0 : true;
-    }
+    at[k].find(q, it[k].a, it[k].b);
   }
 #pragma unroll
-  for (int k = 0; k < K; ++k)
+  for (int k = 0; k < K; ++k) {
+    if (it[k].a >= it[k].b) continue;
+    float v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int32_t at = it[k].a + u * 64 + lane;
-      if (at < it[k].b) grad[at] = counts[k][u] ? c[k] : 0.f;
-    }
+    for (int u = 0; u < U; ++u) v[u] = c[k];
+    at[k].put(grad, v);
+  }
   write_outside(q, grad, (int64_t)b * 256 + threadIdx.x,
                 ((int64_t)gridDim.x - with_loss) * 256);
 }
@@ -568,7 +644,7 @@ __global__ __launch_bounds__(256) void k_policy(batch_t q, policy_t loss, out_t 
   item_t it{};
   if (mine) it = item_of(q, x);
   tokens_t<policy_t, U> t;
-  if (it.a < it.b) t.load(q, loss, it, it.a);
+  if (it.a < it.b) t.load(q, loss, it);
   double n = 0;  // tokens that the loss's mean is over: of the batch, or of the sequence
   if (!loss.sequence_mean) {
     int32_t part = 0;
@@ -610,8 +686,8 @@ __global__ __launch_bounds__(256) void k_policy(batch_t q, policy_t loss, out_t 
     s.f *= weight;
     if (out.grad) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (t.in[u]) out.grad[it.a + u * 64 + lane] = t.counts[u] ? (float)((double)g[u] * c) : 0.f;
+      for (int u = 0; u < U; ++u) g[u] = (float)((double)g[u] * c);
+      t.at.put(out.grad, g);
     }
   }
   if (lane == 0) lds[w] = s;
