@@ -104,6 +104,8 @@ class LoraAdapters(torch.nn.Module):
     graph while the backward is captured: torch would join the eager stream to
     the capture and end the process."""
 
+    dropout, seed, step = 0.0, None, 0  # of modules that were pickled without them
+
     def __init__(self, in_features: int, out_features: int, adapters: int, rank: int,
                  alpha: float = 16.0, ranks=None, dtype=torch.float32, device="cuda",
                  dropout: float = 0.0, seed: int | None = None):

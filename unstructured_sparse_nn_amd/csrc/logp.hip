@@ -7,8 +7,10 @@
 //
 // Both are bound by memory.  The forward reads the logits once: every thread
 // keeps a running maximum and sum, whose sum is scaled where the maximum grows;
-// rows of few are cut among workgroups, whose pairs k_logp_join adds.  The
-// backward reads and writes them once.
+// long rows of few are cut among workgroups, whose pairs k_logp_join adds.  The
+// backward reads and writes them once, and does not read rows whose gradient is 0.
+// 8,192 rows of 32,000 bf16: 92 us (5.7 TB/s), backward 193 us (5.4 TB/s); 4,099 of
+// 50,001, 30% without a target, backward 134 us (5.2 TB/s); 5 of 128,000: 6.1 us.
 #include "common.h"
 #include "internal.h"
 #include "pieces.h"
@@ -162,8 +164,12 @@ __device__ __forceinline__ float grad_of(int32_t t, const float* dlogp, int64_t 
   return t == -1 ? 0.f : t == -2 ? __builtin_nanf("") : dlogp[i];
 }
 
-// Workgroup (c, i): 256 U pieces of row i.
-template <typename T>
+// Workgroup (c, i): 256 U pieces of row i.  BIG: gradients that leave no room in the
+// 256 MB cache before memory are stored past the caches, for the lines that plain
+// stores leave there have to be written back while the next kernel reads (8,192 rows
+// of 32,000: 203 us, 195 us past them).
+constexpr int64_t BIG_BYTES = 128ll << 20;
+template <typename T, bool BIG>
 __global__ __launch_bounds__(256) void k_logp_grad(const T* x, int64_t ldx, int32_t V, ids_t ids,
                                                    const float* __restrict__ dlogp,
                                                    const float2* __restrict__ norm, T* dx,
@@ -186,7 +192,13 @@ __global__ __launch_bounds__(256) void k_logp_grad(const T* x, int64_t ldx, int3
   for (int u = 0; u < U; ++u) {
     if (first + u * 256 >= per) break;
     const cut_t c = cut_of<T>(first + u * 256, V);
-    store_cut(dx, c, V, grad_piece(f[u], c, t, g, n));
+    const frag<T> o = grad_piece(f[u], c, t, g, n);
+    if (BIG && c.from == 0) {  // rows of more than one piece
+      typedef uint32_t u4 __attribute__((ext_vector_type(4), aligned(2)));
+      __builtin_nontemporal_store(__builtin_bit_cast(u4, o), reinterpret_cast<u4*>(dx + c.at));
+    } else {
+      store_cut(dx, c, V, o);
+    }
   }
 }
 
@@ -213,15 +225,15 @@ struct parts_t { int32_t parts, each; };
 // Rows up to this many pieces are short: one wave reads them in four loads.
 constexpr int32_t SHORT = 256;
 
-// A workgroup of 16 waves takes 3 us and 1 us more for every 22,000 of its row's
-// logits (their exponentials, four a cycle): rows of more than CUT are cut where
-// they leave CUs idle, although adding the parts is a launch more (one row of
-// 128,000: 9.0 us whole, 5.7 us in 16 parts; of 32,000: 4.9 us whole).
+// A workgroup takes 3 us and 1 us more for every 22,000 of its row's logits (their
+// exponentials, four a cycle): rows of more than CUT are cut where there are few,
+// although adding the parts is a launch more (5 rows of 128,000: 9.1 us whole, 6.1 us
+// in parts; one of 32,000: 5.0 and 6.0 us; 100 of 128,000: 10.7 and 11.2 us).
 constexpr int32_t CUT = 49152;
 parts_t parts_of(snack_dtype dt, int64_t Tn, int32_t V) {
   const int32_t e = dt == SNACK_BF16 ? 8 : 4;
   int64_t parts = 1;
-  if (V > CUT && Tn < 256)
+  if (V > CUT && Tn <= 64)
     parts = std::min<int64_t>(cdiv(512, std::max<int64_t>(Tn, 1)), V / 8192);
   const int64_t each = cdiv(cdiv(V, parts), 256 * e) * 256 * e;
   return {(int32_t)std::max<int64_t>(1, cdiv(V, each)), (int32_t)std::min<int64_t>(each, INT32_MAX)};
@@ -242,10 +254,10 @@ template <typename T>
 void run_fwd(const T* x, int64_t ldx, int64_t Tn, int32_t V, ids_t ids, float* logp, float2* norm,
              float2* part, parts_t p, hipStream_t s) {
   const int64_t pieces = cdiv(V, EL<T>);
-  // up to four pieces a thread, and 16 waves where rows are few: one wave a row of
-  // 300 logits, 16,384 of them, 9.3 us, 16 lanes 6 us; 900 rows of 32,000 logits 4 waves
-  // 22 us, 16 waves 15 us
-  const int N = pieces <= SHORT / 4 ? 16 : pieces <= SHORT ? 64 : p.parts == 1 && Tn < 1024 ? 1024 : 256;
+  // Up to four pieces a thread (a wave for each of 16,384 rows of 300 logits: 9.3 us,
+  // 16 lanes 5.5 us), and 16 waves where rows are few (one row of 32,000 logits: 5.2 us
+  // with 4 waves, 5.0 us with 16; 64 rows 5.8 and 5.4 us; 900 rows 13.3 and 15.3 us).
+  const int N = pieces <= SHORT / 4 ? 16 : pieces <= SHORT ? 64 : p.parts == 1 && Tn <= 128 ? 1024 : 256;
   auto kernel = N == 16 ? k_logp<T, 16> : N == 64 ? k_logp<T, 64> : N == 256 ? k_logp<T, 256>
                                                                             : k_logp<T, 1024>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(N < 256 ? cdiv(Tn * N, 256) : Tn * p.parts)),
@@ -260,12 +272,15 @@ template <typename T>
 void run_bwd(const T* x, int64_t ldx, int64_t Tn, int32_t V, ids_t ids, const float* dlogp,
              const float2* norm, T* dx, int64_t lddx, hipStream_t s) {
   const int64_t pieces = cdiv(V, EL<T>), blocks = cdiv(pieces, 1024);
-  if (pieces <= 2 * SHORT && Tn * pieces <= MAX_PIECES)
+  if (pieces <= 2 * SHORT && Tn * pieces <= MAX_PIECES) {
     hipLaunchKernelGGL(k_logp_grad_short<T>, dim3((unsigned)cdiv(Tn * pieces, 256)), dim3(256), 0, s,
                        x, ldx, Tn, V, ids, dlogp, norm, dx, lddx, (uint32_t)pieces);
-  else
-    hipLaunchKernelGGL(k_logp_grad<T>, dim3((unsigned)(Tn * blocks)), dim3(256), 0, s, x, ldx, V,
-                       ids, dlogp, norm, dx, lddx, (uint32_t)blocks);
+  } else {
+    const bool big = pieces > 1 && Tn * pieces * 16 > BIG_BYTES;
+    auto kernel = big ? k_logp_grad<T, true> : k_logp_grad<T, false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(Tn * blocks)), dim3(256), 0, s, x, ldx, V, ids,
+                       dlogp, norm, dx, lddx, (uint32_t)blocks);
+  }
 }
 
 }  // namespace

@@ -27,8 +27,12 @@
 // Small batches take one workgroup and one launch (k_seq_small), whose waves keep
 // their tokens in registers.  Sums are 64-bit in a fixed order; whether a ratio is
 // past its border is decided on logarithms in 64 bits.  A token's terms are fp32.
-// Bound by memory where the batch is large: two to five floats a token read and
-// one written; by launches and trips to memory where it is not.
+// Bound by launches, trips to memory and, on one CU, instructions where the batch
+// is small: 1,500 tokens in 16 sequences 5.9 us, a policy's 12,345 in 64 7.7 us.  Large
+// batches are two to five floats a token read and one written, but come to half of
+// memory's rate at most: 4 million tokens in 4,096 sequences 26.3 us (sums 13.3, finish
+// 4.8, gradients 8.1; 2 TB/s), a policy's 2 million in 1,024 24.0 us (counts 4.3, gradients
+// 16.1, finish 4.0; the tokens' terms are 6 us of instructions).
 #include <cmath>
 
 #include "common.h"
@@ -380,7 +384,10 @@ __device__ __forceinline__ void finish_stats(const sums_t& all, const out_t& out
 // ------------------------------------------------------- one workgroup, one launch
 constexpr int SMALL_WAVES = 16;
 constexpr int32_t SMALL_LOG_P = 7, SMALL_SEQS = 127;
-constexpr int SMALL_EACH = 2;  // items of a wave
+// Items of a wave at most.  A policy's tokens are ten times the instructions, and
+// its other path is two launches, not three: 5,000 tokens in 4 sequences 7.1 us
+// there, 10.0 us in one workgroup; a preference's in 16 10.0 and 8.8 us.
+template <typename L> constexpr int SMALL_EACH = L::POLICY ? 2 : 4;
 
 // The starts of all sequences, two a lane.
 struct starts_t {
@@ -393,7 +400,7 @@ struct starts_t {
 
 template <typename L>
 __global__ __launch_bounds__(SMALL_WAVES * 64) void k_seq_small(batch_t q, L loss, out_t out) {
-  constexpr int K = SMALL_EACH, U = 1 << (SMALL_LOG_P - 6);
+  constexpr int K = SMALL_EACH<L>, U = 1 << (SMALL_LOG_P - 6);
   __shared__ sums_t sums[K * SMALL_WAVES];
   __shared__ double coef[SMALL_SEQS + 1];
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64), lane = lane_id();
@@ -494,36 +501,25 @@ __device__ __forceinline__ sums_t block_sum(sums_t s, sums_t* lds) {
   return s;
 }
 
-// K items a wave, whose trips to memory overlap.  table: what k_pref_grads needs of
-// an item.
+// What k_pref_grads needs of an item.
 struct __attribute__((aligned(16))) slot_t { int32_t seq, a, b, zero; };
 
-template <int K>
 __global__ __launch_bounds__(256) void k_pref_sums(batch_t q, pref_t loss,
                                                    sums_t* __restrict__ sums,
                                                    slot_t* __restrict__ table) {
-  constexpr int U = 1 << (LOG_P - 6);
-  item_t it[K];
-  tokens_t<pref_t, U> t[K];
-  const int32_t first = blockIdx.x * (4 * K) + wave_of_block();
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-    it[k] = first + 4 * k < q.items ? item_of(q, first + 4 * k) : item_t{};
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-    if (it[k].a < it[k].b) t[k].load(q, loss, it[k]);
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int32_t x = first + 4 * k;
-    if (x >= q.items) return;
-    sums_t s{0, 0, 0, 0};
-    if (it[k].a < it[k].b) {
-      float g[U];
-      t[k].add(loss, s, g);
-      wave_totals<pref_t>(s);
-    }
-    if (lane_id() == 0) sums[x] = s, table[x] = slot_t{it[k].seq, it[k].a, it[k].b, 0};
+  const int32_t x = blockIdx.x * 4 + wave_of_block();
+  if (x >= q.items) return;
+  const item_t it = item_of(q, x);
+  sums_t s{0, 0, 0, 0};
+  if (it.a < it.b) {
+    constexpr int U = 1 << (LOG_P - 6);
+    tokens_t<pref_t, U> t;
+    float g[U];
+    t.load(q, loss, it);
+    t.add(loss, s, g);
+    wave_totals<pref_t>(s);
   }
+  if (lane_id() == 0) sums[x] = s, table[x] = slot_t{it.seq, it.a, it.b, 0};
 }
 
 __device__ __forceinline__ sums_t range_sums(const sums_t* __restrict__ sums, range_t r) {
@@ -546,7 +542,6 @@ __global__ __launch_bounds__(256) void k_pref_finish(batch_t q, pref_t loss,
 
 // The first workgroup adds the loss's terms, if it is wanted; the others write
 // gradients.
-template <int K>
 __global__ __launch_bounds__(256) void k_pref_grads(batch_t q, const slot_t* __restrict__ table,
                                                     const double* __restrict__ coef,
                                                     const double* __restrict__ terms,
@@ -564,26 +559,18 @@ __global__ __launch_bounds__(256) void k_pref_grads(batch_t q, const slot_t* __r
     return;
   }
   const int32_t b = blockIdx.x - with_loss;
-  const int32_t first = b * (4 * K) + wave_of_block();
-  slot_t it[K];
-  places_t<U> at[K];
-  float c[K];
+  const int32_t x = b * 4 + wave_of_block();
+  if (x < q.items) {
+    const slot_t it = table[x];
+    if (it.a < it.b) {
+      const float c = (float)coef[it.seq];
+      places_t<U> at;
+      at.find(q, it.a, it.b);
+      float v[U];
 #pragma unroll
-  for (int k = 0; k < K; ++k)
-    it[k] = first + 4 * k < q.items ? table[first + 4 * k] : slot_t{0, 0, 0, 0};
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if (it[k].a >= it[k].b) continue;
-    c[k] = (float)coef[it[k].seq];
-    at[k].find(q, it[k].a, it[k].b);
-  }
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if (it[k].a >= it[k].b) continue;
-    float v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = c[k];
-    at[k].put(grad, v);
+      for (int u = 0; u < U; ++u) v[u] = c;
+      at.put(grad, v);
+    }
   }
   write_outside(q, grad, (int64_t)b * 256 + threadIdx.x,
                 ((int64_t)gridDim.x - with_loss) * 256);
@@ -713,11 +700,14 @@ __global__ __launch_bounds__(W * 64) void k_policy_finish(const sums_t* __restri
 // ---------------------------------------------------------------------- host
 constexpr int32_t MAX_SEQS = 1 << 24;
 
-// Items are small (128 tokens) where there are few: a wave's tokens are then two a
-// lane.
+// A policy's items are small (128 tokens) where there are few: a wave's tokens are
+// then two a lane, and more waves share them (12,345 tokens in 64 sequences 7.7 us,
+// 10.0 us with items of 512).
 constexpr int32_t MEDIUM_ITEMS = 2048;
-// Masks up to this many bytes are counted by every workgroup that needs them.
-constexpr int32_t COUNT_TOKENS = 16384;
+// Masks up to this many bytes are counted by every workgroup that needs them, which
+// saves a launch (60,000 tokens: a mean over 500 sequences 7.4 us, 10.2 us with it;
+// over all tokens 9.9 and 10.1 us).
+constexpr int32_t COUNT_TOKENS = 65536;
 
 struct plan_t {
   bool small;
@@ -728,7 +718,7 @@ struct plan_t {
 plan_t plan_of(int32_t S, int32_t Tn, bool policy) {
   plan_t p{};
   auto items = [&](int32_t log_p) { return S == 0 ? 0 : S + (Tn >> log_p); };
-  p.small = S <= SMALL_SEQS && items(SMALL_LOG_P) <= SMALL_EACH * SMALL_WAVES;
+  p.small = S <= SMALL_SEQS && items(SMALL_LOG_P) <= SMALL_WAVES * (policy ? SMALL_EACH<policy_t> : SMALL_EACH<pref_t>);
   p.log_p = p.small || (policy && items(SMALL_LOG_P) <= MEDIUM_ITEMS) ? SMALL_LOG_P : LOG_P;
   p.items = items(p.log_p);
   p.blocks = (int32_t)cdiv(p.items, 4);
@@ -785,17 +775,13 @@ snack_status run(const snack_seqs* b, const plan_t& p, const L& loss, const out_
   } else {
     slot_t* table = (slot_t*)(w + p.table);
     double *coef = (double*)(w + p.coef), *terms = (double*)(w + p.terms);
-    // two items a wave once the card has no place for a wave each
-    const int K = p.items > 8192 ? 2 : 1;
-    const int32_t groups = (int32_t)cdiv(p.items, 4 * K);
-    hipLaunchKernelGGL(K == 2 ? k_pref_sums<2> : k_pref_sums<1>, dim3(groups), dim3(256), 0, s, q,
-                       loss, sums, table);
+    hipLaunchKernelGGL(k_pref_sums, dim3(p.blocks), dim3(256), 0, s, q, loss, sums, table);
     hipLaunchKernelGGL(k_pref_finish, dim3((unsigned)cdiv(b->S / 2, 4)), dim3(256), 0, s, q, loss,
                        sums, out, coef, terms);
-    const int32_t blocks = (out.loss ? 1 : 0) + (out.grad ? groups : 0);
+    const int32_t blocks = (out.loss ? 1 : 0) + (out.grad ? p.blocks : 0);
     if (blocks > 0)
-      hipLaunchKernelGGL(K == 2 ? k_pref_grads<2> : k_pref_grads<1>, dim3(blocks), dim3(256), 0, s,
-                         q, table, coef, terms, out.loss, out.grad);
+      hipLaunchKernelGGL(k_pref_grads, dim3(blocks), dim3(256), 0, s, q, table, coef, terms,
+                         out.loss, out.grad);
   }
   SNK_CHECK_LAUNCH();
   return SNACK_OK;
