@@ -28,11 +28,11 @@
 // their tokens in registers.  Sums are 64-bit in a fixed order; whether a ratio is
 // past its border is decided on logarithms in 64 bits.  A token's terms are fp32.
 // Bound by launches, trips to memory and, on one CU, instructions where the batch
-// is small: 1,500 tokens in 16 sequences 5.9 us, a policy's 12,345 in 64 7.7 us.  Large
+// is small: 1,500 tokens in 16 sequences 5.9 us, a policy's 12,345 in 64 7.8 us.  Large
 // batches are two to five floats a token read and one written, but come to half of
-// memory's rate at most: 4 million tokens in 4,096 sequences 26.3 us (sums 13.3, finish
-// 4.8, gradients 8.1; 2 TB/s), a policy's 2 million in 1,024 24.0 us (counts 4.3, gradients
-// 16.1, finish 4.0; the tokens' terms are 6 us of instructions).
+// memory's rate at most: 4 million tokens in 4,096 sequences 24.8 us (sums 11.5, finish
+// 5.4, gradients 7.5; 2.1 TB/s), a policy's 2 million in 1,024 21.4 us (counts 4.2,
+// gradients 14.8, finish 4.0; the tokens' terms are 6 us of instructions).
 #include <cmath>
 
 #include "common.h"
@@ -129,10 +129,10 @@ struct pref_t {
 
   template <int U> struct in_t { float lp[U], ref[U]; };
   template <int U, typename P>
-  __device__ __forceinline__ void load(const P& at, int32_t n, int32_t, in_t<U>& v) const {
-    at.get(logps, n, v.lp);
+  __device__ __forceinline__ void load(const P& at, int32_t, in_t<U>& v) const {
+    at.get(logps, v.lp);
     if (ref) {
-      at.get(ref, n, v.ref);
+      at.get(ref, v.ref);
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u) v.ref[u] = 0.f;
@@ -173,11 +173,11 @@ struct policy_t {
   struct token_t { float f, df, kl; bool cut; };
   template <int U> struct in_t { float lp[U], old[U], ref[U], adv[U]; };
   template <int U, typename P>
-  __device__ __forceinline__ void load(const P& at, int32_t n, int32_t seq, in_t<U>& v) const {
-    at.get(logps, n, v.lp);
-    if (old) at.get(old, n, v.old);
-    if (ref) at.get(ref, n, v.ref);
-    if (by_token) at.get(adv, n, v.adv);
+  __device__ __forceinline__ void load(const P& at, int32_t seq, in_t<U>& v) const {
+    at.get(logps, v.lp);
+    if (old) at.get(old, v.old);
+    if (ref) at.get(ref, v.ref);
+    if (by_token) at.get(adv, v.adv);
     const float a = by_token ? 0.f : adv[seq];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -247,16 +247,27 @@ __device__ __forceinline__ double upstream(const out_t& out) {
 // A lane's U tokens of an item: runs of four (one, where U is less), which are
 // loaded and stored 16 bytes at once at any alignment: where every array is read
 // four bytes a lane, the addresses cost as much as the sums (2,048 pairs, 4 million
-// tokens: 17.7 us).  A run that would pass the end is taken from the last four
+// tokens: 32.7 us, 26.2 us so).  A run that would pass the end is taken from the last four
 // tokens; `in` says which of them are this lane's own, `counts` which the mask has.
+// (Items of 1,024 tokens instead of 512: 24.1 us for that batch, but 19.2 instead of
+// 18.6 us for 2 million tokens in 4,000 sequences, 12.0 instead of 11.4 us for 100,000 in
+// 1,000, and a policy's 2 million 23.1 instead of 21.4 us.)
 template <int U> struct places_t {
   static constexpr int W = U >= 4 ? 4 : 1, G = U / W;
+  int32_t n;  // the item's tokens
   int32_t at[G];
   uint32_t in[G], counts[G];
 
+  // Whether the wave has tokens in its run g: most items end early, and what is not
+  // there costs no instructions (the same batch 26.3 us without this).
+  __device__ __forceinline__ bool some(int g) const { return g * 64 * W < n; }
+
   __device__ __forceinline__ void find(const batch_t& q, int32_t a, int32_t b) {
+    n = __builtin_amdgcn_readfirstlane(b - a);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
+      in[g] = counts[g] = 0;
+      if (!some(g)) continue;
       const int32_t start = a + (g * 64 + lane_id()) * W;
       if (W == 1) {
         at[g] = start < b ? start : a;
@@ -289,6 +300,7 @@ template <int U> struct places_t {
   __device__ __forceinline__ void put(float* grad, const float (&v)[U]) const {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
+      if (!some(g)) continue;
       float o[W];
 #pragma unroll
       for (int e = 0; e < W; ++e) o[e] = has(g * W + e) ? v[g * W + e] : 0.f;
@@ -302,9 +314,10 @@ template <int U> struct places_t {
     }
   }
   // Elements of a token array.
-  __device__ __forceinline__ void get(const float* p, int32_t n, float (&v)[U]) const {
+  __device__ __forceinline__ void get(const float* p, float (&v)[U]) const {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
+      if (!some(g)) continue;
       if (W == 1 || n >= W) {
         __builtin_memcpy(&v[g * W], p + at[g], 4 * W);
       } else {
@@ -321,7 +334,7 @@ template <typename L, int U> struct tokens_t {
 
   __device__ __forceinline__ void load(const batch_t& q, const L& loss, const item_t& it) {
     at.find(q, it.a, it.b);
-    loss.template load<U>(at, it.b - it.a, it.seq, v);
+    loss.template load<U>(at, it.seq, v);
   }
   // Adds them to this lane's f and kl and to the wave's counts; g: what their
   // gradients are but for the weight.
@@ -329,6 +342,7 @@ template <typename L, int U> struct tokens_t {
     int32_t n = 0, cut = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if (!at.some(u / places_t<U>::W)) continue;
       const bool has = at.has(u);
       n += (int32_t)__popcll(__ballot(has));
       if constexpr (L::POLICY) {
