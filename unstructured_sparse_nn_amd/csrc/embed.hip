@@ -383,8 +383,8 @@ plan_t plan_of(snack_dtype dt, int64_t Tn, int32_t V, int32_t D) {
   p.tiles = Tn > RUN ? cdiv(Tn, RUN) : 0;
   // a sorting workgroup on a CU, with 32 rows at least
   p.range = (int32_t)std::min<int64_t>(MAX_RANGE, std::max<int64_t>(32, cdiv(V, 256)));
-  // 16 waves of them once there are numbers for all (1,024 tokens, 50,000 rows of 768:
-  // 22.3 us with 4, 23.7 us with 16; 20,000, 32,000 of 1,000: 16)
+  // 16 waves of them once there are two blocks of numbers for each (1,024 tokens, 50,000
+  // rows of 768: 22.3 us with 4 waves, 23.7 us with 16)
   p.waves = Tn <= 2048 && p.range <= 256 ? 4 : 16;
   size_t o = 0;
   auto take = [&](size_t b) {

@@ -44,7 +44,11 @@ class _EmbedFn(torch.autograd.Function):
 
 class TokenEmbedding(torch.nn.Module):
     """A trainable table of ``rows`` tokens by ``features``, looked up and scaled.
-    Starts normal with standard deviation 0.02."""
+    Starts normal with standard deviation 0.02.
+
+    Forward and backward can be captured into a graph; as with any torch module,
+    no output of an eager step may still hold this parameter's autograd graph
+    while the backward is captured."""
 
     def __init__(self, rows: int, features: int, scale: float = 1.0, dtype=torch.float32,
                  device="cuda"):
