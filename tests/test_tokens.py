@@ -405,6 +405,33 @@ def test_offsets_past_32_bits():
     within(x[[3, T - 1]], ref, tol + 1.01 * 2.0 ** -8 * ref.abs(), "dx")
 
 
+@gpu
+@pytest.mark.parametrize("V", [65536, 65541])
+def test_gradients_past_128_megabytes(V):
+    """Stored past the caches: the same bits as in parts that are not."""
+    T = 1100
+    x = (torch.randn(T, V, device="cuda") * 2).to(H)
+    t = torch.randint(-1, V, (T,), device="cuda")
+    g = torch.randn(T, device="cuda")
+    norm = snk.logp_fwd(x, t)[1]
+    whole = snk.logp_bwd(g, x, t, norm)
+    for rows in (slice(0, 500), slice(500, T)):
+        part = snk.logp_bwd(g[rows], x[rows], t[rows], norm[rows])
+        assert torch.equal(whole[rows], part)
+    assert torch.equal(snk.logp_bwd(g, x, t, norm, out=x), whole)
+
+
+@gpu
+@pytest.mark.parametrize("how", ["text", "one", "few", "mixed"])
+def test_gradient_of_many_tokens(how):
+    """More numbers than a wave lists, and rows of tens of thousands of tokens."""
+    T, V, D = 150001, 5000, 16
+    ids = ids_of(T, V, how, 1)
+    dy = torch.randn(T, D, device="cuda")
+    ref, tol = grad_formula(dy, ids, V, 1.0, None)
+    within(snk.embed_bwd(dy, ids, V), ref, tol, how)
+
+
 # --------------------------------------------------------------------- together
 @gpu
 def test_other_streams_graphs_and_the_binding():
