@@ -52,8 +52,8 @@ class _DropoutFn(torch.autograd.Function):
 
 
 def random_seed() -> int:
-    """A seed from torch's generator of the CPU."""
-    return int(torch.randint(0, 2 ** 62, ()))
+    """A seed from torch's generator of the CPU, whatever the default device."""
+    return int(torch.randint(0, 2 ** 62, (), device="cpu"))
 
 
 class Dropout(torch.nn.Module):
