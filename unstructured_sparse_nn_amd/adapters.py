@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import torch
 
-from .dropout import dropout_bwd, dropout_fwd, random_seed
+from .dropout import CountedSteps, dropout_bwd, dropout_fwd, random_seed
 from .native import calls
 
 
@@ -86,7 +86,7 @@ class _DroppedLoraFn(torch.autograd.Function):
         return (dx, dA, dB, gy if ctx.needs_input_grad[3] else None, *[None] * 6)
 
 
-class LoraAdapters(torch.nn.Module):
+class LoraAdapters(CountedSteps, torch.nn.Module):
     """L trainable low-rank adapters of one projection.
 
     A starts normal with standard deviation 1/sqrt(in_features), B at zero, so
@@ -95,9 +95,9 @@ class LoraAdapters(torch.nn.Module):
 
     ``dropout``: in training, the adapters see x with that share of its elements
     dropped (base does not).  Its mask comes from ``seed`` (drawn from torch's
-    generator if None) and ``step``, which counts the calls in training and is no
-    part of the state dict; a call may name its own, a number or one int64 on the
-    GPU (:mod:`.dropout`).
+    generator if None) and ``step``, which counts the calls in training (one that
+    activation checkpointing runs again once) and is no part of the state dict; a call may name its
+    own, a number or one int64 on the GPU (:mod:`.dropout`).
 
     Forward and backward can be captured into a graph.  As with any torch
     module, no output of an eager step may still hold these parameters' autograd
@@ -142,7 +142,7 @@ class LoraAdapters(torch.nn.Module):
         """base + each row's adapter applied to x (rows of x: tokens)."""
         if self.training and self.dropout > 0:
             if step is None:
-                step, self.step = self.step, self.step + 1
+                step = self._next_step()
             return _DroppedLoraFn.apply(x, self.A, self.B, base, ids, self.scale, self.ranks,
                                         self.dropout, self.seed, step)
         if torch.is_grad_enabled():

@@ -2,12 +2,17 @@
 counter-based generator and is never stored.
 
 Element i of a call is dropped or kept by ``seed``, ``step`` and i alone, so the
-backward pass (and a recomputed forward) finds the same mask again.  One seed to
-a place in the model and one step to a call give independent masks.  ``step``
-may be a number or one int64 on the GPU, which is read when the kernel runs: a
-captured graph whose step is counted up between replays draws anew.
+backward pass (and a recomputed forward, given the same step) finds the same mask
+again.  One seed to a place in the model and one step to a call give independent
+masks.  ``step`` may be a number or one int64 on the GPU, which is read when the
+kernel runs: a captured graph whose step is counted up between replays draws anew.
+
+The modules count their calls in training where a call names no step
+(:class:`CountedSteps`).
 """
 from __future__ import annotations
+
+import weakref
 
 import torch
 
@@ -56,11 +61,49 @@ def random_seed() -> int:
     return int(torch.randint(0, 2 ** 62, (), device="cpu"))
 
 
-class Dropout(torch.nn.Module):
+# Calls of a module that may still be run again.
+RECENT = 4096
+_in_backward = torch._C._current_graph_task_id  # -1: not
+_known = weakref.WeakKeyDictionary()  # module: [its step after the last call, {draw: step}]
+
+
+class CountedSteps:
+    """The steps of a module's calls: ``self.step``, counted up.
+
+    A call that is run again (``torch.utils.checkpoint``, either form) takes the
+    step of its first run.  It is known by a number that every call draws from
+    torch's generator of the CPU, whose state a recomputation restores: as of
+    torch's own dropout, calls from one state of the generator drop the same
+    elements, unless ``self.step`` was set between them.  A call that the backward
+    runs from another state (``preserve_rng_state=False``), or again after RECENT
+    others, is refused."""
+
+    def _next_step(self):
+        draw = random_seed()
+        in_backward = _in_backward() != -1
+        known = _known.get(self)
+        if known is None or (known[0] != self.step and not in_backward):
+            known = _known[self] = [self.step, {}]
+        step = known[1].get(draw)
+        if step is None:
+            if in_backward:
+                raise RuntimeError(f"{type(self).__name__}: a call that the backward runs again "
+                                   "has no known step; name the step, or let the recomputation "
+                                   "restore torch's generator of the CPU")
+            if len(known[1]) >= RECENT:
+                del known[1][next(iter(known[1]))]
+            step = known[1][draw] = self.step
+            self.step += 1
+            known[0] = self.step
+        return step
+
+
+class Dropout(CountedSteps, torch.nn.Module):
     """Dropout in training, with a residual added in the same pass if given.
 
-    ``step`` counts the calls in training (no part of the state dict); a call may
-    name its own, a number or one int64 on the GPU."""
+    ``step`` counts the calls in training (no part of the state dict; a call that
+    activation checkpointing runs again counts once, :class:`CountedSteps`); a call
+    may name its own, a number or one int64 on the GPU."""
 
     def __init__(self, p: float, seed: int | None = None):
         super().__init__()
@@ -72,7 +115,7 @@ class Dropout(torch.nn.Module):
         if not self.training or self.p == 0:
             return x if residual is None else residual + x
         if step is None:
-            step, self.step = self.step, self.step + 1
+            step = self._next_step()
         return _DropoutFn.apply(x, residual, self.p, self.seed, step)
 
     def extra_repr(self):
