@@ -164,3 +164,45 @@ def test_what_a_module_remembers_is_bounded(on_the_cpu, monkeypatch):
 def test_checkpointed_calls():
     forms_of_checkpoint("cuda")
     what_cannot_be_known_is_refused("cuda")
+
+
+# ------------------------------------------------------------------ in a graph
+def modules_of_a_capture(device):
+    return ((snk.Dropout(0.5, seed=1), ()),
+            (snk.LoraAdapters(8, 8, 1, 4, dropout=0.5, seed=1, device=device),
+             (torch.zeros(4, dtype=torch.int32, device=device),)))
+
+
+def test_a_captured_call_has_to_name_its_step(on_the_cpu, monkeypatch):
+    class OnGpu(torch.Tensor):
+        is_cuda = True
+
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    x = torch.ones(4, 8).as_subclass(OnGpu)
+    for m, ids in modules_of_a_capture("cpu"):
+        with pytest.raises(RuntimeError, match="captured.*step"):
+            m(x, *ids)
+        assert m.step == 0
+
+
+@gpu
+def test_captures_with_and_without_a_step():
+    x = torch.ones(4, 8, device="cuda")
+    step = torch.tensor([2], device="cuda")
+    s = torch.cuda.Stream()
+    for m, ids in modules_of_a_capture("cuda"):
+        with torch.cuda.stream(s):
+            m(x, *ids, step=step)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            with pytest.raises(RuntimeError, match="captured.*step"):
+                m(x, *ids)
+            y = m(x, *ids, step=step)
+            z = m(x, *ids, step=4)  # a number of the caller's own stays what it is
+        for k in (3, 2 ** 33, 3):
+            step.fill_(k)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, m(x, *ids, step=k)) and torch.equal(z, m(x, *ids, step=4))
+        assert m.step == 0

@@ -96,13 +96,14 @@ class LoraAdapters(CountedSteps, torch.nn.Module):
     ``dropout``: in training, the adapters see x with that share of its elements
     dropped (base does not).  Its mask comes from ``seed`` (drawn from torch's
     generator if None) and ``step``, which counts the calls in training (one that
-    activation checkpointing runs again once) and is no part of the state dict; a call may name its
-    own, a number or one int64 on the GPU (:mod:`.dropout`).
+    activation checkpointing runs again once) and is no part of the state dict; a
+    call may name its own, a number or one int64 on the GPU (:mod:`.dropout`).
 
-    Forward and backward can be captured into a graph.  As with any torch
-    module, no output of an eager step may still hold these parameters' autograd
-    graph while the backward is captured: torch would join the eager stream to
-    the capture and end the process."""
+    Forward and backward can be captured into a graph; with dropout the captured
+    call has to name its step, on the GPU if replays are to draw anew.  As with
+    any torch module, no output of an eager step may still hold these parameters'
+    autograd graph while the backward is captured: torch would join the eager
+    stream to the capture and end the process."""
 
     dropout, seed, step = 0.0, None, 0  # of modules that were pickled without them
 
@@ -142,7 +143,7 @@ class LoraAdapters(CountedSteps, torch.nn.Module):
         """base + each row's adapter applied to x (rows of x: tokens)."""
         if self.training and self.dropout > 0:
             if step is None:
-                step = self._next_step()
+                step = self._next_step(x)
             return _DroppedLoraFn.apply(x, self.A, self.B, base, ids, self.scale, self.ranks,
                                         self.dropout, self.seed, step)
         if torch.is_grad_enabled():

@@ -76,9 +76,13 @@ class CountedSteps:
     torch's own dropout, calls from one state of the generator drop the same
     elements, unless ``self.step`` was set between them.  A call that the backward
     runs from another state (``preserve_rng_state=False``), or again after RECENT
-    others, is refused."""
+    others, is refused, and so is a counted step in a capture: every replay would
+    drop the same elements."""
 
-    def _next_step(self):
+    def _next_step(self, x):
+        if x.is_cuda and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError(f"{type(self).__name__}: a captured call has to name its step, one "
+                               "int64 on the GPU that is counted up between the replays")
         draw = random_seed()
         in_backward = _in_backward() != -1
         known = _known.get(self)
@@ -103,7 +107,8 @@ class Dropout(CountedSteps, torch.nn.Module):
 
     ``step`` counts the calls in training (no part of the state dict; a call that
     activation checkpointing runs again counts once, :class:`CountedSteps`); a call
-    may name its own, a number or one int64 on the GPU."""
+    may name its own, a number or one int64 on the GPU.  A captured call has to:
+    with the latter, counted up between replays, each draws anew."""
 
     def __init__(self, p: float, seed: int | None = None):
         super().__init__()
@@ -115,7 +120,7 @@ class Dropout(CountedSteps, torch.nn.Module):
         if not self.training or self.p == 0:
             return x if residual is None else residual + x
         if step is None:
-            step = self._next_step()
+            step = self._next_step(x)
         return _DropoutFn.apply(x, residual, self.p, self.seed, step)
 
     def extra_repr(self):
