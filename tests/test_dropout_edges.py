@@ -206,3 +206,47 @@ def test_captures_with_and_without_a_step():
             torch.cuda.synchronize()
             assert torch.equal(y, m(x, *ids, step=k)) and torch.equal(z, m(x, *ids, step=4))
         assert m.step == 0
+
+
+# -------------------------------------------------------------------- deep copies
+def copies_drop_other_elements(device):
+    import copy
+
+    class Layer(torch.nn.Module):
+        def __init__(self):
+            super().__init__()
+            self.drop = snk.Dropout(0.5, seed=1)
+            self.same = self.drop
+            self.ad = snk.LoraAdapters(8, 8, 1, 4, dropout=0.5, seed=2, device=device)
+            self.plain = snk.LoraAdapters(8, 8, 1, 4, device=device)
+
+    first = Layer()
+    first.drop(torch.ones(2, 8, device=device))
+    state = torch.get_rng_state()
+    a, c = copy.deepcopy(first), copy.deepcopy(first)
+    d = copy.deepcopy(a)
+    assert torch.equal(torch.get_rng_state(), state)  # the program's random numbers are as before
+    layers = [first, a, c, d]
+    x = torch.ones(40, 8, device=device)
+    masks = [layer.drop(x, step=3) for layer in layers]
+    for i in range(4):
+        assert layers[i].same is layers[i].drop and layers[i].plain.seed is None
+        assert layers[i].drop.step == 1 and layers[i].drop.p == 0.5
+        assert torch.equal(layers[i].ad.A, first.ad.A) and layers[i].ad.ranks is None
+        for j in range(i):
+            assert not torch.equal(masks[i], masks[j])
+            assert layers[i].drop.seed != layers[j].drop.seed
+            assert layers[i].ad.seed != layers[j].ad.seed
+            assert layers[i].ad.A is not layers[j].ad.A
+    # the same program has the same seeds
+    again = Layer()
+    assert [copy.deepcopy(again).drop.seed for _ in range(2)] == [a.drop.seed, c.drop.seed]
+
+
+def test_deep_copies_on_the_cpu(on_the_cpu):
+    copies_drop_other_elements("cpu")
+
+
+@gpu
+def test_deep_copies():
+    copies_drop_other_elements("cuda")

@@ -12,6 +12,8 @@ The modules count their calls in training where a call names no step
 """
 from __future__ import annotations
 
+import copy
+import random
 import weakref
 
 import torch
@@ -77,7 +79,22 @@ class CountedSteps:
     elements, unless ``self.step`` was set between them.  A call that the backward
     runs from another state (``preserve_rng_state=False``), or again after RECENT
     others, is refused, and so is a counted step in a capture: every replay would
-    drop the same elements."""
+    drop the same elements.
+
+    A deep copy has a seed of its own, made from this one's and the number of copies
+    made before: layers that are copies of one draw independent masks."""
+
+    copies = 0
+
+    def __deepcopy__(self, memo):
+        make, args, state = self.__reduce_ex__(2)[:3]
+        other = memo[id(self)] = make(*args)
+        other.__setstate__(copy.deepcopy(state, memo))
+        if self.seed is not None:
+            other.seed = random.Random(f"{self.seed} {self.copies}").getrandbits(62)
+        other.copies = 0
+        self.copies += 1
+        return other
 
     def _next_step(self, x):
         if x.is_cuda and torch.cuda.is_current_stream_capturing():
