@@ -1,0 +1,40 @@
+"""Values of the losses at infinities, on the paths of small and of large batches,
+and a policy's large batches: items of 512 tokens, sequences of many items,
+masks that are counted by a launch of their own."""
+import math
+
+import pytest
+import torch
+
+import unstructured_sparse_nn_amd as snk
+from test_losses import INF, NAN, batch, close, policy
+
+gpu = pytest.mark.gpu
+PADS = [0, 9000, 300000]  # one workgroup, items of 128 tokens, items of 512
+
+
+def padded(values, pad):
+    """Sequences of one token each, the last with `pad` tokens more (zeros)."""
+    lp = torch.zeros(len(values) + pad, device="cuda")
+    lp[:len(values)] = torch.tensor(values)
+    starts = list(range(len(values))) + [len(values) + pad]
+    return lp, torch.tensor(starts, dtype=torch.int32, device="cuda")
+
+
+@gpu
+@pytest.mark.parametrize("pad", PADS)
+def test_the_kl_estimate_of_a_token_that_cannot_be_drawn(pad):
+    """exp(k) - k - 1 is infinite at both ends of k, and NaN stays."""
+    lp, st = padded([-1.0, -INF, -1.0, NAN], pad)
+    ref = lp.clone()
+    ref[1:4] = torch.tensor([-1.0, -INF, -1.0])  # k infinite, -infinite, NaN
+    adv, keep = torch.zeros(4, device="cuda"), torch.ones_like(lp, dtype=torch.bool)
+    old = torch.where(torch.isfinite(lp), lp, -1.0)
+    # and -(exp(k) - 1), a fourth of it for the share of a sequence
+    for one, value, slope in ((1, INF, -INF), (2, INF, 0.25), (3, NAN, NAN)):
+        keep[1:4] = False
+        keep[one] = True
+        loss, stats, g = snk.policy_grads(lp, old, adv, st, ref=ref, mask=keep, kl=1.0,
+                                          average="sequences")
+        for got, want in ((loss, value), (stats[0], value), (g[one], slope)):
+            assert float(got) == want or math.isnan(want) and math.isnan(float(got)), (one, want)

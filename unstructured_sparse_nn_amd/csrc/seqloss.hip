@@ -205,7 +205,7 @@ struct policy_t {
       *em1 = k + s;
     } else {
       *em1 = expm1f(k);
-      s = *em1 - k;
+      s = *em1 - fminf(k, 3.4028234663852886e38f);  // infinite at k = infinity
     }
     return s;
   }
