@@ -38,3 +38,22 @@ def test_the_kl_estimate_of_a_token_that_cannot_be_drawn(pad):
                                           average="sequences")
         for got, want in ((loss, value), (stats[0], value), (g[one], slope)):
             assert float(got) == want or math.isnan(want) and math.isnan(float(got)), (one, want)
+
+
+@gpu
+@pytest.mark.parametrize("pad", PADS)
+def test_a_kl_weight_of_zero_leaves_the_term_out(pad):
+    """The estimate may be past every float where it is only looked at."""
+    lp, st = padded([-1.0, -200.0, -INF, -2.0], pad)
+    ref, old = lp.clone(), lp.clone()
+    ref[1:3] = -1.0  # exp(199) and exp(inf)
+    old[2] = -100.0  # a ratio of 0
+    adv = torch.tensor([1.0, -0.5, 2.0, 1.0], device="cuda")
+    for average in ("tokens", "sequences"):
+        loss, stats, g = snk.policy_grads(lp, old, adv, st, ref=ref, average=average, kl=0.0)
+        want = snk.policy_grads(lp, old, adv, st, average=average)
+        assert torch.equal(loss, want[0]) and torch.isfinite(loss)
+        assert torch.equal(g, want[2]) and torch.isfinite(g).all()
+        assert float(stats[0]) == INF and torch.equal(stats[1], want[1][1])
+        some = snk.policy_grads(lp, old, adv, st, ref=ref, average=average, kl=0.1)
+        assert float(some[0]) == INF and float(some[2][1]) == -INF

@@ -223,8 +223,10 @@ struct policy_t {
     if (ref) {
       float em1;
       o.kl = above((float)((double)v.ref[u] - (double)v.lp[u]), &em1);
-      o.f = fmaf(kl, o.kl, o.f);
-      o.df = fmaf(-kl, em1, o.df);
+      if (kl != 0.f) {  // otherwise for the statistics alone, however large it is
+        o.f = fmaf(kl, o.kl, o.f);
+        o.df = fmaf(-kl, em1, o.df);
+      }
     }
     return o;
   }
