@@ -57,3 +57,17 @@ def test_a_kl_weight_of_zero_leaves_the_term_out(pad):
         assert float(stats[0]) == INF and torch.equal(stats[1], want[1][1])
         some = snk.policy_grads(lp, old, adv, st, ref=ref, average=average, kl=0.1)
         assert float(some[0]) == INF and float(some[2][1]) == -INF
+
+
+@gpu
+@pytest.mark.parametrize("pad", [0, 9000])
+def test_all_smoothing_has_no_product_of_zero_and_infinity(pad):
+    """smoothing 1 is the loss of the pair turned round: 0 at z = -infinity."""
+    for worse in (0, 1):
+        lp, st = padded([0.0, 0.0], pad)
+        lp[worse] = -INF
+        loss, _, g = snk.preference_grads(lp, st, beta=1.0, smoothing=1.0)
+        turned = 0.0 if worse == 0 else INF
+        assert float(loss) == turned
+        # its derivative by h is sigmoid(z) of z = -infinity or infinity
+        assert float(g[0]) == (0.0 if worse == 0 else 1.0) and float(g[1]) == -float(g[0])

@@ -158,7 +158,7 @@ struct pref_t {
     const double sig = z >= 0 ? up : down, not_sig = z >= 0 ? down : up;
     *dh = beta * (eps * sig - (1.0 - eps) * not_sig);
     const double a = (1.0 - eps) * (soft + fmax(-z, 0.0)), b = eps * (soft + fmax(z, 0.0));
-    return eps > 0.0 ? a + b : a;  // eps 0: no product of 0 and infinity
+    return eps == 0.0 ? a : eps == 1.0 ? b : a + b;  // no product of 0 and infinity
   }
 };
 

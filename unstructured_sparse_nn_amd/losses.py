@@ -101,8 +101,9 @@ def policy_loss(logps, old, advantages, starts=None, ref=None, mask=None, clip=(
     With r = exp(logps - old) (old None: r = 1) and A the advantage of the token
     (``by`` "tokens") or of its sequence, at each token
     ``-min(r A, clamp(r, 1 - clip[0], 1 + clip[1]) A) + kl (exp(k) - k - 1)``, k = ref - logps
-    (ref None: no KL term; with kl 0 ref is for stats alone), averaged over all tokens, or (``average`` "sequences")
-    over each sequence's and then over the sequences.  Gradients go to logps."""
+    (ref None: no KL term; with kl 0 ref is for stats alone), averaged over all tokens,
+    or (``average`` "sequences") over each sequence's and then over the sequences.
+    Gradients go to logps."""
     return _PolicyFn.apply(logps, old, advantages, starts, ref, mask,
                            (clip, kl, _one_of(average, ("tokens", "sequences"), "average"),
                             _one_of(by, ("tokens", "sequences"), "by")))
