@@ -71,3 +71,28 @@ def test_all_smoothing_has_no_product_of_zero_and_infinity(pad):
         assert float(loss) == turned
         # its derivative by h is sigmoid(z) of z = -infinity or infinity
         assert float(g[0]) == (0.0 if worse == 0 else 1.0) and float(g[1]) == -float(g[0])
+
+
+@gpu
+@pytest.mark.parametrize("pad", PADS)
+@pytest.mark.parametrize("by", ["tokens", "sequences"])
+def test_an_advantage_of_zero_adds_nothing(pad, by):
+    """However far the ratio is past every float; NaN is kept."""
+    lp, st = padded([-1.0, -1.0, -1.0, -1.0, -1.0], pad)
+    old, ref = lp.clone(), lp - 0.5
+    old[1], old[2], old[3] = -101.0, -INF, NAN  # ratios of exp(100), infinity, NaN
+    adv = torch.zeros(5, device="cuda")
+    adv[4] = 1.0
+    if by == "tokens":
+        adv = torch.cat([adv, torch.ones(pad, device="cuda")])
+    keep = torch.ones_like(lp, dtype=torch.bool)
+    keep[3] = False
+    loss, stats, g = snk.policy_grads(lp, old, adv, st, by=by, mask=keep)
+    fine = snk.policy_grads(lp, lp, adv, st, by=by, mask=keep)
+    assert torch.equal(loss, fine[0]) and torch.equal(g, fine[2]) and torch.isfinite(loss)
+    assert (g[:3] == 0).all() and float(stats[1]) == 0.0
+    # with a KL term the token has that alone
+    a, c = (snk.policy_grads(lp, o, adv, st, by=by, mask=keep, ref=ref, kl=0.1) for o in (old, lp))
+    assert torch.equal(a[0], c[0]) and torch.equal(a[2], c[2]) and float(a[2][1]) > 0
+    loss, _, g = snk.policy_grads(lp, old, adv, st, by=by)
+    assert math.isnan(float(loss)) and torch.isnan(g).nonzero().tolist() == [[3]]

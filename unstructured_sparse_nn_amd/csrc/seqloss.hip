@@ -214,11 +214,12 @@ struct policy_t {
   __device__ __forceinline__ token_t token(const in_t<U>& v, int u) const {
     const float a = v.adv[u];
     const double move = (double)v.lp[u] - (double)v.old[u];
-    const float r = expf((float)move);
+    // an advantage of 0 has nothing of a ratio past every float
+    const float r = expf((float)move), ra = a == 0.f && move == move ? 0.f : r * a;
     token_t o;
     o.cut = (a > 0.f && move > log_high) || (a < 0.f && move < log_low);
-    o.f = o.cut ? -(a > 0.f ? high : low) * a : -r * a;
-    o.df = o.cut ? 0.f : -r * a;
+    o.f = o.cut ? -(a > 0.f ? high : low) * a : -ra;
+    o.df = o.cut ? 0.f : -ra;
     o.kl = 0.f;
     if (ref) {
       float em1;
