@@ -762,9 +762,9 @@ SNACK_API snack_status snack_logp_bwd(snack_dtype dtype, const float* dlogp, con
  * 1 / S sum_j (sum f / n_j), empty ones as 0.  The clamp has no gradient where it
  * decides; whether it does goes by logps - old against log(1 - low) and
  * log(1 + high) in 64 bits.  Where A is 0 the first term is 0, however large r is.
- * old (nullable): logps itself, r = 1.  ref (nullable): no KL term; with kl 0 it is
- * for stats alone, and exp(k) may be past every float.  stats (2 floats): the means
- * over the N tokens of exp(k) - k - 1 and of whether the clamp decided.
+ * old (nullable): r = 1, NaN where logps is.  ref (nullable): no KL term; with kl 0
+ * it is for stats alone, and exp(k) may be past every float.  stats (2 floats): the
+ * means over the N tokens of exp(k) - k - 1 and of whether the clamp decided.
  *
  * Both: dloss (nullable, device float: 1) is the loss's gradient; loss, rewards
  * or stats, and dlogps (T floats, overwritten) are written if not NULL.  Sums

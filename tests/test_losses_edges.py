@@ -96,3 +96,20 @@ def test_an_advantage_of_zero_adds_nothing(pad, by):
     assert torch.equal(a[0], c[0]) and torch.equal(a[2], c[2]) and float(a[2][1]) > 0
     loss, _, g = snk.policy_grads(lp, old, adv, st, by=by)
     assert math.isnan(float(loss)) and torch.isnan(g).nonzero().tolist() == [[3]]
+
+
+@gpu
+@pytest.mark.parametrize("pad", PADS)
+def test_without_old_the_ratio_is_one(pad):
+    """Also where a token cannot be drawn; NaN stays."""
+    lp, st = padded([-INF, -1.0, INF, NAN, -2.0], pad)
+    adv = torch.tensor([3.0, -0.5, 2.0, 1.0, 1.0], device="cuda")
+    keep = ~torch.isnan(lp)
+    fine = torch.where(keep & torch.isfinite(lp), lp, -1.0)
+    for average in ("tokens", "sequences"):
+        got = snk.policy_grads(lp, None, adv, st, mask=keep, average=average)
+        want = snk.policy_grads(fine, fine, adv, st, mask=keep, average=average)
+        assert all(torch.equal(a, c) for a, c in zip(got, want))
+        assert float(got[2][0]) < 0
+        loss, _, g = snk.policy_grads(lp, None, adv, st, average=average)
+        assert math.isnan(float(loss)) and torch.isnan(g).nonzero().tolist() == [[3]]

@@ -180,10 +180,8 @@ struct policy_t {
     if (by_token) at.get(adv, v.adv);
     const float a = by_token ? 0.f : adv[seq];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (!old) v.old[u] = v.lp[u];
+    for (int u = 0; u < U; ++u)
       if (!by_token) v.adv[u] = a;
-    }
   }
 
   // exp(k) - 1 - k without its cancellation near 0, and exp(k) - 1.
@@ -213,7 +211,8 @@ struct policy_t {
   template <int U>
   __device__ __forceinline__ token_t token(const in_t<U>& v, int u) const {
     const float a = v.adv[u];
-    const double move = (double)v.lp[u] - (double)v.old[u];
+    // without old 0, but for NaN
+    const double lp = v.lp[u], move = old ? lp - (double)v.old[u] : lp == lp ? 0.0 : lp;
     // an advantage of 0 has nothing of a ratio past every float
     const float r = expf((float)move), ra = a == 0.f && move == move ? 0.f : r * a;
     token_t o;
@@ -223,7 +222,7 @@ struct policy_t {
     o.kl = 0.f;
     if (ref) {
       float em1;
-      o.kl = above((float)((double)v.ref[u] - (double)v.lp[u]), &em1);
+      o.kl = above((float)((double)v.ref[u] - lp), &em1);
       if (kl != 0.f) {  // otherwise for the statistics alone, however large it is
         o.f = fmaf(kl, o.kl, o.f);
         o.df = fmaf(-kl, em1, o.df);
