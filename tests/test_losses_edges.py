@@ -113,3 +113,49 @@ def test_without_old_the_ratio_is_one(pad):
         assert float(got[2][0]) < 0
         loss, _, g = snk.policy_grads(lp, None, adv, st, average=average)
         assert math.isnan(float(loss)) and torch.isnan(g).nonzero().tolist() == [[3]]
+
+
+# S, T: what takes items of 512 tokens, S + T / 128 of them being more than 2,048
+LARGE = [(1024, 400003),  # of every length up to several items, masked beyond 65,536 bytes
+         (2, 300001),     # a sequence over hundreds of items, some runs of 256 tokens whole
+         (1, 262144),     # items that are full to the last token
+         (700, 180001),   # few tokens beyond an item
+         (3, 1100000)]
+
+
+@gpu
+@pytest.mark.parametrize("average", ["tokens", "sequences"])
+@pytest.mark.parametrize("by", ["tokens", "sequences"])
+@pytest.mark.parametrize("S,T", LARGE)
+def test_large_policies(S, T, by, average):
+    assert S + T // 128 > 2048 and T > 65536
+    for k, (old, ref, mask) in enumerate(((True, True, True), (True, True, False),
+                                          (True, False, True))):
+        d = batch(S, T, S + T + k, outside=k > 0, empty=k == 0)
+        d["mask"][::3] = False if k == 2 else d["mask"][::3]
+        adv = d["adv_t"] if by == "tokens" else d["adv_s"]
+        want = policy(d, 0.2, 0.3, 0.05, average, by, old, ref, mask, 1.5)
+        args = (d["logps"], d["old"], adv, d["starts"])
+        more = dict(ref=d["ref"] if ref else None, mask=d["mask"] if mask else None,
+                    clip=(0.2, 0.3), kl=0.05, average=average, by=by)
+        up = torch.tensor(1.5, device="cuda")
+        loss, stats, g = snk.policy_grads(*args, **more, dloss=up)
+        close(loss, want[0], want[3], "loss")
+        close(stats, want[1], want[4], "stats")
+        close(g, want[2], want[5], "gradient")
+        only = snk.policy_grads(*args, **more, dloss=up, want=(False, True))
+        assert torch.equal(only[2], g)
+        again = snk.policy_grads(*args, **more, want=(True, False))
+        assert torch.equal(again[0], loss) and torch.equal(again[1], stats)
+
+
+@gpu
+def test_large_masks_of_nothing_and_of_everything():
+    S, T = 1024, 400003
+    d = batch(S, T, 1)
+    for average in ("tokens", "sequences"):
+        args = (d["logps"], d["old"], d["adv_s"], d["starts"])
+        none = snk.policy_grads(*args, mask=torch.zeros_like(d["mask"]), average=average)
+        assert float(none[0]) == 0 and (none[1] == 0).all() and (none[2] == 0).all()
+        every = snk.policy_grads(*args, mask=torch.ones_like(d["mask"]), average=average)
+        assert all(torch.equal(a, c) for a, c in zip(every, snk.policy_grads(*args, average=average)))
