@@ -715,11 +715,12 @@ SNACK_API snack_status snack_embed_bwd(snack_dtype dtype, const void* ids, int32
  *     norm[2i]   = m_i, norm[2i + 1] = l_i           (fp32, for the gradient)
  *     dX[i, v]   = dlogp[i] * ([v = t_i] - exp((X[i, v] - m_i) - l_i))
  * targets: as the ids above.  A negative target means none: logp 0, a row of
- * zeros in dX.  One >= V: logp NaN, a row of NaN.  Rows whose dlogp is 0, or
- * without a target, are zeros in dX and their logits are not read.  Logits of
- * -infinity have probability 0; a row of nothing else has m the lowest float, l
- * -infinity, logp -infinity and a zero gradient.  A NaN or +infinity makes its
- * row NaN.  dX may be X itself (same stride).  Outputs share no other memory.
+ * zeros in dX.  One >= V: logp NaN, a row of NaN whatever dlogp.  Other rows whose
+ * dlogp is 0, and those without a target, are zeros in dX and their logits are not
+ * read.  Logits of -infinity have probability 0; a row of nothing else has m the
+ * lowest float, l -infinity, logp -infinity and a zero gradient (NaN if dlogp is).
+ * A NaN or +infinity makes its row NaN.  dX may be X itself (same stride).  Outputs
+ * share no other memory.
  * snack_logp_workspace: bytes of ws for snack_logp_fwd (may be 0).
  * Asynchronous; same bits for the same inputs.  Errors: SNACK_E_NULL,
  * SNACK_E_DTYPE (dtype, id_bytes), SNACK_E_SHAPE (V < 1, sizes, strides,

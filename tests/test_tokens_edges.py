@@ -1,0 +1,26 @@
+"""Values of the lookup and of the logits' gradient at infinities and NaN."""
+import pytest
+import torch
+
+import unstructured_sparse_nn_amd as snk
+from test_tokens import F, H, INF, NAN, logits_of
+
+gpu = pytest.mark.gpu
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, H])
+@pytest.mark.parametrize("V", [100, 3001, 9001])  # pieces of all short rows, and rows
+def test_a_gradient_of_nan_is_kept_where_nothing_is_left(V, dt):
+    """A row of -infinity throughout has a zero gradient, but for a target past the end
+    and a NaN that comes in: those make every row NaN."""
+    x, t = logits_of(6, V, dt, 5)
+    x[:5] = -INF
+    t = t.clamp(min=0)
+    t[1], t[3], t[4] = V, -1, V + 7
+    g = torch.tensor([1.0, 1.0, NAN, NAN, 0.0, NAN], device="cuda")
+    logp, norm = snk.logp_fwd(x, t)
+    assert torch.isnan(logp[[1, 4]]).all() and float(logp[0]) == -INF and float(logp[3]) == 0
+    dx = snk.logp_bwd(g, x, t, norm)
+    nan = torch.tensor([False, True, True, False, True, True])
+    assert torch.isnan(dx[nan.cuda()]).all() and (dx[~nan.cuda()] == 0).all()

@@ -149,7 +149,8 @@ template <typename T>
 __device__ __forceinline__ frag<T> grad_piece(const frag<T>& f, cut_t c, int32_t t, float g,
                                               float2 n) {
   constexpr int E = EL<T>;
-  const bool zero = g == 0.f || n.y == -__builtin_inff();  // or a row of -infinity only
+  // or a row of -infinity only, but for NaN
+  const bool zero = g == 0.f || (n.y == -__builtin_inff() && g == g);
   float v[E];
   floats_of(f, v);
 #pragma unroll
