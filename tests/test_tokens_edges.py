@@ -24,3 +24,19 @@ def test_a_gradient_of_nan_is_kept_where_nothing_is_left(V, dt):
     dx = snk.logp_bwd(g, x, t, norm)
     nan = torch.tensor([False, True, True, False, True, True])
     assert torch.isnan(dx[nan.cuda()]).all() and (dx[~nan.cuda()] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, H])
+@pytest.mark.parametrize("V", [100, 3001, 9001])
+def test_a_gradient_of_infinity_is_infinite_at_the_target(V, dt):
+    """dlogp times 1 - p and -p, which have no zero here."""
+    x, t = logits_of(2, V, dt, 7)
+    x = (x.float().clamp(-3, 3)).to(dt)
+    t = torch.tensor([3, V - 1], device="cuda")
+    norm = snk.logp_fwd(x, t)[1]
+    for v in (INF, -INF):
+        dx = snk.logp_bwd(torch.full((2,), v, device="cuda"), x, t, norm)
+        want = torch.full_like(dx, -v)
+        want[[0, 1], t] = v
+        assert torch.equal(dx, want)

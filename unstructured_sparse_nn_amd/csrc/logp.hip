@@ -154,11 +154,13 @@ __device__ __forceinline__ frag<T> grad_piece(const frag<T>& f, cut_t c, int32_t
   float v[E];
   floats_of(f, v);
 #pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = zero ? 0.f : -g * exp_of((v[e] - n.x) - n.y);
-  if ((uint32_t)(t - c.at) < (uint32_t)E && !zero) {  // one piece of the row
+  for (int e = 0; e < E; ++e) v[e] = exp_of((v[e] - n.x) - n.y);
+  if ((uint32_t)(t - c.at) < (uint32_t)E) {  // one piece of the row
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] += c.at + e == t ? g : 0.f;
+    for (int e = 0; e < E; ++e) v[e] -= c.at + e == t ? 1.f : 0.f;
   }
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = zero ? 0.f : -g * v[e];
   return to_frag(v);
 }
 __device__ __forceinline__ float grad_of(int32_t t, const float* dlogp, int64_t i) {
