@@ -40,3 +40,18 @@ def test_a_gradient_of_infinity_is_infinite_at_the_target(V, dt):
         want = torch.full_like(dx, -v)
         want[[0, 1], t] = v
         assert torch.equal(dx, want)
+
+
+@gpu
+@pytest.mark.parametrize("dt", [F, H])
+@pytest.mark.parametrize("D", [3, 8, 33])
+def test_no_token_is_a_row_of_zeros_under_every_scale(D, dt):
+    w = torch.rand(5, D, device="cuda").to(dt) + 1
+    ids = torch.tensor([-1, 2, -9, 5], device="cuda")
+    for scale, there in ((INF, INF), (-INF, -INF), (NAN, NAN), (-1.0, None), (0.0, 0.0)):
+        y = snk.embed_fwd(ids, w, scale)
+        assert torch.equal(y[[0, 2]], torch.zeros(2, D, dtype=dt, device="cuda"))
+        assert not torch.signbit(y[[0, 2]].float()).any() and torch.isnan(y[3]).all()
+        if there is not None:
+            row = torch.full((D,), there, dtype=dt, device="cuda")
+            assert torch.equal(y[1].nan_to_num(7.0), row.nan_to_num(7.0))

@@ -40,7 +40,7 @@ __global__ __launch_bounds__(256) void k_embed(ids_t ids, int64_t Tn, const T* _
   const int32_t v = ids.get(i, V);
   frag<T> f{};
   if (v >= 0) f = load_cut(W + (int64_t)v * ldw, c, D);
-  if (scale != 1.f || v == -2) {
+  if (v >= 0 ? scale != 1.f : v == -2) {  // no token: zeros under every scale
     float x[EL<T>];
     floats_of(f, x);
 #pragma unroll
