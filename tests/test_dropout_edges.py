@@ -250,3 +250,23 @@ def test_deep_copies_on_the_cpu(on_the_cpu):
 @gpu
 def test_deep_copies():
     copies_drop_other_elements("cuda")
+
+
+# ------------------------------------------------------------------ longest rows
+@gpu
+def test_more_elements_than_one_launch_holds():
+    """2^32 work items of eight elements in fp32 are 2^35: 128 GiB, in place."""
+    n = 2 ** 35 + 3 * 2 ** 12 + 5
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 5 * n:
+        pytest.skip("160 GiB of free memory needed")
+    from test_dropout import field
+    x = torch.ones(n, device="cuda")
+    try:
+        snk.dropout_fwd(x, 0.5, 21, 22, out=x)
+        for at in (0, 2 ** 32 - 300, 2 ** 33 - 300, 2 ** 34 - 300, 2 ** 35 - 300, n - 600):
+            want = [0.0 if field(21, 22, i) < 32768 else 2.0 for i in range(at, at + 600)]
+            assert x[at:at + 600].tolist() == want, at
+    finally:
+        del x
+        torch.cuda.empty_cache()

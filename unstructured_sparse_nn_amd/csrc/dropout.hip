@@ -26,7 +26,8 @@ struct drop_arg {
   const void* res;
   void* y;
   int64_t ldx, ldr, ldy;
-  int64_t rows, cols;  // flat: one row
+  int64_t rows, cols;  // flat: one row,
+  int64_t from;        // of which a launch takes the elements from here on
   uint64_t seed, step;
   const uint64_t* more;  // added to step, or NULL
   uint32_t level;        // of 2^16
@@ -71,11 +72,12 @@ template <typename T, bool RES>
 __global__ __launch_bounds__(256) void k_dropout_flat(drop_arg a) {
   constexpr int E = EL<T>, U = 2;
   const uint64_t stream = stream_of(a);
-  const int64_t n = a.cols, first = (int64_t)blockIdx.x * (256 * U * E) + threadIdx.x * E;
+  const int64_t n = a.cols, block = a.from + (int64_t)blockIdx.x * (256 * U * E);
+  const int64_t first = block + threadIdx.x * E;
   const T *x = (const T*)a.x + first, *res = (const T*)a.res + first;
   T* y = (T*)a.y + first;
   frag<T> f[U], r[U] = {};
-  if (((int64_t)blockIdx.x + 1) * (256 * U * E) <= n) {
+  if (block + 256 * U * E <= n) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       f[u] = load_frag(x + u * 256 * E);
@@ -114,6 +116,9 @@ __global__ __launch_bounds__(256) void k_dropout_rows(drop_arg a, uint32_t per) 
   store_cut((T*)a.y + row * a.ldy, c, n, drop_piece<T>(a, stream_of(a), i0, false, f, r, RES));
 }
 
+// Elements of a launch, which holds fewer than 2^32 threads.
+constexpr int64_t LAUNCH = 1ll << 32;
+
 template <typename T>
 snack_status run(const drop_arg& a, hipStream_t s) {
   const bool flat = a.rows == 1 || (a.ldx == a.cols && a.ldy == a.cols &&
@@ -122,9 +127,11 @@ snack_status run(const drop_arg& a, hipStream_t s) {
     drop_arg f = a;
     f.cols = a.rows * a.cols;
     f.rows = 1;
-    const dim3 grid((unsigned)cdiv(f.cols, 512 * EL<T>));
     auto kernel = a.res ? k_dropout_flat<T, true> : k_dropout_flat<T, false>;
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, f);
+    for (f.from = 0; f.from < f.cols; f.from += LAUNCH) {
+      const int64_t n = std::min(f.cols - f.from, LAUNCH);
+      hipLaunchKernelGGL(kernel, dim3((unsigned)cdiv(n, 512 * EL<T>)), dim3(256), 0, s, f);
+    }
   } else {
     const int64_t per = cdiv(a.cols, EL<T>);
     if (a.cols > INT32_MAX || per * a.rows > MAX_PIECES) return SNACK_E_OVERFLOW;
@@ -162,7 +169,7 @@ extern "C" snack_status snack_dropout(snack_dtype dtype, const void* X, int64_t 
                        {step_dev, 8}};
   if (any_overlap(out, in)) return SNACK_E_SHAPE;
   const uint32_t level = (uint32_t)(p * 65536.0 + 0.5);
-  const drop_arg a{X, residual, Y, ldx, ldr, ldy, rows, cols, seed, step, step_dev, level,
+  const drop_arg a{X, residual, Y, ldx, ldr, ldy, rows, cols, 0, seed, step, step_dev, level,
                    level < 65536 ? (float)(65536.0 / (65536 - level)) : 0.f};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return dtype == SNACK_BF16 ? run<bf16>(a, s) : run<float>(a, s);
