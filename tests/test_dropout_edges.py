@@ -270,3 +270,29 @@ def test_more_elements_than_one_launch_holds():
     finally:
         del x
         torch.cuda.empty_cache()
+
+
+def test_draws_under_modes_of_torch(on_the_cpu):
+    """The number is the program's own also where tensors are made otherwise."""
+    import threading
+    want = {}
+
+    def draws():
+        torch.manual_seed(5)
+        with torch.inference_mode():
+            a = snk.dropout._draw()
+        with torch.device("meta"), torch.no_grad():
+            c = snk.dropout._draw()
+        want[threading.get_ident()] = a, c, snk.dropout._draw()
+
+    t = threading.Thread(target=draws)
+    t.start()
+    t.join()
+    draws()
+    one, two = want.values()
+    assert one == two and len(set(one)) == 3
+    # the generator moves on by each call, so a block that is run again meets the same
+    m = snk.Dropout(0.5, seed=1)
+    torch.manual_seed(5)
+    m(torch.ones(3))
+    assert list(snk.dropout._known[m][1]) == [one[0]]
