@@ -214,7 +214,7 @@ struct policy_t {
     // without old 0, but for NaN
     const double lp = v.lp[u], move = old ? lp - (double)v.old[u] : lp == lp ? 0.0 : lp;
     // an advantage of 0 has nothing of a ratio past every float
-    const float r = expf((float)move), ra = a == 0.f && move == move ? 0.f : r * a;
+    const float r = expf((float)move), ra = a == 0.f && r == r ? 0.f : r * a;
     token_t o;
     o.cut = (a > 0.f && move > log_high) || (a < 0.f && move < log_low);
     o.f = o.cut ? -(a > 0.f ? high : low) * a : -ra;
