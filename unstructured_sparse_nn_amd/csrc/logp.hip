@@ -9,8 +9,9 @@
 // keeps a running maximum and sum, whose sum is scaled where the maximum grows;
 // long rows of few are cut among workgroups, whose pairs k_logp_join adds.  The
 // backward reads and writes them once, and does not read rows whose gradient is 0.
-// 8,192 rows of 32,000 bf16: 92 us (5.7 TB/s), backward 193 us (5.4 TB/s); 4,099 of
-// 50,001, 30% without a target, backward 134 us (5.2 TB/s); 5 of 128,000: 6.1 us.
+// Figures here are of replays of a graph of calls.  8,192 rows of 32,000 bf16: 95 us
+// (5.5 TB/s; 92 us in calls one after another), backward 190 us (5.5 TB/s); 4,099 of
+// 50,001, 30% without a target, backward 134 us (5.2 TB/s); 5 of 128,000: 6.4 us.
 #include "common.h"
 #include "internal.h"
 #include "pieces.h"

@@ -28,11 +28,12 @@
 // their tokens in registers.  Sums are 64-bit in a fixed order; whether a ratio is
 // past its border is decided on logarithms in 64 bits.  A token's terms are fp32.
 // Bound by launches, trips to memory and, on one CU, instructions where the batch
-// is small: 1,500 tokens in 16 sequences 5.9 us, a policy's 12,345 in 64 7.8 us.  Large
-// batches are two to five floats a token read and one written, but come to half of
-// memory's rate at most: 4 million tokens in 4,096 sequences 24.8 us (sums 11.5, finish
-// 5.4, gradients 7.5; 2.1 TB/s), a policy's 2 million in 1,024 21.4 us (counts 4.2,
-// gradients 14.8, finish 4.0; the tokens' terms are 6 us of instructions).
+// is small: 1,500 tokens in 16 sequences 6.1 us, a policy's 12,345 in 64 7.9 us (replays
+// of a graph of calls; kernels of a trace).  Large batches are two to five floats a
+// token read and one written, but come to half of memory's rate at most: 4 million
+// tokens in 4,096 sequences 24.5 us (sums 12.0, finish 5.0, gradients 7.9; 2.1 TB/s), a
+// policy's 2 million in 1,024 22.5 us (counts 4.4, gradients 15.0, finish 4.0; the
+// tokens' terms are 6 us of instructions).
 #include <cmath>
 
 #include "common.h"

@@ -433,7 +433,6 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!out.defined()) out = at::empty(x0.sizes(), x0.options());
     matrix_t x = matrix(x0, "x", false), y = matrix(out, "out", true), r = x;
     if (res0.defined()) r = matrix(res0, "residual", false);
-    // one contiguous tensor has no rows: the others' count then
     const int64_t rows = x.rows, cols = x.cols;
     void* s = stream();
     check(unlocked([&] {

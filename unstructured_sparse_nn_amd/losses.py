@@ -5,7 +5,8 @@ Log-probabilities are float32, one a token.  ``starts`` (int32, one more than
 sequences) says where each sequence begins among them; without it every row of
 a matrix is a sequence.  ``mask`` (bool or uint8, the same shape) leaves tokens
 out of every sum and count.  The losses are scalars on the GPU; nothing here
-waits for it.
+waits for it.  The backwards of :func:`preference_loss` and :func:`policy_loss`
+compute the sums again; ``*_grads`` give loss and gradient of one call.
 """
 from __future__ import annotations
 

@@ -1,5 +1,6 @@
 """The C++ calls of csrc/torch_calls.cpp (checks, buffers and launch of the
-adapters, of clipping, dropout, embedding, log-probabilities and losses), bound to the library that binding.py has loaded.
+adapters, of clipping, dropout, embedding, log-probabilities and losses), bound
+to the library that binding.py has loaded.
 The extension module is loaded by the first call that needs it; without it
 that call fails."""
 from __future__ import annotations

@@ -68,8 +68,10 @@ def logp_fwd(logits, targets):
     """(logp, norm): the log-probability of each row's target (float32), and the
     row's largest logit with the logarithm of the sum of exp(logit - largest),
     one axis of 2 more, for :func:`logp_bwd`.  Their sum is the log of the
-    partition function.  Autograd does not record this call
-    (:func:`token_logps` does)."""
+    partition function.  Rows are read where they lie if they are evenly apart;
+    others are copied first, as those of ``logits[:, :-1]`` of several sequences are,
+    here and in the backward (all rows with -1 as the last target are not).
+    Autograd does not record this call (:func:`token_logps` does)."""
     return calls().logp_fwd(logits, targets)
 
 
@@ -97,5 +99,7 @@ class _LogpFn(torch.autograd.Function):
 
 def token_logps(logits, targets):
     """The log-probability of each target under its row of logits: float32 of the
-    targets' shape, 0 where a target is negative."""
+    targets' shape, 0 where a target is negative.  For the next token of each,
+    ``targets = ids.roll(-1, 1)`` with its last column -1 needs no copy of the logits
+    (:func:`logp_fwd`)."""
     return _LogpFn.apply(logits, targets)
